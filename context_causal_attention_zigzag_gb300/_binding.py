@@ -24,6 +24,7 @@ CONTIGUOUS = 0
 ZIGZAG = 1
 F32 = 0
 BF16 = 1
+F16 = 2  # the answering calls only
 GRAD_F32 = 0x10  # OR into the backward's dtype: dq, dk, dv written as float32
 ONEPASS = 0x20   # OR into the backward's dtype: one-pass tensor-core backward (dQ by reductions)
 PATH_SIMT = 0
@@ -68,6 +69,14 @@ SIGNATURES = {
     "cpattn_ring_bwd": (_i, [_vp] * 9 + [_i] * 9 + [_f, _vp, _sz, _vp]),
     "cpattn_ring_bwd_noalloc": (_i, [_vp] * 9 + [_i] * 9 + [_f, _vp]),
     "cpattn_ring_bwd_census": (_i, [_vp] * 9 + [_i] * 9 + [_f, _vp, _sz, _vp, _vp, _vp]),
+    "cpattn_page_tables": (_i, [_vp, _vp, _i, _i, _vp, _i, _vp, _i, _i64, _vp, _vp, _i64, _vp, _vp]),
+    "cpattn_cache_write": (_i, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i, _i64, _i64,
+                                _i64, _i, _i, _i, _vp]),
+    "cpattn_tree_attn_workspace_bytes": (_sz, [_i] * 4),
+    "cpattn_tree_attn": (_i, [_vp, _i64, _vp, _vp, _i64, _i, _i64, _i64, _i64, _vp, _i, _i64]
+                         + [_vp] * 5 + [_i] * 6 + [_f, _vp, _sz, _vp]),
+    "cpattn_prompt_attn_workspace_bytes": (_sz, [_i] * 2),
+    "cpattn_prompt_attn": (_i, [_vp, _i64] * 3 + [_vp] * 4 + [_i] * 8 + [_f, _vp, _sz, _vp]),
     "cpattn_tile_counts": (_i, [_i64, _i, _i, _i, _i64, _vp, _vp]),
     "cpattn_device_status": (_i, [_vp]),
     "cpattn_wait_probe": (_i, [_i64, _vp]),
@@ -679,6 +688,208 @@ def hier_bwd(q, k, v, out, dout, lse, cp_a2a, cp_p2p, layout=ZIGZAG, causal=True
                                _ptr(bounds), _ptr(workspace), workspace.numel(), _stream(q))
     _check("cpattn_hier_bwd", rc)
     return dq, dk, dv
+
+
+# ---------------------------------------------------------------------------
+# answering: the paged cache and packed prompts
+# ---------------------------------------------------------------------------
+
+_ANSWER_DTYPES = {torch.bfloat16: BF16, torch.float16: F16}
+
+
+def _answer_dtype(t):
+    code = _ANSWER_DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}: bfloat16 or float16")
+    return code
+
+
+def _heads_rows(t, name):
+    """The token stride of [tokens, heads, D] whose heads lie back to back."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, D]")
+    s0, s1, s2 = t.stride()
+    n, h, d = t.shape
+    if (s2 != 1 and d > 1) or (s1 != d and h > 1):
+        raise ValueError(f"a token's heads must lie back to back in {name} (strides {t.stride()})")
+    return s0 if n > 1 else h * d
+
+
+def _on(device, name, t, dtype=None, numel=None):
+    """One checked operand of an answering call, contiguous on q's device."""
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if numel is not None and t.numel() != numel:
+        raise ValueError(f"{name} must hold {numel} values")
+
+
+def _cuda_device(t):
+    if not t.is_cuda:
+        raise ValueError("tensor must be on a CUDA device")
+    return t.device
+
+
+def _table_args(table, R, device):
+    if table.dim() != 2 or table.shape[0] != R or table.dtype != torch.int32 \
+            or table.device != device:
+        raise ValueError(f"block_table must be int32 [{R}, width] on {device}")
+    if table.stride(1) != 1 and table.shape[1] > 1:
+        raise ValueError("block_table's rows must be contiguous")
+    return table.shape[1], (table.stride(0) if R > 1 else table.shape[1])
+
+
+def _cache_args(k_cache, v_cache, Hkv, D, dtype, device):
+    """(num_pages, page_size, strides) of a cache [pages, page_size, Hkv, D]."""
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape \
+            or k_cache.stride() != v_cache.stride():
+        raise ValueError("k_cache and v_cache must be [pages, page_size, Hkv, D] of one shape "
+                         "and strides")
+    if k_cache.shape[2] != Hkv or k_cache.shape[3] != D or k_cache.stride(3) != 1:
+        raise ValueError(f"the cache must hold {Hkv} heads of {D} contiguous values")
+    if k_cache.dtype != dtype or v_cache.dtype != dtype:
+        raise TypeError(f"the cache must be {dtype}")
+    if k_cache.device != device or v_cache.device != device:
+        raise ValueError(f"the cache must be on {device}")
+    return (k_cache.shape[0], k_cache.shape[1]) + k_cache.stride()[:3]
+
+
+def page_tables(ctx_lens, new_lens, block_table, free_pages, page_size, num_slots, slots=None,
+                cu=None, used=None):
+    """Block tables and slot maps from request lengths (cpattn_page_tables).
+    ctx_lens, new_lens int32 [R]; block_table int32 [R, width], updated in
+    place with pages from free_pages (int32).  Returns (slots int64
+    [num_slots], cu int32 [R + 1], used int32 [1])."""
+    dev = _cuda_device(ctx_lens)
+    R = ctx_lens.numel()
+    _on(dev, "ctx_lens", ctx_lens, torch.int32)
+    _on(dev, "new_lens", new_lens, torch.int32, R)
+    _on(dev, "free_pages", free_pages, torch.int32)
+    width, stride = _table_args(block_table, R, dev)
+    if slots is None:
+        slots = torch.empty(int(num_slots), device=dev, dtype=torch.int64)
+    if cu is None:
+        cu = torch.empty(R + 1, device=dev, dtype=torch.int32)
+    if used is None:
+        used = torch.empty(1, device=dev, dtype=torch.int32)
+    _on(dev, "slots", slots, torch.int64, int(num_slots))
+    _on(dev, "cu", cu, torch.int32, R + 1)
+    _on(dev, "used", used, torch.int32, 1)
+    with torch.cuda.device(dev):
+        rc = lib().cpattn_page_tables(_ptr(ctx_lens), _ptr(new_lens), R, int(page_size),
+                                      _ptr(free_pages), free_pages.numel(), _ptr(block_table),
+                                      width, stride, _ptr(cu), _ptr(slots), int(num_slots),
+                                      _ptr(used), _stream(ctx_lens))
+    _check("cpattn_page_tables", rc)
+    return slots, cu, used
+
+
+def cache_write(k, v, k_cache, v_cache, slots):
+    """Writes k, v [N, Hkv, D] to their slots of the paged cache
+    [pages, page_size, Hkv, D] (cpattn_cache_write); returns (k_cache, v_cache)."""
+    dev = _cuda_device(k)
+    if k.shape != v.shape or k.dtype != v.dtype or v.device != dev:
+        raise ValueError("k and v must share a shape, dtype and device")
+    code, ks, vs = _answer_dtype(k), _heads_rows(k, "k"), _heads_rows(v, "v")
+    N, Hkv, D = k.shape
+    cache = _cache_args(k_cache, v_cache, Hkv, D, k.dtype, dev)
+    _on(dev, "slots", slots, torch.int64, N)
+    with torch.cuda.device(dev):
+        rc = lib().cpattn_cache_write(_ptr(k), ks, _ptr(v), vs, _ptr(slots), N, _ptr(k_cache),
+                                      _ptr(v_cache), *cache, Hkv, D, code, _stream(k))
+    _check("cpattn_cache_write", rc)
+    return k_cache, v_cache
+
+
+def _answer_outputs(q, out, lse, dev):
+    N, H, D = q.shape
+    if out is None:
+        out = torch.empty((N, H, D), device=dev, dtype=q.dtype)
+    if lse is None:
+        lse = torch.empty((H, N), device=dev, dtype=torch.float32)
+    _on(dev, "out", out, q.dtype, N * H * D)
+    _on(dev, "lse", lse, torch.float32, H * N)
+    return out, lse
+
+
+def _workspace(need, workspace, dev):
+    if workspace is None:
+        return torch.empty(max(need, 1), device=dev, dtype=torch.uint8)
+    _on(dev, "workspace", workspace, torch.uint8)
+    return workspace
+
+
+def tree_attention_workspace(q, k_cache, cu):
+    """Scratch for tree_attention calls with q of this shape."""
+    N, H, D = q.shape
+    need = int(lib().cpattn_tree_attn_workspace_bytes(N, H, k_cache.shape[2], D))
+    return torch.empty(max(need, 1), device=q.device, dtype=torch.uint8)
+
+
+def tree_attention(q, k_cache, v_cache, block_table, ctx_lens, cu, tree=None, scale=None, out=None,
+                   lse=None, workspace=None):
+    """New tokens q [N, H, D] against the paged cache [pages, page_size, Hkv,
+    D] (cpattn_tree_attn).  cu int32 [R + 1]: the requests' rows of q;
+    ctx_lens int32 [R]: tokens in the cache before them; tree int64 [N]: the
+    new tokens of its request that each sees (bits), None for those up to
+    itself.  Returns (out [N, H, D], lse float32 [H, N])."""
+    dev = _cuda_device(q)
+    code, qs = _answer_dtype(q), _heads_rows(q, "q")
+    N, H, D = q.shape
+    Hkv, R = k_cache.shape[2], cu.numel() - 1
+    cache = _cache_args(k_cache, v_cache, Hkv, D, q.dtype, dev)
+    _on(dev, "cu", cu, torch.int32)
+    _on(dev, "ctx_lens", ctx_lens, torch.int32, R)
+    width, stride = _table_args(block_table, R, dev)
+    if tree is not None:
+        _on(dev, "tree", tree, torch.int64, N)
+    out, lse = _answer_outputs(q, out, lse, dev)
+    ws = _workspace(lib().cpattn_tree_attn_workspace_bytes(N, H, Hkv, D), workspace, dev)
+    with torch.cuda.device(dev):
+        rc = lib().cpattn_tree_attn(_ptr(q), qs, _ptr(k_cache), _ptr(v_cache), *cache,
+                                    _ptr(block_table), width, stride, _ptr(ctx_lens), _ptr(cu),
+                                    _ptr(tree), _ptr(out), _ptr(lse), R, N, H, Hkv, D, code,
+                                    _scale(scale), _ptr(ws), ws.numel(), _stream(q))
+    _check("cpattn_tree_attn", rc)
+    return out, lse
+
+
+def prompt_attention_workspace(q, cu_q):
+    """Scratch for prompt_attention calls with q and offsets of this shape."""
+    need = int(lib().cpattn_prompt_attn_workspace_bytes(cu_q.numel() - 1, q.shape[0]))
+    return torch.empty(max(need, 1), device=q.device, dtype=torch.uint8)
+
+
+def prompt_attention(q, k, v, cu_q, cu_k=None, causal=True, scale=None, out=None, lse=None,
+                     workspace=None):
+    """Packed prompts q [Nq, H, D], k, v [Nk, Hkv, D] (cpattn_prompt_attn).
+    cu_q, cu_k int32 [R + 1]: each sequence's rows (cu_k None: those of q).
+    Returns (out [Nq, H, D], lse float32 [H, Nq])."""
+    dev = _cuda_device(q)
+    cu_k = cu_q if cu_k is None else cu_k
+    if k.shape != v.shape or k.dtype != q.dtype or v.dtype != q.dtype \
+            or k.device != dev or v.device != dev:
+        raise ValueError("k and v must share a shape, and q's dtype and device")
+    code, qs, ks, vs = _answer_dtype(q), *map(_heads_rows, (q, k, v), "qkv")
+    Nq, H, D = q.shape
+    Nk, Hkv = k.shape[:2]
+    if k.shape[2] != D:
+        raise ValueError("q, k and v must share D")
+    R = cu_q.numel() - 1
+    _on(dev, "cu_q", cu_q, torch.int32)
+    _on(dev, "cu_k", cu_k, torch.int32, R + 1)
+    out, lse = _answer_outputs(q, out, lse, dev)
+    ws = _workspace(lib().cpattn_prompt_attn_workspace_bytes(R, Nq), workspace, dev)
+    with torch.cuda.device(dev):
+        rc = lib().cpattn_prompt_attn(_ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(cu_q),
+                                      _ptr(cu_k), _ptr(out), _ptr(lse), R, Nq, Nk, H, Hkv, D,
+                                      int(bool(causal)), code, _scale(scale), _ptr(ws),
+                                      ws.numel(), _stream(q))
+    _check("cpattn_prompt_attn", rc)
+    return out, lse
 
 
 # ---------------------------------------------------------------------------

@@ -19,6 +19,10 @@ __device__ int g_device_error;
 constexpr int kMaxDevices = 64;
 int* g_err_ptr[kMaxDevices] = {nullptr};
 
+}  // namespace
+
+namespace cpattn {
+
 int* device_error_word() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
@@ -29,6 +33,10 @@ int* device_error_word() {
   }
   return g_err_ptr[dev];
 }
+
+}  // namespace cpattn
+
+namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
@@ -791,7 +799,7 @@ int cpattn_device_status(cpattn_stream_t stream) {
     int zero = 0;
     if (cudaMemcpy(err, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess)
       return CPATTN_ERR_CUDA;
-    if (host == kErrBadDocs) return CPATTN_ERR_INVALID_ARG;
+    if (host == kErrBadDocs || host == kErrBadTables) return CPATTN_ERR_INVALID_ARG;
     if (host == kErrLaunch) return CPATTN_ERR_UNSUPPORTED;
     return CPATTN_ERR_DEVICE_TIMEOUT;
   }

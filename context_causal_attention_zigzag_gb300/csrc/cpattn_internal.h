@@ -262,6 +262,10 @@ cudaError_t launch_doc_bounds(const int* cu, int ndocs, int S, int2* docs, int* 
 constexpr int kErrTimeout = 1;
 constexpr int kErrBadDocs = 2;
 constexpr int kErrLaunch = 3;  // a kernel found its launch unusable (shared-memory alignment)
+constexpr int kErrBadTables = 4;  // an answering call found broken lengths, tables or slots
+
+// The current device's error word (nullptr if it cannot be found).
+int* device_error_word();
 
 // Flags callers OR into the dtype argument (include/cpattn.h).
 constexpr int kDtypeFlags = CPATTN_GRAD_F32 | CPATTN_BWD_ONEPASS;
@@ -296,6 +300,100 @@ cudaError_t launch_grad_reduce(const float* dk_part, const float* dv_part, void*
 cudaError_t launch_grad_convert(const float* dq_acc, const float* dk_acc, const float* dv_acc,
                                 void* dq, void* dk, void* dv, int64_t n_q, int64_t n_kv,
                                 int out_dtype, cudaStream_t stream);
+
+// ---------------------------------------------------------------------------
+// Answering calls (include/cpattn.h): packed prompts and the paged cache.
+// ---------------------------------------------------------------------------
+
+// A paged cache; strides in elements, the same for keys and values.
+struct CacheShape {
+  int64_t num_pages;
+  int page_size;
+  int64_t page_stride, token_stride, head_stride;
+};
+
+struct TablesArgs {
+  const int* ctx;
+  const int* fresh;  // new tokens of each request
+  int R, page_size;
+  const int* free_pages;
+  int num_free;
+  int* table;
+  int width;
+  int64_t table_stride;
+  int* cu;
+  int64_t* slots;
+  int64_t num_slots;
+  int* used;
+  int* err;
+};
+
+struct CacheWriteArgs {
+  const void* k;
+  const void* v;
+  int64_t k_stride, v_stride;
+  const int64_t* slots;
+  int64_t N;
+  void* k_cache;
+  void* v_cache;
+  CacheShape cache;
+  int Hkv, D;
+  int* err;
+};
+
+struct TreeArgs {
+  const void* q;
+  int64_t q_stride;
+  const void* k_cache;
+  const void* v_cache;
+  CacheShape cache;
+  const int* table;
+  int width;
+  int64_t table_stride;
+  const int* ctx;
+  const int* cu;
+  const unsigned long long* tree;  // nullptr: each new token sees those up to itself
+  void* out;
+  float* lse;
+  int R, N, H, Hkv, D;
+  float scale, scale_log2;
+  void* workspace;
+  int* err;
+};
+
+struct PromptArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_stride, k_stride, v_stride;
+  const int* cu_q;
+  const int* cu_k;
+  void* out;
+  float* lse;
+  int R, Nq, Nk, H, Hkv, D, causal;
+  float scale, scale_log2;
+  void* workspace;
+  int* err;
+};
+
+// Rows [first, first + n) of one sequence from its offsets, held to [0, total]
+// whatever they say; false when they break the rules (0 first, never falling,
+// never past the end).
+__device__ __forceinline__ bool packed_rows(const int* cu, int r, int total, int& first, int& n) {
+  const int a = cu[r], b = cu[r + 1];
+  const bool ok = a >= 0 && b >= a && b <= total && (r > 0 || a == 0);
+  first = a < 0 ? 0 : (a > total ? total : a);
+  const int end = b < first ? first : (b > total ? total : b);
+  n = end - first;
+  return ok;
+}
+
+cudaError_t launch_page_tables(const TablesArgs& a, cudaStream_t stream);
+cudaError_t launch_cache_write(const CacheWriteArgs& a, cudaStream_t stream);
+size_t tree_workspace_bytes(int N, int H, int Hkv, int D);
+cudaError_t launch_tree_attn(const TreeArgs& a, int dtype, cudaStream_t stream);
+size_t prompt_workspace_bytes(int R, int Nq);
+cudaError_t launch_prompt_attn(const PromptArgs& a, int dtype, cudaStream_t stream);
 
 // One CTA whose bounded mbarrier wait gives up after limit_ns (raising *err).
 cudaError_t launch_wait_probe(int* err, uint64_t limit_ns, cudaStream_t stream);

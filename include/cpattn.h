@@ -72,6 +72,10 @@ enum cpattn_layout { CPATTN_LAYOUT_CONTIGUOUS = 0, CPATTN_LAYOUT_ZIGZAG = 1 };
 enum cpattn_dtype {
   CPATTN_F32 = 0,
   CPATTN_BF16 = 1,
+  /* float16: taken by the answering calls only (cpattn_cache_write,
+   * cpattn_tree_attn, cpattn_prompt_attn); every other call answers
+   * CPATTN_ERR_INVALID_ARG. */
+  CPATTN_F16 = 2,
   /* Flag for the backward calls (OR it into dtype): dq, dk, dv are written
    * as float32 whatever the input dtype.  A bf16 gradient element of
    * magnitude >= 8 carries a rounding error of up to 2^-5; float32 output
@@ -534,6 +538,123 @@ CPATTN_API int cpattn_attention_host_docs(const void* q, const void* k, const vo
                                           size_t workspace_bytes, cpattn_stream_t stream);
 
 /*
+ * Answering from a long context: prompts of any lengths as they come, a paged
+ * key/value cache, and the attention that reads it.  The pages describe
+ * training; these calls are what the same attention needs once the model
+ * answers.  They take no layout and no cp_size: sequences lie back to back in
+ * natural order.  dtype is CPATTN_BF16 or CPATTN_F16 (float32 is answered
+ * with CPATTN_ERR_UNSUPPORTED: the ring calls take it), D is 64 or 128, H is a
+ * multiple of Hkv and H / Hkv at most 128; products and softmax statistics
+ * are float32.  Strides are in elements; a token's heads lie back to back
+ * ([heads, D]), so that a slice of a fused projection can be passed as it is.
+ *
+ * Lengths and tables are device memory, never read by the host.  Entries that
+ * break a rule below (offsets that do not start at 0, fall or pass the end, a
+ * negative length, a table too narrow for its request, a page outside the
+ * cache, a pool that runs out) raise the device error word, reported as
+ * CPATTN_ERR_INVALID_ARG by the next cpattn_device_status; the calls stay
+ * within their buffers, and the results of the call are then undefined.
+ *
+ * The cache: k_cache and v_cache hold num_pages pages of page_size tokens,
+ * element (page, i, g, d) at page * page_stride + i * token_stride +
+ * g * head_stride + d, the same strides for both: [pages, tokens, heads, D],
+ * [pages, heads, tokens, D] and keys and values interleaved by page are all
+ * taken.  page_size is 16, 32, 64 or a multiple of 128 up to 1024.  A
+ * request's position p lies in page block_table[r * table_stride + p /
+ * page_size] at p % page_size; the slot of that position is page * page_size
+ * + p % page_size.  16-byte aligned pointers, strides multiples of 8, page_size *
+ * num_pages below 2^31.
+ */
+
+/*
+ * Block tables and slot maps from request lengths: request r holds ctx_lens[r]
+ * tokens in the cache and adds new_lens[r] >= 0.  Each request takes the pages
+ * it lacks (ceil((ctx + new) / page_size) - ceil(ctx / page_size)) from
+ * free_pages, in request order from its start, and they are entered behind
+ * the pages it has; entries before and behind those stay as they are.
+ *   block_table [R, table_width] int32, rows table_stride apart (in, out);
+ *   cu_new [R + 1] int32: offsets of the requests' new tokens;
+ *   slots [num_slots] int64: the slot of each new token, then -1 up to
+ *   num_slots (a padded batch); used [1] int32: pages taken.
+ * A call with the same inputs gives the same tables, so it can be repeated.
+ * Tokens whose page is missing (a bad length, a narrow table, an empty pool)
+ * get slot -1, so that cpattn_cache_write skips them; tokens behind num_slots
+ * are left out (also an error).  Sums of new tokens and of pages stay below
+ * 2^31.
+ */
+CPATTN_API int cpattn_page_tables(const int32_t* ctx_lens, const int32_t* new_lens, int R,
+                                  int page_size, const int32_t* free_pages, int num_free,
+                                  int32_t* block_table, int table_width, int64_t table_stride,
+                                  int32_t* cu_new, int64_t* slots, int64_t num_slots,
+                                  int32_t* used, cpattn_stream_t stream);
+
+/*
+ * Writes N tokens' keys and values into the cache: token i goes to slot
+ * slots[i]; a negative slot is skipped, one outside the cache is skipped and
+ * raises the error word.  Everything else in the cache stays as it is.  Slots
+ * of one call are distinct (of tokens that share one, any of them may be
+ * found there).  k, v: [N, Hkv, D], tokens k_stride / v_stride apart.
+ */
+CPATTN_API int cpattn_cache_write(const void* k, int64_t k_stride, const void* v,
+                                  int64_t v_stride, const int64_t* slots, int64_t N,
+                                  void* k_cache, void* v_cache, int64_t num_pages, int page_size,
+                                  int64_t page_stride, int64_t token_stride, int64_t head_stride,
+                                  int Hkv, int D, int dtype, cpattn_stream_t stream);
+
+/*
+ * Attention of new tokens over the cache.  Request r's new tokens are rows
+ * cu_new[r] .. cu_new[r + 1] - 1 of q; their own keys and values are in the
+ * cache already, at positions ctx_lens[r] + 0, 1, ...  Token i of a request
+ * sees every position below ctx_lens[r] and, of the new ones,
+ *   tree == NULL: those up to itself (one token of an ordinary step, or the
+ *   next part of a prompt; any number of tokens);
+ *   tree [N] uint64: those whose bit is set in its word, bit j for the
+ *   request's j-th new token (a drafted tree: itself and its ancestors; at
+ *   most 64 new tokens a request, more are an error).
+ *   q [N, H, D], tokens q_stride apart; out [N, H, D]; lse [H, N] float32.
+ * A token that sees nothing gets out = 0 and lse = -inf.  Rows of out and lse
+ * behind cu_new[R] are left as they were.  What lies in the cache behind a
+ * request's last position, or in another request's pages, does not reach it,
+ * NaN included; a key or value that is not finite within the request may
+ * reach any of its rows.
+ * workspace: device, at least cpattn_tree_attn_workspace_bytes, 256-byte
+ * aligned, scratch (calls whose execution overlaps need one each).
+ */
+CPATTN_API size_t cpattn_tree_attn_workspace_bytes(int N, int H, int Hkv, int D);
+CPATTN_API int cpattn_tree_attn(const void* q, int64_t q_stride, const void* k_cache,
+                                const void* v_cache, int64_t num_pages, int page_size,
+                                int64_t page_stride, int64_t token_stride, int64_t head_stride,
+                                const int32_t* block_table, int table_width,
+                                int64_t table_stride, const int32_t* ctx_lens,
+                                const int32_t* cu_new, const uint64_t* tree, void* out, float* lse,
+                                int R, int N, int H, int Hkv, int D, int dtype,
+                                float softmax_scale, void* workspace, size_t workspace_bytes,
+                                cpattn_stream_t stream);
+
+/*
+ * Attention over whole prompts packed back to back: sequence r has the query
+ * rows cu_q[r] .. cu_q[r + 1] - 1 and the key rows cu_k[r] .. cu_k[r + 1] - 1.
+ * With nq queries and nk keys, query i sees (causal = 1) the keys
+ * j <= i + nk - nq -- the last query sees every key, so that keys of a part
+ * answered earlier may stand in front -- or (causal = 0) all nk.
+ *   q [Nq, H, D], k, v [Nk, Hkv, D], tokens q_stride, k_stride, v_stride apart;
+ *   out [Nq, H, D]; lse [H, Nq] float32.
+ * A query that sees nothing gets out = 0 and lse = -inf.  Rows of out and lse
+ * behind cu_q[R] are left as they were; what lies in rows of other sequences
+ * does not reach a sequence, NaN included (a value that is not finite may
+ * reach any row of its own sequence).
+ * workspace: device, at least cpattn_prompt_attn_workspace_bytes, 256-byte
+ * aligned, scratch (calls whose execution overlaps need one each).
+ */
+CPATTN_API size_t cpattn_prompt_attn_workspace_bytes(int R, int Nq);
+CPATTN_API int cpattn_prompt_attn(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                  const void* v, int64_t v_stride, const int32_t* cu_q,
+                                  const int32_t* cu_k, void* out, float* lse, int R, int Nq,
+                                  int Nk, int H, int Hkv, int D, int causal, int dtype,
+                                  float softmax_scale, void* workspace, size_t workspace_bytes,
+                                  cpattn_stream_t stream);
+
+/*
  * Closed-form work census of the ring (host only): for every rank r and
  * step t, the number of tile x tile blocks with at least one visible
  * (query, key) pair, tiles_rt[r*cp_size + t], and the number of visible
@@ -549,7 +670,8 @@ CPATTN_API int cpattn_tile_counts(int64_t S, int cp_size, int layout, int causal
  * Waits for `stream`, then reads and clears this device's error word.
  * Returns CPATTN_ERR_DEVICE_TIMEOUT if a kernel's bounded wait gave up since
  * the last call, CPATTN_ERR_INVALID_ARG if cpattn_doc_bounds found broken
- * document offsets since the last call, CPATTN_ERR_CUDA if the stream
+ * document offsets or an answering call broken lengths, tables or slots since
+ * the last call, CPATTN_ERR_CUDA if the stream
  * reports a CUDA error, else CPATTN_OK.  Synchronous.
  */
 CPATTN_API int cpattn_device_status(cpattn_stream_t stream);

@@ -1,0 +1,110 @@
+"""Answering calls: what they refuse, before any launch (no GPU needed)."""
+import ctypes
+
+import pytest
+import torch
+
+import context_causal_attention_zigzag_gb300 as cp_attn
+from context_causal_attention_zigzag_gb300 import _binding
+
+E, U, W = _binding.ERR_INVALID_ARG, _binding.ERR_UNSUPPORTED, _binding.ERR_WORKSPACE
+null, fake, odd = ctypes.c_void_p(0), ctypes.c_void_p(0x1000), ctypes.c_void_p(0x1004)
+
+
+def call(name, args, **changes):
+    args = dict(args, **changes)
+    return getattr(cp_attn.lib(), name)(*args.values())
+
+
+TABLES = dict(ctx=fake, new=fake, R=2, P=16, free=fake, num_free=4, table=fake, width=4, stride=4,
+              cu=fake, slots=fake, num_slots=8, used=fake, stream=null)
+CACHE = dict(pages=8, P=16, ps=16 * 2 * 64, ts=2 * 64, hs=64)
+WRITE = dict(k=fake, ks=128, v=fake, vs=128, slots=fake, N=4, kc=fake, vc=fake, **CACHE, Hkv=2, D=64,
+             dtype=1, stream=null)
+TREE = dict(q=fake, qs=256, kc=fake, vc=fake, **CACHE, table=fake, width=4, stride=4, ctx=fake,
+            cu=fake, tree=null, out=fake, lse=fake, R=2, N=4, H=4, Hkv=2, D=64, dtype=1, scale=0.0,
+            ws=fake, wb=1 << 30, stream=null)
+PROMPT = dict(q=fake, qs=256, k=fake, ks=128, v=fake, vs=128, cu_q=fake, cu_k=fake, out=fake,
+              lse=fake, R=2, Nq=4, Nk=4, H=4, Hkv=2, D=64, causal=1, dtype=1, scale=0.0, ws=fake,
+              wb=1 << 30, stream=null)
+
+
+@pytest.mark.parametrize("changes", [
+    dict(R=-1), dict(P=0), dict(P=24), dict(P=192), dict(P=2048), dict(num_free=-1), dict(width=-1),
+    dict(stride=3), dict(num_slots=-1), dict(num_slots=1 << 31), dict(ctx=null), dict(new=null),
+    dict(free=null), dict(table=null), dict(cu=null), dict(slots=null), dict(used=null),
+    dict(slots=odd), dict(ctx=ctypes.c_void_p(0x1002))])
+def test_page_tables_refuses(changes):
+    assert call("cpattn_page_tables", TABLES, **changes) == E
+
+
+BAD_CACHE = [dict(pages=0), dict(pages=1 << 28), dict(P=17), dict(ps=32), dict(ts=100), dict(hs=66),
+             dict(hs=32), dict(ps=1 << 40), dict(kc=null), dict(vc=odd)]
+BAD_HEADS = [dict(D=32), dict(D=96), dict(Hkv=0), dict(dtype=9), dict(dtype=0x11)]
+
+
+@pytest.mark.parametrize("changes", BAD_CACHE + BAD_HEADS + [
+    dict(N=-1), dict(N=1 << 31), dict(k=null), dict(v=odd), dict(slots=null), dict(slots=odd),
+    dict(ks=127), dict(vs=120), dict(ks=1 << 40)])
+def test_cache_write_refuses(changes):
+    assert call("cpattn_cache_write", WRITE, **changes) == E
+
+
+@pytest.mark.parametrize("changes", BAD_CACHE + BAD_HEADS + [
+    dict(H=3), dict(H=0), dict(H=258, qs=258 * 64), dict(R=-1), dict(N=-1), dict(width=-1), dict(stride=2),
+    dict(width=1 << 28, stride=1 << 28), dict(q=null), dict(qs=250), dict(out=odd), dict(lse=null),
+    dict(table=null), dict(ctx=null), dict(cu=null), dict(tree=odd),
+    dict(scale=float("nan")), dict(scale=float("inf"))])
+def test_tree_attention_refuses(changes):
+    assert call("cpattn_tree_attn", TREE, **changes) == E
+
+
+@pytest.mark.parametrize("changes", BAD_HEADS + [
+    dict(H=3), dict(R=-1), dict(Nq=-1), dict(Nk=-1), dict(causal=2), dict(q=null), dict(k=null),
+    dict(v=odd), dict(qs=250), dict(ks=100), dict(vs=129), dict(cu_q=null), dict(cu_k=null),
+    dict(out=null), dict(lse=null), dict(scale=float("nan"))])
+def test_prompt_attention_refuses(changes):
+    assert call("cpattn_prompt_attn", PROMPT, **changes) == E
+
+
+def test_float32_is_unsupported():
+    assert call("cpattn_cache_write", WRITE, dtype=0) == U
+    assert call("cpattn_tree_attn", TREE, dtype=0) == U
+    assert call("cpattn_prompt_attn", PROMPT, dtype=0) == U
+
+
+def test_the_ring_calls_refuse_float16():
+    fwd = cp_attn.lib().cpattn_ring_fwd
+    assert fwd(*[fake] * 5, 1, 4, 2, 64, 64, 2, 1, 1, cp_attn.F16, 0.0, null) == E
+
+
+def test_workspace_is_checked():
+    lib = cp_attn.lib()
+    need = lib.cpattn_tree_attn_workspace_bytes(4, 4, 2, 64)
+    assert need > 0 and lib.cpattn_tree_attn_workspace_bytes(-1, 4, 2, 64) == 0
+    for bad in (dict(ws=null), dict(ws=ctypes.c_void_p(0x1010)), dict(wb=need - 1)):
+        assert call("cpattn_tree_attn", TREE, **bad) == W
+    need = lib.cpattn_prompt_attn_workspace_bytes(2, 4)
+    assert need > 0 and lib.cpattn_prompt_attn_workspace_bytes(-1, 4) == 0
+    for bad in (dict(ws=null), dict(ws=ctypes.c_void_p(0x1010)), dict(wb=need - 1)):
+        assert call("cpattn_prompt_attn", PROMPT, **bad) == W
+
+
+def test_empty_calls_do_nothing():
+    assert call("cpattn_cache_write", WRITE, N=0, k=null, v=null, slots=null) == 0
+    assert call("cpattn_tree_attn", TREE, N=0, q=null, out=null, lse=null) == 0
+    assert call("cpattn_tree_attn", TREE, R=0) == 0
+    assert call("cpattn_prompt_attn", PROMPT, Nq=0, q=null, out=null, lse=null) == 0
+
+
+def test_binding_refuses_host_tensors():
+    x = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    i = torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        cp_attn.prompt_attention(x, x, x, i)
+    with pytest.raises(ValueError):
+        cp_attn.cache_write(x, x, x[None], x[None], i)
+    with pytest.raises(ValueError):
+        cp_attn.page_tables(i, i, i[None], i, 16, 8)
+    with pytest.raises(ValueError):
+        cp_attn.tree_attention(x, x[None], x[None], i[None], i, i)
