@@ -1,5 +1,6 @@
 // C-ABI layer of the answering calls: argument checks and dispatch.
 // Declarations and the meaning of every argument are in include/cpattn.h.
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <limits.h>
 #include <math.h>
@@ -45,9 +46,42 @@ bool check_cache(const void* k, const void* v, const CacheShape& c, int D) {
 
 bool scale_ok(float s) { return s <= 0.f || isfinite(s); }
 
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  if (fn == nullptr) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(p);
+  }
+  return fn;
+}
+
 int status(cudaError_t e) { return e == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA; }
 
 }  // namespace
+
+namespace cpattn {
+
+bool encode_tiled(CUtensorMap* m, bool bf16, int rank, const void* ptr, const cuuint64_t* dims,
+                  const cuuint64_t* strides, const cuuint32_t* box) {
+  EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr) return false;
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
+             const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace cpattn
 
 extern "C" {
 
@@ -165,6 +199,8 @@ int cpattn_prompt_attn(const void* q, int64_t q_stride, const void* k, int64_t k
   if (R < 0 || R > (1 << 24) || Nq < 0 || Nk < 0 || Nq > (1 << 30) || Nk > (1 << 30) ||
       (causal != 0 && causal != 1) || !scale_ok(softmax_scale))
     return CPATTN_ERR_INVALID_ARG;
+  // Work items are numbered in an int.
+  if (((int64_t)Nq / 128 + R) * H > INT32_MAX) return CPATTN_ERR_INVALID_ARG;
   if (R == 0 || Nq == 0) return CPATTN_OK;
   if (!check_rows(q, q_stride, H, D) || !check_rows(out, (int64_t)H * D, H, D) || !lse ||
       !aligned(lse, 4) || !cu_q || !cu_k || !aligned(cu_q, 4) || !aligned(cu_k, 4))

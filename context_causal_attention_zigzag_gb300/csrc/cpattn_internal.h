@@ -2,6 +2,7 @@
 // translation units.  Not installed; not part of the ABI.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -387,6 +388,11 @@ __device__ __forceinline__ bool packed_rows(const int* cu, int r, int total, int
   n = end - first;
   return ok;
 }
+
+// A tiled tensor map of 16-bit values with 128-byte swizzle, out of bounds read
+// as zeros.
+bool encode_tiled(CUtensorMap* m, bool bf16, int rank, const void* ptr, const cuuint64_t* dims,
+                  const cuuint64_t* strides, const cuuint32_t* box);
 
 cudaError_t launch_page_tables(const TablesArgs& a, cudaStream_t stream);
 cudaError_t launch_cache_write(const CacheWriteArgs& a, cudaStream_t stream);

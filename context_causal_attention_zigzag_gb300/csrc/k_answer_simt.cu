@@ -96,34 +96,11 @@ __global__ void __launch_bounds__(128) tree_simt_kernel(const TreeArgs a) {
   row.store(static_cast<T*>(a.out) + ((int64_t)i * a.H + h) * D, a.lse + (int64_t)h * a.N + i);
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(128) prompt_simt_kernel(const PromptArgs a) {
-  if (blockIdx.x == 0) {
-    check_rows(a.cu_q, a.R, a.Nq, a.err);
-    check_rows(a.cu_k, a.R, a.Nk, a.err);
-  }
-  const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int i = (int)(w / a.H), h = (int)(w % a.H);
-  if (i >= a.Nq) return;
-  int r, first, n, kfirst, nk;
-  if (!find_row(a.cu_q, a.R, a.Nq, i, r, first, n, a.err)) return;
-  if (!packed_rows(a.cu_k, r, a.Nk, kfirst, nk)) atomicExch(a.err, kErrBadTables);
-  const int hi = a.causal ? min(nk - 1, i - first + nk - n) : nk - 1;
-  Row<T, D> row;
-  row.load(static_cast<const T*>(a.q) + i * a.q_stride + h * D, a.scale);
-  const int hk = h / (a.H / a.Hkv);
-  for (int j = 0; j <= hi; ++j)
-    row.key(static_cast<const T*>(a.k) + (int64_t)(kfirst + j) * a.k_stride + hk * D,
-            static_cast<const T*>(a.v) + (int64_t)(kfirst + j) * a.v_stride + hk * D);
-  row.store(static_cast<T*>(a.out) + ((int64_t)i * a.H + h) * D, a.lse + (int64_t)h * a.Nq + i);
-}
-
 int grid_of(int rows, int H) { return (int)(((int64_t)rows * H + 3) / 4); }
 
 }  // namespace
 
 size_t tree_workspace_bytes(int N, int H, int Hkv, int D) { return 256; }
-size_t prompt_workspace_bytes(int R, int Nq) { return 256; }
 
 #define CPATTN_BY_TYPE(kernel, rows)                                                        \
   if (dtype == CPATTN_BF16 && a.D == 128)                                                   \
@@ -138,9 +115,6 @@ size_t prompt_workspace_bytes(int R, int Nq) { return 256; }
 
 cudaError_t launch_tree_attn(const TreeArgs& a, int dtype, cudaStream_t stream) {
   CPATTN_BY_TYPE(tree_simt_kernel, a.N);
-}
-cudaError_t launch_prompt_attn(const PromptArgs& a, int dtype, cudaStream_t stream) {
-  CPATTN_BY_TYPE(prompt_simt_kernel, a.Nq);
 }
 
 }  // namespace cpattn

@@ -1,0 +1,707 @@
+// Attention over packed prompts on the tensor cores (sm_103a): tcgen05.mma
+// with TMEM accumulators, TMA-staged tiles, warp-specialised, persistent.
+//
+//   o_i = sum_j p_ij v_j,  p_ij = exp(scale q_i k_j - lse_i),  j <= i + nk - nq
+//
+// for each sequence by itself, by one pass over its keys with the running
+// maximum and sum of the softmax.  Compute bound from a few hundred tokens on:
+// 4 D flops per visible pair and head against one K and V tile of 64 KB that
+// 256 query rows share.
+//
+// A work item is two 128-row query tiles that walk the same key tiles.  With
+// an even number of query heads per kv head they are the same 128 rows of two
+// neighbouring heads: both see the same keys, so no tile is loaded or
+// multiplied for one of them alone, and an item is as small as 128 rows (a
+// short prompt fills it).  With an odd number they are 256 rows of one head.
+// Items are sorted by their number of key tiles (prompt_plan_kernel; a single
+// sequence needs no sorting) and dealt in cost bands in snake order, as in the
+// ring forward (banded_item).
+//
+// Sequences start at any row: TMA takes any first row, and a tile's rows
+// behind the sequence's end belong to others.  Their scores are replaced by
+// -inf, and their V rows, which enter the product with weight 0, are zeroed in
+// shared memory by the softmax threads before the product, since 0 * NaN is
+// NaN.  Only a sequence's last tile pays for that.
+//
+// Roles and barriers of a CTA (384 threads) as in the ring forward: warp 0
+// loads (Q pair once per item, K(j), V(j) in consecutive slots of one ring),
+// warp 1 owns TMEM and issues the products S_i = Q_i K^T (SS) and O_i += P_i V
+// (TS, P in TMEM over S), warps 4-7 and 8-11 are the softmax of tile 0 and 1,
+// one thread per row.  MMA order per key tile: PV0(j), S0(j+1), PV1(j),
+// S1(j+1).  The weights are rounded to the input type for the second product
+// (their sum is taken before rounding, in float32): the tensor cores take 16-bit
+// operands, and the rounding is as large as that of the output itself.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "cpattn_internal.h"
+#include "tc_ptx.cuh"
+
+namespace cpattn {
+namespace {
+
+using namespace tc;
+
+constexpr int kT = 128;  // tile edge (rows, keys)
+constexpr int kBoxBytes = kT * 64 * 2;
+constexpr int kThreads = 384;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units
+
+// One block of query rows of a sequence, as the plan lists it.
+struct __align__(16) Block {
+  int qrow;   // its first row of q
+  int nrows;  // rows of the sequence from there on
+  int krow;   // the sequence's first row of k and v
+  int nk;     // its keys
+  int diag;   // keys that the block's first row sees under the causal rule (may be <= 0)
+  int pad[3];
+};
+
+// Number of key tiles that rows [at, at + n) of a block see (n <= 0: none).
+__device__ __forceinline__ int key_tiles(const Block& b, int causal, int at, int n) {
+  const int last = min(at + n, b.nrows) - 1;  // last row
+  if (last < at) return 0;
+  const int end = causal ? min(b.nk, b.diag + last) : b.nk;
+  return end > 0 ? (end + kT - 1) / kT : 0;
+}
+
+// ---------------------------------------------------------------------------
+// Plan: the blocks of all sequences in order of falling cost.  One CTA; a
+// counting sort over kBins costs.  The order inside a bin varies from run to
+// run; results do not (each block's arithmetic is its own).
+// ---------------------------------------------------------------------------
+constexpr int kBins = 1024;
+
+struct Plan {
+  int nblocks;
+  int pad[63];
+};
+
+__device__ __forceinline__ Block make_block(int q0, int nq, int k0, int nk, int at) {
+  Block b;
+  b.qrow = q0 + at;
+  b.nrows = nq - at;
+  b.krow = k0;
+  b.nk = nk;
+  b.diag = at + nk - nq + 1;
+  b.pad[0] = b.pad[1] = b.pad[2] = 0;
+  return b;
+}
+
+__global__ void __launch_bounds__(1024) prompt_plan_kernel(const PromptArgs a, int rows, int cap,
+                                                           Plan* plan, Block* list) {
+  __shared__ int s_bin[kBins], s_warp[32], s_most;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  launch_dependents();
+  s_bin[tid] = 0;
+  if (tid == 0) s_most = 1;
+  __syncthreads();
+  int q0, nq, k0, nk, most = 1;
+  bool bad = false;
+  for (int r = tid; r < a.R; r += 1024) {
+    bad |= !packed_rows(a.cu_q, r, a.Nq, q0, nq);
+    bad |= !packed_rows(a.cu_k, r, a.Nk, k0, nk);
+    most = max(most, (nk + kT - 1) / kT);
+  }
+  atomicMax(&s_most, most);
+  if (bad) atomicExch(a.err, kErrBadTables);
+  __syncthreads();
+  most = s_most;
+  // Largest cost first: bin 0 holds the blocks with the most key tiles.
+  auto bin_of = [&](const Block& b) {
+    const int c = key_tiles(b, a.causal, 0, rows);
+    return (int)((long long)(most - c) * (kBins - 1) / most);
+  };
+  for (int pass = 0; pass < 2; ++pass) {
+    for (int r = warp; r < a.R; r += 32) {
+      packed_rows(a.cu_q, r, a.Nq, q0, nq);
+      packed_rows(a.cu_k, r, a.Nk, k0, nk);
+      for (int at = lane * rows; at < nq; at += 32 * rows) {
+        const Block b = make_block(q0, nq, k0, nk, at);
+        const int x = atomicAdd(&s_bin[bin_of(b)], 1);
+        if (pass == 1 && x < cap) list[x] = b;  // broken offsets may name more than fit
+      }
+    }
+    __syncthreads();
+    if (pass == 1) break;
+    // Exclusive sums of the bins, in place: where each bin's blocks start.
+    const int own = s_bin[tid];
+    int x = own;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += u;
+    }
+    if (lane == 31) s_warp[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+      int z = s_warp[lane];
+      for (int d = 1; d < 32; d <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, z, d);
+        if (lane >= d) z += u;
+      }
+      s_warp[lane] = z;
+    }
+    __syncthreads();
+    s_bin[tid] = x - own + (warp > 0 ? s_warp[warp - 1] : 0);
+    if (tid == 1023) plan->nblocks = min(s_bin[tid] + own, cap);
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The attention kernel.
+// ---------------------------------------------------------------------------
+template <int D>
+struct Cfg {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kTileBytes = kHalves * kBoxBytes;
+  static constexpr int kSlots = D == 128 ? 5 : 8;  // K(j), V(j) take consecutive slots
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffRing = 2 * kTileBytes;
+  static constexpr int kOffBar = kOffRing + kSlots * kTileBytes;
+  static constexpr int kBarQFull = 0;
+  static constexpr int kBarQEmpty = 1;
+  static constexpr int kBarFull = 2;
+  static constexpr int kBarEmpty = kBarFull + kSlots;
+  static constexpr int kBarS = kBarEmpty + kSlots;
+  static constexpr int kBarP = kBarS + 2;
+  static constexpr int kBarO = kBarP + 2;
+  static constexpr int kBarDrain = kBarO + 2;
+  static constexpr int kNumBars = kBarDrain + 1;
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  static constexpr int kSmemBytes = kOffMisc + 16 + 1024;  // + slack for 1024-B alignment
+};
+
+__host__ __device__ constexpr uint32_t col_s(int i) { return 128u * (uint32_t)i; }
+__host__ __device__ constexpr uint32_t col_o(int i) { return 256u + 128u * (uint32_t)i; }
+
+struct Work {
+  const Plan* plan;   // nullptr: one sequence, decoded in closed form
+  const Block* list;
+  int rows;           // rows of a block: 128 (two heads an item) or 256 (two row tiles)
+  int inner;          // items per block and kv head
+};
+
+// Walks the items of one CTA; the next item's block is fetched an item ahead.
+struct Items {
+  int nblocks, n_items, k, grp, Hkv, rows, inner;
+  const Block* list;
+  int q0, nq, k0, nk;  // the single sequence
+  Block next_block;
+  int next_g, next_sub;
+  bool next_ok;
+
+  __device__ __forceinline__ void fetch() {
+    const int grid = (int)gridDim.x, cta = (int)blockIdx.x;
+    const long long idx = (long long)k * grid + ((k & 1) ? (grid - 1 - cta) : cta);
+    next_ok = idx < n_items;
+    if (!next_ok) return;
+    int rank;
+    banded_item((int)idx, Hkv, nblocks, inner, grid, 0, next_g, rank, next_sub);
+    if (list != nullptr) {
+      const int4* p = reinterpret_cast<const int4*>(list + rank);
+      const int4 x = p[0];
+      next_block.qrow = x.x;
+      next_block.nrows = x.y;
+      next_block.krow = x.z;
+      next_block.nk = x.w;
+      next_block.diag = p[1].x;
+    } else {
+      next_block = make_block(q0, nq, k0, nk, (nblocks - 1 - rank) * rows);
+    }
+  }
+  __device__ __forceinline__ void init(const PromptArgs& a, const Work& w) {
+    Hkv = a.Hkv;
+    grp = a.H / a.Hkv;
+    rows = w.rows;
+    inner = w.inner;
+    list = w.plan != nullptr ? w.list : nullptr;
+    if (w.plan != nullptr) {
+      nblocks = w.plan->nblocks;
+    } else {
+      packed_rows(a.cu_q, 0, a.Nq, q0, nq);
+      packed_rows(a.cu_k, 0, a.Nk, k0, nk);
+      nblocks = (nq + rows - 1) / rows;
+    }
+    n_items = nblocks * Hkv * inner;
+    k = 0;
+    fetch();
+  }
+  // The item: its block, kv head g and, per query tile i, head and first row.
+  __device__ __forceinline__ bool next(Block& b, int& g, int& h0) {
+    if (!next_ok) return false;
+    b = next_block;
+    g = next_g;
+    h0 = next_g * grp + next_sub * (rows == kT ? 2 : 1);
+    ++k;
+    fetch();
+    return true;
+  }
+};
+
+template <bool kBf16, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_v, const PromptArgs a, const Work w) {
+  using C = Cfg<D>;
+  constexpr int kSlots = C::kSlots;
+  constexpr uint32_t kIdescQK = idesc_f16(kBf16, 128, 128, false, false);
+  constexpr uint32_t kIdescPV = idesc_f16(kBf16, 128, D, false, true);
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base - raw);
+  const uint32_t sQ = base + C::kOffQ, sRing = base + C::kOffRing;
+  const uint32_t bars = base + C::kOffBar;
+  auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const WaitCtl wc{abort_flag, a.err};
+  const int row_step = w.rows == kT ? 0 : kT;   // second query tile: rows further on,
+  const int head_step = w.rows == kT ? 1 : 0;   // or the next head
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar(C::kBarQFull), 1);
+    mbar_init(bar(C::kBarQEmpty), 1);
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(bar(C::kBarFull + s), 1);
+      mbar_init(bar(C::kBarEmpty + s), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(C::kBarS + i), 1);
+      mbar_init(bar(C::kBarP + i), 128);
+      mbar_init(bar(C::kBarO + i), 1);
+    }
+    mbar_init(bar(C::kBarDrain), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (w.plan != nullptr) {
+    wait_prior_grid();  // the plan
+  } else if (blockIdx.x == 0 && threadIdx.x == 0) {
+    int x, y;
+    if (!packed_rows(a.cu_q, 0, a.Nq, x, y) || !packed_rows(a.cu_k, 0, a.Nk, x, y))
+      atomicExch(a.err, kErrBadTables);
+  }
+
+  Items items;
+  Block b;
+  int g, h0;
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA
+    const bool leader = elect_one();
+    auto wwait = [&](uint32_t bar_addr, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar_addr, parity, wc));
+    };
+    if (leader) {
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
+    uint32_t seq = 0, q_armed = 0, armed[kSlots] = {0};
+    bool ok = true;
+    items.init(a, w);
+    for (int k = 0; ok && items.next(b, g, h0); ++k) {
+      if (!wwait(bar(C::kBarQEmpty), (k & 1) ^ 1)) {
+        ok = false;
+        break;
+      }
+      ++q_armed;
+      if (leader) {
+        mbar_arrive_expect_tx(bar(C::kBarQFull), 2 * C::kTileBytes);
+        for (int i = 0; i < 2; ++i)
+          for (int half = 0; half < C::kHalves; ++half)
+            tma_load_3d(sQ + i * C::kTileBytes + half * kBoxBytes, &tm_q, bar(C::kBarQFull),
+                        half * 64, h0 + i * head_step, b.qrow + i * row_step);
+      }
+      const int nt = max(key_tiles(b, a.causal, 0, kT), key_tiles(b, a.causal, row_step, kT));
+      for (int m = 0; ok && m < nt; ++m) {
+        for (int which = 0; which < 2; ++which) {  // K(m), then V(m)
+          const uint32_t n = seq++;
+          const int sl = n % kSlots;
+          if (!wwait(bar(C::kBarEmpty + sl), ((n / kSlots) & 1) ^ 1)) {
+            ok = false;
+            break;
+          }
+          ++armed[sl];
+          if (leader) {
+            mbar_arrive_expect_tx(bar(C::kBarFull + sl), C::kTileBytes);
+            for (int half = 0; half < C::kHalves; ++half)
+              tma_load_3d(sRing + sl * C::kTileBytes + half * kBoxBytes, which == 0 ? &tm_k : &tm_v,
+                          bar(C::kBarFull + sl), half * 64, g, b.krow + m * kT);
+          }
+        }
+      }
+    }
+    if (!ok) {
+      // Let the copies already issued land before the CTA exits.
+      if (q_armed) mbar_drain(bar(C::kBarQFull), (q_armed - 1) & 1);
+      for (int s = 0; s < kSlots; ++s)
+        if (armed[s]) mbar_drain(bar(C::kBarFull + s), (armed[s] - 1) & 1);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA
+    const bool leader = elect_one();
+    auto wwait = [&](uint32_t bar_addr, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar_addr, parity, wc));
+    };
+    uint32_t kv_it = 0, p_ph[2] = {0, 0};
+    bool ok = true;
+    // Operand descriptors, computed once and advanced by byte offsets.
+    const uint64_t d_q = sdesc_sw128(sQ, 16, 1024);
+    const uint64_t d_k = sdesc_sw128(sRing, 16, 1024);
+    const uint64_t d_v = sdesc_sw128(sRing, kBoxBytes, 1024);
+    auto slot_off = [](uint32_t n) { return (n % kSlots) * (uint32_t)C::kTileBytes; };
+    auto scores = [&](int i, uint32_t kn) {  // S_i = Q_i K^T of ring entry kn
+      if (!leader) return;
+      const uint64_t a0 = sdesc_advance(d_q, i * C::kTileBytes);
+      const uint64_t b0 = sdesc_advance(d_k, slot_off(kn));
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = (kk >> 2) * kBoxBytes + (kk & 3) * 32;
+        mma_ss(tmem + col_s(i), sdesc_advance(a0, off), sdesc_advance(b0, off), kIdescQK, kk > 0);
+      }
+      mma_commit(bar(C::kBarS + i));
+    };
+    items.init(a, w);
+    for (int k = 0; ok && items.next(b, g, h0); ++k) {
+      if (!wwait(bar(C::kBarQFull), k & 1)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const int nt0 = key_tiles(b, a.causal, 0, kT), nt1 = key_tiles(b, a.causal, row_step, kT);
+      const int nt = max(nt0, nt1);
+      if (nt == 0) {
+        if (leader) mma_commit(bar(C::kBarQEmpty));
+        continue;
+      }
+      // K(m) is ring entry 2 * kv_it, V(m) entry 2 * kv_it + 1.
+      uint32_t kn = 2 * kv_it;
+      if (!wwait(bar(C::kBarFull + kn % kSlots), (kn / kSlots) & 1)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      if (nt0 > 0) scores(0, kn);
+      if (nt1 > 0) scores(1, kn);
+      if (leader) mma_commit(bar(C::kBarEmpty + kn % kSlots));
+      for (int m = 0; m < nt; ++m) {
+        const bool have_next = m + 1 < nt;
+        const uint32_t vn = 2 * kv_it + 1, nkn = 2 * kv_it + 2;
+        if (!wwait(bar(C::kBarFull + vn % kSlots), (vn / kSlots) & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        bool k_ready = false;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int nti = i == 0 ? nt0 : nt1;
+          if (m < nti) {
+            if (!wwait(bar(C::kBarP + i), p_ph[i])) {
+              ok = false;
+              break;
+            }
+            p_ph[i] ^= 1;
+            tc_fence_after();
+            const uint64_t bv = sdesc_advance(d_v, slot_off(vn));
+            if (leader) {
+#pragma unroll
+              for (int kk = 0; kk < kT / 16; ++kk)
+                mma_ts(tmem + col_o(i), tmem + col_s(i) + kk * 8, sdesc_advance(bv, kk * 2048),
+                       kIdescPV, (m > 0) | (kk > 0));
+            }
+          }
+          if (m + 1 < nti) {
+            if (!k_ready) {
+              if (!wwait(bar(C::kBarFull + nkn % kSlots), (nkn / kSlots) & 1)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              k_ready = true;
+            }
+            scores(i, nkn);
+          }
+        }
+        if (!ok) break;
+        if (leader) {
+          mma_commit(bar(C::kBarEmpty + vn % kSlots));
+          if (have_next) mma_commit(bar(C::kBarEmpty + nkn % kSlots));
+        }
+        ++kv_it;
+      }
+      if (!ok) break;
+      if (leader) {
+        // O_i is released only to a warpgroup that waits for it.
+        if (nt0 > 0) mma_commit(bar(C::kBarO + 0));
+        if (nt1 > 0) mma_commit(bar(C::kBarO + 1));
+        mma_commit(bar(C::kBarQEmpty));
+      }
+    }
+    if (!ok) {
+      // Let every MMA already issued retire before TMEM is released.
+      if (leader) mma_commit(bar(C::kBarDrain));
+      mbar_drain(bar(C::kBarDrain), 0);
+    }
+  } else if (warp >= 4) {
+    // -------------------------------------------------------------- softmax
+    const int ti = (warp - 4) >> 2;  // query tile of this warpgroup
+    const int wq = warp & 3;         // TMEM sub-partition = rows 32*wq ..
+    const int row = wq * 32 + lane;  // row within the tile
+    const uint32_t tl = tmem + ((uint32_t)(wq * 32) << 16);
+    const uint32_t colS = col_s(ti), colO = col_o(ti);
+    const float sl2 = a.scale_log2;
+    uint32_t s_ph = 0, o_ph = 0, kv_it = 0;
+    bool ok = true;
+    items.init(a, w);
+    while (ok && items.next(b, g, h0)) {
+      const int nt0 = key_tiles(b, a.causal, 0, kT), nt1 = key_tiles(b, a.causal, row_step, kT);
+      const int nt = ti == 0 ? nt0 : nt1;
+      const int at = ti * row_step + row;  // row within the block
+      const int end = a.causal ? min(b.nk, b.diag + at) : b.nk;  // keys that the row sees
+      float m = -INFINITY, l = 0.f;
+      for (int t = 0; t < nt; ++t) {
+        const int see = end - t * kT;  // visible columns of the tile
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(C::kBarS + ti), s_ph, wc))) {
+          ok = false;
+          break;
+        }
+        s_ph ^= 1;
+        tc_fence_after();
+        uint32_t r[128];
+        tmem_ld32(tl + colS + 0, r + 0);
+        tmem_ld32(tl + colS + 32, r + 32);
+        tmem_ld32(tl + colS + 64, r + 64);
+        tmem_ld32(tl + colS + 96, r + 96);
+        tmem_wait_ld_regs(r);
+        reg_fence32(r + 32);
+        reg_fence32(r + 64);
+        reg_fence32(r + 96);
+        if (see < kT) {
+#pragma unroll
+          for (int j = 0; j < 128; ++j)
+            if (j >= see) r[j] = __float_as_uint(-INFINITY);
+        }
+        float mx0 = __uint_as_float(r[0]), mx1 = __uint_as_float(r[1]);
+        float mx2 = __uint_as_float(r[2]), mx3 = __uint_as_float(r[3]);
+#pragma unroll
+        for (int j = 4; j < 128; j += 4) {
+          mx0 = fmaxf(mx0, __uint_as_float(r[j]));
+          mx1 = fmaxf(mx1, __uint_as_float(r[j + 1]));
+          mx2 = fmaxf(mx2, __uint_as_float(r[j + 2]));
+          mx3 = fmaxf(mx3, __uint_as_float(r[j + 3]));
+        }
+        const float m_tile = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * sl2;
+        const float m_new = fmaxf(m, m_tile);
+        const bool need = m_new > m + kRescaleThreshold;
+        const bool rescale = __any_sync(0xffffffffu, need);
+        float alpha = 1.f;
+        if (rescale) {
+          // A row that has seen no key yet keeps m = -inf and alpha = 1.
+          alpha = m_new == -INFINITY ? 1.f : ex2(m - m_new);
+          l *= alpha;
+          m = m_new;
+        }
+        const float nm = m == -INFINITY ? 0.f : -m;
+        float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t p[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float a0 = ex2(fmaf(__uint_as_float(r[64 * h + 2 * j]), sl2, nm));
+            const float a1 = ex2(fmaf(__uint_as_float(r[64 * h + 2 * j + 1]), sl2, nm));
+            l0 += a0;
+            l1 += a1;
+            p[j] = pack16<kBf16>(a0, a1);
+          }
+          tmem_st32(tl + colS + 32 * h, p);
+        }
+        l += l0 + l1;
+        if (rescale && t > 0) {
+          // Softmax-state correction: O <- O * 2^(m_old - m_new).  The S
+          // barrier of this tile also covers the previous P V product, and the
+          // next one is issued only after the P barrier below.
+#pragma unroll
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t o[32];
+            tmem_ld32(tl + colO + cc * 32, o);
+            tmem_wait_ld_regs(o);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+            tmem_st32(tl + colO + cc * 32, o);
+          }
+        }
+        const int valid = b.nk - t * kT;
+        if (valid < kT && (ti == 0 || t >= nt0)) {
+          // V rows behind the sequence's end.  The warpgroup of the first
+          // query tile that uses the V tile clears them: the other's product
+          // is issued after its product.
+          const uint32_t vn = 2 * (kv_it + t) + 1;
+          if (!__all_sync(0xffffffffu,
+                          mbar_wait(bar(C::kBarFull + vn % kSlots), (vn / kSlots) & 1, wc))) {
+            ok = false;
+            break;
+          }
+          if (row >= valid) {
+            uint8_t* p = smem + C::kOffRing + (vn % kSlots) * C::kTileBytes + row * 128;
+#pragma unroll
+            for (int half = 0; half < C::kHalves; ++half)
+#pragma unroll
+              for (int c = 0; c < 8; ++c)
+                *reinterpret_cast<uint4*>(p + half * kBoxBytes + c * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_async_shared();
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(C::kBarP + ti));
+      }
+      if (!ok) break;
+      kv_it += max(nt0, nt1);
+      // ------------------------------------------------------------ epilogue
+      const bool live = at < b.nrows;
+      const int64_t qrow = b.qrow + at;
+      const int head = h0 + ti * head_step;
+      uint4* op = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
+                                           (qrow * a.H + head) * D);
+      float* lp = a.lse + (int64_t)head * a.Nq + qrow;
+      if (nt == 0) {
+        if (live) {
+          for (int j = 0; j < D / 8; ++j) op[j] = make_uint4(0u, 0u, 0u, 0u);
+          *lp = -INFINITY;
+        }
+        continue;
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait(bar(C::kBarO + ti), o_ph, wc))) {
+        ok = false;
+        break;
+      }
+      o_ph ^= 1;
+      tc_fence_after();
+      const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees nothing: 0
+#pragma unroll
+      for (int cc = 0; cc < D / 32; ++cc) {
+        uint32_t o[32];
+        tmem_ld32(tl + colO + cc * 32, o);
+        tmem_wait_ld_regs(o);
+        if (live) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint4 v;
+            v.x = pack16<kBf16>(__uint_as_float(o[8 * j + 0]) * inv, __uint_as_float(o[8 * j + 1]) * inv);
+            v.y = pack16<kBf16>(__uint_as_float(o[8 * j + 2]) * inv, __uint_as_float(o[8 * j + 3]) * inv);
+            v.z = pack16<kBf16>(__uint_as_float(o[8 * j + 4]) * inv, __uint_as_float(o[8 * j + 5]) * inv);
+            v.w = pack16<kBf16>(__uint_as_float(o[8 * j + 6]) * inv, __uint_as_float(o[8 * j + 7]) * inv);
+            op[cc * 4 + j] = v;
+          }
+        }
+      }
+      if (live) *lp = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+// Rows of [heads, D], `stride` elements apart, as a 3-D tensor (d, head, row),
+// box (64, 1, 128) with 128-byte swizzle.
+bool make_map(CUtensorMap* m, const void* ptr, bool bf16, int heads, int D, int64_t stride,
+              int64_t rows) {
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows};
+  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+  cuuint32_t box[3] = {64, 1, (cuuint32_t)kT};
+  return encode_tiled(m, bf16, 3, ptr, dims, strides, box);
+}
+
+// Blocks that the plan may list: a sequence's last block of `rows` may be short.
+int64_t most_blocks(int R, int Nq) { return (int64_t)Nq / kT + R; }
+
+template <bool kBf16, int D>
+cudaError_t run(const PromptArgs& a, cudaStream_t stream) {
+  const int grp = a.H / a.Hkv;
+  Work w;
+  w.rows = grp % 2 == 0 ? kT : 2 * kT;
+  w.inner = grp % 2 == 0 ? grp / 2 : grp;
+  w.plan = nullptr;
+  w.list = nullptr;
+  CUtensorMap mq, mk, mv;
+  // No keys at all: every item has no tiles, nothing is read through the maps.
+  const bool keys = a.Nk > 0;
+  if (!make_map(&mq, a.q, kBf16, a.H, D, a.q_stride, a.Nq) ||
+      !make_map(&mk, keys ? a.k : a.q, kBf16, keys ? a.Hkv : a.H, D, keys ? a.k_stride : a.q_stride,
+                keys ? a.Nk : a.Nq) ||
+      !make_map(&mv, keys ? a.v : a.q, kBf16, keys ? a.Hkv : a.H, D, keys ? a.v_stride : a.q_stride,
+                keys ? a.Nk : a.Nq))
+    return cudaErrorInvalidValue;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int smem = Cfg<D>::kSmemBytes;
+  e = cudaFuncSetAttribute(prompt_kernel<kBf16, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           smem);
+  if (e != cudaSuccess) return e;
+  const int64_t most = (a.Nq / w.rows + (int64_t)a.R) * a.Hkv * w.inner;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(most < sms ? most : sms));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  if (a.R > 1) {
+    // The plan goes first; this kernel sets itself up meanwhile.
+    Plan* plan = static_cast<Plan*>(a.workspace);
+    Block* list = reinterpret_cast<Block*>(plan + 1);
+    const int cap = (int)most_blocks(a.R, a.Nq);
+    prompt_plan_kernel<<<1, 1024, 0, stream>>>(a, w.rows, cap, plan, list);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    w.plan = plan;
+    w.list = list;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+  }
+  return cudaLaunchKernelEx(&cfg, prompt_kernel<kBf16, D>, mq, mk, mv, a, w);
+}
+
+}  // namespace
+
+size_t prompt_workspace_bytes(int R, int Nq) {
+  return sizeof(Plan) + (size_t)most_blocks(R, Nq) * sizeof(Block);
+}
+
+cudaError_t launch_prompt_attn(const PromptArgs& a, int dtype, cudaStream_t stream) {
+  if (dtype == CPATTN_BF16) return a.D == 128 ? run<true, 128>(a, stream) : run<true, 64>(a, stream);
+  return a.D == 128 ? run<false, 128>(a, stream) : run<false, 64>(a, stream);
+}
+
+}  // namespace cpattn

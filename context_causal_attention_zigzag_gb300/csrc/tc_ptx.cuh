@@ -17,6 +17,7 @@
 
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -269,16 +270,20 @@ __device__ __forceinline__ uint64_t sdesc_advance(uint64_t desc, uint32_t bytes)
   return desc + (uint64_t)(bytes >> 4);
 }
 
-// Instruction descriptor, kind::f16: bf16 A and B, fp32 accumulator, M x N.
+// Instruction descriptor, kind::f16: bf16 (or both fp16) A and B, fp32
+// accumulator, M x N.
 // a_mn / b_mn: operand is MN-major (output dim contiguous) instead of K-major.
-__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn, bool b_mn) {
+__host__ __device__ constexpr uint32_t idesc_f16(bool bf16, int M, int N, bool a_mn, bool b_mn) {
   return (1u << 4)                          // D format: f32
-         | (1u << 7)                        // A format: bf16
-         | (1u << 10)                       // B format: bf16
+         | ((bf16 ? 1u : 0u) << 7)          // A format: bf16 or fp16
+         | ((bf16 ? 1u : 0u) << 10)         // B format
          | ((a_mn ? 1u : 0u) << 15)         // A major
          | ((b_mn ? 1u : 0u) << 16)         // B major
          | ((uint32_t)(N >> 3) << 17)       // N / 8
          | ((uint32_t)(M >> 4) << 24);      // M / 16
+}
+__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn, bool b_mn) {
+  return idesc_f16(true, M, N, a_mn, b_mn);
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -290,6 +295,32 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// Two values of one 16-bit type, rounded to nearest.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  if constexpr (kBf16) {
+    return pack_bf16(lo, hi);
+  } else {
+    __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&v);
+  }
+}
+
+// Orders this thread's shared-memory writes before later accesses of the
+// tensor cores and TMA (the async proxy).
+__device__ __forceinline__ void fence_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Programmatic launches: lets the next kernel of the stream start, and waits
+// until the one before has finished and its writes are visible.
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_prior_grid() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 }  // namespace tc
