@@ -612,6 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             op[cc * 4 + j] = v;
           }
         }
+        __syncwarp();
       }
       if (live) *lp = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     }
