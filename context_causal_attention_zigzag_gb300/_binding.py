@@ -716,7 +716,7 @@ def _heads_rows(t, name):
 
 
 def _on(device, name, t, dtype=None, numel=None):
-    """One checked operand of an answering call, contiguous on q's device."""
+    """Refuses an operand that is not contiguous, on `device`, of this type and size."""
     if t.device != device:
         raise ValueError(f"{name} must be on {device}")
     if dtype is not None and t.dtype != dtype:
@@ -744,17 +744,31 @@ def _table_args(table, R, device):
 
 def _cache_args(k_cache, v_cache, Hkv, D, dtype, device):
     """(num_pages, page_size, strides) of a cache [pages, page_size, Hkv, D]."""
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape \
-            or k_cache.stride() != v_cache.stride():
+    shape, strides = k_cache.shape, k_cache.stride()
+    if len(shape) != 4 or shape != v_cache.shape or strides != v_cache.stride():
         raise ValueError("k_cache and v_cache must be [pages, page_size, Hkv, D] of one shape "
                          "and strides")
-    if k_cache.shape[2] != Hkv or k_cache.shape[3] != D or k_cache.stride(3) != 1:
+    if shape[2] != Hkv or shape[3] != D or strides[3] != 1:
         raise ValueError(f"the cache must hold {Hkv} heads of {D} contiguous values")
     if k_cache.dtype != dtype or v_cache.dtype != dtype:
         raise TypeError(f"the cache must be {dtype}")
     if k_cache.device != device or v_cache.device != device:
         raise ValueError(f"the cache must be on {device}")
-    return (k_cache.shape[0], k_cache.shape[1]) + k_cache.stride()[:3]
+    return shape[0], shape[1], strides[0], strides[1], strides[2]
+
+
+def _launch(name, device, *args):
+    """Calls the library on `device`'s current stream.  These calls are short
+    enough for their way through Python to count: pointers go as plain numbers,
+    and the device is switched only if it has to be."""
+    fn = getattr(_lib or lib(), name)
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    if rc != OK:
+        raise CpattnError(name, rc)
 
 
 def page_tables(ctx_lens, new_lens, block_table, free_pages, page_size, num_slots, slots=None,
@@ -764,26 +778,23 @@ def page_tables(ctx_lens, new_lens, block_table, free_pages, page_size, num_slot
     place with pages from free_pages (int32).  Returns (slots int64
     [num_slots], cu int32 [R + 1], used int32 [1])."""
     dev = _cuda_device(ctx_lens)
-    R = ctx_lens.numel()
-    _on(dev, "ctx_lens", ctx_lens, torch.int32)
-    _on(dev, "new_lens", new_lens, torch.int32, R)
-    _on(dev, "free_pages", free_pages, torch.int32)
-    width, stride = _table_args(block_table, R, dev)
+    R, num_slots = ctx_lens.numel(), int(num_slots)
     if slots is None:
-        slots = torch.empty(int(num_slots), device=dev, dtype=torch.int64)
+        slots = torch.empty(num_slots, device=dev, dtype=torch.int64)
     if cu is None:
         cu = torch.empty(R + 1, device=dev, dtype=torch.int32)
     if used is None:
         used = torch.empty(1, device=dev, dtype=torch.int32)
-    _on(dev, "slots", slots, torch.int64, int(num_slots))
+    _on(dev, "ctx_lens", ctx_lens, torch.int32)
+    _on(dev, "new_lens", new_lens, torch.int32, R)
+    _on(dev, "free_pages", free_pages, torch.int32)
+    _on(dev, "slots", slots, torch.int64, num_slots)
     _on(dev, "cu", cu, torch.int32, R + 1)
     _on(dev, "used", used, torch.int32, 1)
-    with torch.cuda.device(dev):
-        rc = lib().cpattn_page_tables(_ptr(ctx_lens), _ptr(new_lens), R, int(page_size),
-                                      _ptr(free_pages), free_pages.numel(), _ptr(block_table),
-                                      width, stride, _ptr(cu), _ptr(slots), int(num_slots),
-                                      _ptr(used), _stream(ctx_lens))
-    _check("cpattn_page_tables", rc)
+    width, stride = _table_args(block_table, R, dev)
+    _launch("cpattn_page_tables", dev, ctx_lens.data_ptr(), new_lens.data_ptr(), R,
+            int(page_size), free_pages.data_ptr(), free_pages.numel(), block_table.data_ptr(),
+            width, stride, cu.data_ptr(), slots.data_ptr(), num_slots, used.data_ptr())
     return slots, cu, used
 
 
@@ -797,15 +808,12 @@ def cache_write(k, v, k_cache, v_cache, slots):
     N, Hkv, D = k.shape
     cache = _cache_args(k_cache, v_cache, Hkv, D, k.dtype, dev)
     _on(dev, "slots", slots, torch.int64, N)
-    with torch.cuda.device(dev):
-        rc = lib().cpattn_cache_write(_ptr(k), ks, _ptr(v), vs, _ptr(slots), N, _ptr(k_cache),
-                                      _ptr(v_cache), *cache, Hkv, D, code, _stream(k))
-    _check("cpattn_cache_write", rc)
+    _launch("cpattn_cache_write", dev, k.data_ptr(), ks, v.data_ptr(), vs, slots.data_ptr(), N,
+            k_cache.data_ptr(), v_cache.data_ptr(), *cache, Hkv, D, code)
     return k_cache, v_cache
 
 
-def _answer_outputs(q, out, lse, dev):
-    N, H, D = q.shape
+def _answer_outputs(q, N, H, D, out, lse, dev):
     if out is None:
         out = torch.empty((N, H, D), device=dev, dtype=q.dtype)
     if lse is None:
@@ -815,9 +823,10 @@ def _answer_outputs(q, out, lse, dev):
     return out, lse
 
 
-def _workspace(need, workspace, dev):
+def _workspace(workspace, dev, need, *shape):
+    """The caller's workspace, or one of need(*shape) bytes."""
     if workspace is None:
-        return torch.empty(max(need, 1), device=dev, dtype=torch.uint8)
+        return torch.empty(max(need(*shape), 1), device=dev, dtype=torch.uint8)
     _on(dev, "workspace", workspace, torch.uint8)
     return workspace
 
@@ -825,8 +834,8 @@ def _workspace(need, workspace, dev):
 def tree_attention_workspace(q, k_cache, cu):
     """Scratch for tree_attention calls with q of this shape."""
     N, H, D = q.shape
-    need = int(lib().cpattn_tree_attn_workspace_bytes(N, H, k_cache.shape[2], D))
-    return torch.empty(max(need, 1), device=q.device, dtype=torch.uint8)
+    return _workspace(None, q.device, lib().cpattn_tree_attn_workspace_bytes, N, H,
+                      k_cache.shape[2], D)
 
 
 def tree_attention(q, k_cache, v_cache, block_table, ctx_lens, cu, tree=None, scale=None, out=None,
@@ -846,21 +855,19 @@ def tree_attention(q, k_cache, v_cache, block_table, ctx_lens, cu, tree=None, sc
     width, stride = _table_args(block_table, R, dev)
     if tree is not None:
         _on(dev, "tree", tree, torch.int64, N)
-    out, lse = _answer_outputs(q, out, lse, dev)
-    ws = _workspace(lib().cpattn_tree_attn_workspace_bytes(N, H, Hkv, D), workspace, dev)
-    with torch.cuda.device(dev):
-        rc = lib().cpattn_tree_attn(_ptr(q), qs, _ptr(k_cache), _ptr(v_cache), *cache,
-                                    _ptr(block_table), width, stride, _ptr(ctx_lens), _ptr(cu),
-                                    _ptr(tree), _ptr(out), _ptr(lse), R, N, H, Hkv, D, code,
-                                    _scale(scale), _ptr(ws), ws.numel(), _stream(q))
-    _check("cpattn_tree_attn", rc)
+    out, lse = _answer_outputs(q, N, H, D, out, lse, dev)
+    ws = _workspace(workspace, dev, lib().cpattn_tree_attn_workspace_bytes, N, H, Hkv, D)
+    _launch("cpattn_tree_attn", dev, q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(),
+            *cache, block_table.data_ptr(), width, stride, ctx_lens.data_ptr(), cu.data_ptr(),
+            None if tree is None else tree.data_ptr(), out.data_ptr(), lse.data_ptr(), R, N, H,
+            Hkv, D, code, _scale(scale), ws.data_ptr(), ws.numel())
     return out, lse
 
 
 def prompt_attention_workspace(q, cu_q):
     """Scratch for prompt_attention calls with q and offsets of this shape."""
-    need = int(lib().cpattn_prompt_attn_workspace_bytes(cu_q.numel() - 1, q.shape[0]))
-    return torch.empty(max(need, 1), device=q.device, dtype=torch.uint8)
+    return _workspace(None, q.device, lib().cpattn_prompt_attn_workspace_bytes, cu_q.numel() - 1,
+                      q.shape[0])
 
 
 def prompt_attention(q, k, v, cu_q, cu_k=None, causal=True, scale=None, out=None, lse=None,
@@ -873,22 +880,20 @@ def prompt_attention(q, k, v, cu_q, cu_k=None, causal=True, scale=None, out=None
     if k.shape != v.shape or k.dtype != q.dtype or v.dtype != q.dtype \
             or k.device != dev or v.device != dev:
         raise ValueError("k and v must share a shape, and q's dtype and device")
-    code, qs, ks, vs = _answer_dtype(q), *map(_heads_rows, (q, k, v), "qkv")
+    code, qs, ks, vs = (_answer_dtype(q), _heads_rows(q, "q"), _heads_rows(k, "k"),
+                        _heads_rows(v, "v"))
     Nq, H, D = q.shape
-    Nk, Hkv = k.shape[:2]
-    if k.shape[2] != D:
+    Nk, Hkv, Dk = k.shape
+    if Dk != D:
         raise ValueError("q, k and v must share D")
     R = cu_q.numel() - 1
     _on(dev, "cu_q", cu_q, torch.int32)
     _on(dev, "cu_k", cu_k, torch.int32, R + 1)
-    out, lse = _answer_outputs(q, out, lse, dev)
-    ws = _workspace(lib().cpattn_prompt_attn_workspace_bytes(R, Nq), workspace, dev)
-    with torch.cuda.device(dev):
-        rc = lib().cpattn_prompt_attn(_ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(cu_q),
-                                      _ptr(cu_k), _ptr(out), _ptr(lse), R, Nq, Nk, H, Hkv, D,
-                                      int(bool(causal)), code, _scale(scale), _ptr(ws),
-                                      ws.numel(), _stream(q))
-    _check("cpattn_prompt_attn", rc)
+    out, lse = _answer_outputs(q, Nq, H, D, out, lse, dev)
+    ws = _workspace(workspace, dev, lib().cpattn_prompt_attn_workspace_bytes, R, Nq)
+    _launch("cpattn_prompt_attn", dev, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+            cu_q.data_ptr(), cu_k.data_ptr(), out.data_ptr(), lse.data_ptr(), R, Nq, Nk, H, Hkv, D,
+            1 if causal else 0, code, _scale(scale), ws.data_ptr(), ws.numel())
     return out, lse
 
 

@@ -389,6 +389,21 @@ __device__ __forceinline__ bool packed_rows(const int* cu, int r, int total, int
   return ok;
 }
 
+// A kernel's permission for `bytes` of dynamic shared memory, asked for once on
+// each device (a call costs about a microsecond).  Two threads that come first
+// together both ask, which is harmless.
+struct DeviceOnce {
+  static constexpr int kDevices = 64;
+  volatile bool done[kDevices];
+  cudaError_t shared_memory(const void* kernel, int device, int bytes) {
+    if (device >= 0 && device < kDevices && done[device]) return cudaSuccess;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && device >= 0 && device < kDevices) done[device] = true;
+    return e;
+  }
+};
+
 // A tiled tensor map of 16-bit values with 128-byte swizzle, out of bounds read
 // as zeros.
 bool encode_tiled(CUtensorMap* m, bool bf16, int rank, const void* ptr, const cuuint64_t* dims,

@@ -163,9 +163,9 @@ struct Cfg {
   static constexpr int kOffQ = 0;
   static constexpr int kOffRing = 2 * kTileBytes;
   static constexpr int kOffBar = kOffRing + kSlots * kTileBytes;
-  static constexpr int kBarQFull = 0;
-  static constexpr int kBarQEmpty = 1;
-  static constexpr int kBarFull = 2;
+  static constexpr int kBarQFull = 0;   // [2] per query tile
+  static constexpr int kBarQEmpty = 2;  // [2]
+  static constexpr int kBarFull = 4;
   static constexpr int kBarEmpty = kBarFull + kSlots;
   static constexpr int kBarS = kBarEmpty + kSlots;
   static constexpr int kBarP = kBarS + 2;
@@ -267,13 +267,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int head_step = w.rows == kT ? 1 : 0;   // or the next head
 
   if (threadIdx.x == 0) {
-    mbar_init(bar(C::kBarQFull), 1);
-    mbar_init(bar(C::kBarQEmpty), 1);
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(bar(C::kBarFull + s), 1);
       mbar_init(bar(C::kBarEmpty + s), 1);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(C::kBarQFull + i), 1);
+      mbar_init(bar(C::kBarQEmpty + i), 1);
       mbar_init(bar(C::kBarS + i), 1);
       mbar_init(bar(C::kBarP + i), 128);
       mbar_init(bar(C::kBarO + i), 1);
@@ -305,30 +305,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------------ TMA
     const bool leader = elect_one();
     auto wwait = [&](uint32_t bar_addr, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_wait(bar_addr, parity, wc));
+      return __all_sync(0xffffffffu, mbar_wait_short(bar_addr, parity, wc));
     };
     if (leader) {
       tma_prefetch_desc(&tm_q);
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
     }
-    uint32_t seq = 0, q_armed = 0, armed[kSlots] = {0};
+    uint32_t seq = 0, q_armed[2] = {0, 0}, armed[kSlots] = {0};
     bool ok = true;
     items.init(a, w);
-    for (int k = 0; ok && items.next(b, g, h0); ++k) {
-      if (!wwait(bar(C::kBarQEmpty), (k & 1) ^ 1)) {
-        ok = false;
-        break;
-      }
-      ++q_armed;
-      if (leader) {
-        mbar_arrive_expect_tx(bar(C::kBarQFull), 2 * C::kTileBytes);
-        for (int i = 0; i < 2; ++i)
+    while (ok && items.next(b, g, h0)) {
+      int nt = 0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int nti = key_tiles(b, a.causal, i * row_step, kT);
+        if (!ok || nti == 0) continue;  // a tile without keys is not multiplied
+        nt = max(nt, nti);
+        ok = wwait(bar(C::kBarQEmpty + i), (q_armed[i] & 1) ^ 1);
+        if (!ok) continue;
+        ++q_armed[i];
+        if (leader) {
+          mbar_arrive_expect_tx(bar(C::kBarQFull + i), C::kTileBytes);
           for (int half = 0; half < C::kHalves; ++half)
-            tma_load_3d(sQ + i * C::kTileBytes + half * kBoxBytes, &tm_q, bar(C::kBarQFull),
+            tma_load_3d(sQ + i * C::kTileBytes + half * kBoxBytes, &tm_q, bar(C::kBarQFull + i),
                         half * 64, h0 + i * head_step, b.qrow + i * row_step);
+        }
       }
-      const int nt = max(key_tiles(b, a.causal, 0, kT), key_tiles(b, a.causal, row_step, kT));
       for (int m = 0; ok && m < nt; ++m) {
         for (int which = 0; which < 2; ++which) {  // K(m), then V(m)
           const uint32_t n = seq++;
@@ -349,7 +352,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok) {
       // Let the copies already issued land before the CTA exits.
-      if (q_armed) mbar_drain(bar(C::kBarQFull), (q_armed - 1) & 1);
+      for (int i = 0; i < 2; ++i)
+        if (q_armed[i]) mbar_drain(bar(C::kBarQFull + i), (q_armed[i] - 1) & 1);
       for (int s = 0; s < kSlots; ++s)
         if (armed[s]) mbar_drain(bar(C::kBarFull + s), (armed[s] - 1) & 1);
     }
@@ -357,17 +361,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------------ MMA
     const bool leader = elect_one();
     auto wwait = [&](uint32_t bar_addr, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_wait(bar_addr, parity, wc));
+      return __all_sync(0xffffffffu, mbar_wait_short(bar_addr, parity, wc));
     };
-    uint32_t kv_it = 0, p_ph[2] = {0, 0};
+    uint32_t kv_it = 0, p_ph[2] = {0, 0}, q_ph[2] = {0, 0};
     bool ok = true;
     // Operand descriptors, computed once and advanced by byte offsets.
     const uint64_t d_q = sdesc_sw128(sQ, 16, 1024);
     const uint64_t d_k = sdesc_sw128(sRing, 16, 1024);
     const uint64_t d_v = sdesc_sw128(sRing, kBoxBytes, 1024);
     auto slot_off = [](uint32_t n) { return (n % kSlots) * (uint32_t)C::kTileBytes; };
-    auto scores = [&](int i, uint32_t kn) {  // S_i = Q_i K^T of ring entry kn
-      if (!leader) return;
+    auto scores = [&](int i, uint32_t kn) {  // S_i = Q_i K^T, K in ring entry kn
       const uint64_t a0 = sdesc_advance(d_q, i * C::kTileBytes);
       const uint64_t b0 = sdesc_advance(d_k, slot_off(kn));
 #pragma unroll
@@ -377,33 +380,52 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       mma_commit(bar(C::kBarS + i));
     };
+    auto values = [&](int i, uint32_t vn, uint32_t accumulate) {  // O_i += P_i V
+      const uint64_t bv = sdesc_advance(d_v, slot_off(vn));
+#pragma unroll
+      for (int kk = 0; kk < kT / 16; ++kk)
+        mma_ts(tmem + col_o(i), tmem + col_s(i) + kk * 8, sdesc_advance(bv, kk * 2048), kIdescPV,
+               accumulate | (kk > 0));
+    };
+    auto full = [&](uint32_t n) { return wwait(bar(C::kBarFull + n % kSlots), (n / kSlots) & 1); };
+    // An item's first scores of query tile i, which sees nti > 0 key tiles.
+    // After a tile's last scores its next Q may load.
+    auto first_scores = [&](int i, uint32_t kn, int nti) {
+      if (!wwait(bar(C::kBarQFull + i), q_ph[i]) || !full(kn)) return false;
+      q_ph[i] ^= 1;
+      tc_fence_after();
+      if (leader) {
+        scores(i, kn);
+        if (nti == 1) mma_commit(bar(C::kBarQEmpty + i));
+      }
+      return true;
+    };
+    // The next item with keys, as the tiles its two query tiles see.
+    int cur[2], nxt[2] = {0, 0};
     items.init(a, w);
-    for (int k = 0; ok && items.next(b, g, h0); ++k) {
-      if (!wwait(bar(C::kBarQFull), k & 1)) {
-        ok = false;
-        break;
+    auto next_item = [&](int (&nt)[2]) {
+      while (items.next(b, g, h0)) {
+        nt[0] = key_tiles(b, a.causal, 0, kT);
+        nt[1] = key_tiles(b, a.causal, row_step, kT);
+        if (nt[0] > 0 || nt[1] > 0) return true;
       }
-      tc_fence_after();
-      const int nt0 = key_tiles(b, a.causal, 0, kT), nt1 = key_tiles(b, a.causal, row_step, kT);
-      const int nt = max(nt0, nt1);
-      if (nt == 0) {
-        if (leader) mma_commit(bar(C::kBarQEmpty));
-        continue;
-      }
-      // K(m) is ring entry 2 * kv_it, V(m) entry 2 * kv_it + 1.
-      uint32_t kn = 2 * kv_it;
-      if (!wwait(bar(C::kBarFull + kn % kSlots), (kn / kSlots) & 1)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      if (nt0 > 0) scores(0, kn);
-      if (nt1 > 0) scores(1, kn);
-      if (leader) mma_commit(bar(C::kBarEmpty + kn % kSlots));
-      for (int m = 0; m < nt; ++m) {
-        const bool have_next = m + 1 < nt;
+      nt[0] = nt[1] = 0;
+      return false;
+    };
+    bool have = next_item(cur);
+    if (have) {
+      for (int i = 0; ok && i < 2; ++i)
+        if (cur[i] > 0) ok = first_scores(i, 0, cur[i]);
+      if (ok && leader) mma_commit(bar(C::kBarEmpty + 0));
+    }
+    // K(m) is ring entry 2 * kv_it, V(m) entry 2 * kv_it + 1.  Behind each query
+    // tile's product come its next scores.
+    while (ok && have) {
+      const bool more = next_item(nxt);
+      const int nt = max(cur[0], cur[1]);
+      for (int m = 0; m + 1 < nt; ++m) {
         const uint32_t vn = 2 * kv_it + 1, nkn = 2 * kv_it + 2;
-        if (!wwait(bar(C::kBarFull + vn % kSlots), (vn / kSlots) & 1)) {
+        if (!full(vn)) {
           ok = false;
           break;
         }
@@ -411,48 +433,66 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool k_ready = false;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int nti = i == 0 ? nt0 : nt1;
-          if (m < nti) {
+          if (m < cur[i]) {
             if (!wwait(bar(C::kBarP + i), p_ph[i])) {
               ok = false;
               break;
             }
             p_ph[i] ^= 1;
             tc_fence_after();
-            const uint64_t bv = sdesc_advance(d_v, slot_off(vn));
             if (leader) {
-#pragma unroll
-              for (int kk = 0; kk < kT / 16; ++kk)
-                mma_ts(tmem + col_o(i), tmem + col_s(i) + kk * 8, sdesc_advance(bv, kk * 2048),
-                       kIdescPV, (m > 0) | (kk > 0));
+              values(i, vn, m > 0);
+              if (m + 1 == cur[i]) mma_commit(bar(C::kBarO + i));
             }
           }
-          if (m + 1 < nti) {
+          if (m + 1 < cur[i]) {
             if (!k_ready) {
-              if (!wwait(bar(C::kBarFull + nkn % kSlots), (nkn / kSlots) & 1)) {
+              if (!full(nkn)) {
                 ok = false;
                 break;
               }
               tc_fence_after();
               k_ready = true;
             }
-            scores(i, nkn);
+            if (leader) {
+              scores(i, nkn);
+              if (m + 2 == cur[i]) mma_commit(bar(C::kBarQEmpty + i));
+            }
           }
         }
         if (!ok) break;
         if (leader) {
           mma_commit(bar(C::kBarEmpty + vn % kSlots));
-          if (have_next) mma_commit(bar(C::kBarEmpty + nkn % kSlots));
+          mma_commit(bar(C::kBarEmpty + nkn % kSlots));
         }
         ++kv_it;
       }
       if (!ok) break;
-      if (leader) {
-        // O_i is released only to a warpgroup that waits for it.
-        if (nt0 > 0) mma_commit(bar(C::kBarO + 0));
-        if (nt1 > 0) mma_commit(bar(C::kBarO + 1));
-        mma_commit(bar(C::kBarQEmpty));
+      // The item's last key tile: behind its products come the next item's first
+      // scores, so that the softmax finds them when it leaves the epilogue.
+      const uint32_t vn = 2 * kv_it + 1, nkn = 2 * kv_it + 2;
+      ok = full(vn);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (ok && nt == cur[i]) {
+          ok = wwait(bar(C::kBarP + i), p_ph[i]);
+          p_ph[i] ^= 1;
+          tc_fence_after();
+          if (ok && leader) {
+            values(i, vn, nt > 1);
+            mma_commit(bar(C::kBarO + i));
+          }
+        }
+        if (ok && nxt[i] > 0) ok = first_scores(i, nkn, nxt[i]);
       }
+      if (ok && leader) {
+        mma_commit(bar(C::kBarEmpty + vn % kSlots));
+        if (more) mma_commit(bar(C::kBarEmpty + nkn % kSlots));
+      }
+      ++kv_it;
+      cur[0] = nxt[0];
+      cur[1] = nxt[1];
+      have = more;
     }
     if (!ok) {
       // Let every MMA already issued retire before TMEM is released.
@@ -478,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -INFINITY, l = 0.f;
       for (int t = 0; t < nt; ++t) {
         const int see = end - t * kT;  // visible columns of the tile
-        if (!__all_sync(0xffffffffu, mbar_wait(bar(C::kBarS + ti), s_ph, wc))) {
+        if (!__all_sync(0xffffffffu, mbar_wait_short(bar(C::kBarS + ti), s_ph, wc))) {
           ok = false;
           break;
         }
@@ -538,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // Softmax-state correction: O <- O * 2^(m_old - m_new).  The S
           // barrier of this tile also covers the previous P V product, and the
           // next one is issued only after the P barrier below.
-#pragma unroll
+#pragma unroll 1
           for (int cc = 0; cc < D / 32; ++cc) {
             uint32_t o[32];
             tmem_ld32(tl + colO + cc * 32, o);
@@ -555,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // is issued after its product.
           const uint32_t vn = 2 * (kv_it + t) + 1;
           if (!__all_sync(0xffffffffu,
-                          mbar_wait(bar(C::kBarFull + vn % kSlots), (vn / kSlots) & 1, wc))) {
+                          mbar_wait_short(bar(C::kBarFull + vn % kSlots), (vn / kSlots) & 1, wc))) {
             ok = false;
             break;
           }
@@ -589,29 +629,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         continue;
       }
-      if (!__all_sync(0xffffffffu, mbar_wait(bar(C::kBarO + ti), o_ph, wc))) {
+      if (!__all_sync(0xffffffffu, mbar_wait_short(bar(C::kBarO + ti), o_ph, wc))) {
         ok = false;
         break;
       }
       o_ph ^= 1;
       tc_fence_after();
       const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees nothing: 0
-#pragma unroll
+      // After the transpose this lane writes piece lane % 4 of each 64 bytes of
+      // the quad's four rows.
+      const int quad_at = at - (lane & 3);
+      uint16_t* quad_out = static_cast<uint16_t*>(a.out) +
+                           ((int64_t)(b.qrow + quad_at) * a.H + head) * D + (lane & 3) * 8;
+      const int64_t row_step_out = (int64_t)a.H * D;
+#pragma unroll 1
       for (int cc = 0; cc < D / 32; ++cc) {
         uint32_t o[32];
         tmem_ld32(tl + colO + cc * 32, o);
         tmem_wait_ld_regs(o);
-        if (live) {
+        uint4 v[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint4 v;
-            v.x = pack16<kBf16>(__uint_as_float(o[8 * j + 0]) * inv, __uint_as_float(o[8 * j + 1]) * inv);
-            v.y = pack16<kBf16>(__uint_as_float(o[8 * j + 2]) * inv, __uint_as_float(o[8 * j + 3]) * inv);
-            v.z = pack16<kBf16>(__uint_as_float(o[8 * j + 4]) * inv, __uint_as_float(o[8 * j + 5]) * inv);
-            v.w = pack16<kBf16>(__uint_as_float(o[8 * j + 6]) * inv, __uint_as_float(o[8 * j + 7]) * inv);
-            op[cc * 4 + j] = v;
-          }
+        for (int j = 0; j < 4; ++j) {
+          v[j].x = pack16<kBf16>(__uint_as_float(o[8 * j + 0]) * inv, __uint_as_float(o[8 * j + 1]) * inv);
+          v[j].y = pack16<kBf16>(__uint_as_float(o[8 * j + 2]) * inv, __uint_as_float(o[8 * j + 3]) * inv);
+          v[j].z = pack16<kBf16>(__uint_as_float(o[8 * j + 4]) * inv, __uint_as_float(o[8 * j + 5]) * inv);
+          v[j].w = pack16<kBf16>(__uint_as_float(o[8 * j + 6]) * inv, __uint_as_float(o[8 * j + 7]) * inv);
         }
+        quad_transpose(v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (quad_at + j < b.nrows)
+            *reinterpret_cast<uint4*>(quad_out + j * row_step_out + cc * 32) = v[j];
         __syncwarp();
       }
       if (live) *lp = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
@@ -666,8 +714,8 @@ cudaError_t run(const PromptArgs& a, cudaStream_t stream) {
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const int smem = Cfg<D>::kSmemBytes;
-  e = cudaFuncSetAttribute(prompt_kernel<kBf16, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           smem);
+  static DeviceOnce allowed;
+  e = allowed.shared_memory(reinterpret_cast<const void*>(prompt_kernel<kBf16, D>), dev, smem);
   if (e != cudaSuccess) return e;
   const int64_t most = (a.Nq / w.rows + (int64_t)a.R) * a.Hkv * w.inner;
   cudaLaunchConfig_t cfg = {};

@@ -17,23 +17,27 @@
 //    a cut divides leaves float32 partials (normalised O, lse), at most two a
 //    CTA, which tree_merge_kernel joins; its launch overlaps this kernel's
 //    tail.  The lengths stay on the device: each CTA sums them itself.
+//    A piece also costs its start and its end, so an item counts kItemCost
+//    tiles more than it has when the line is cut.
 //  * TMA brings the pages of a tile, one box a page and 64 columns, into a
-//    ring of 160 KB per SM.
+//    ring of 192 KB per SM.
 //  * The two softmax warpgroups take turns on the key tiles (even, odd), each
 //    with its own running maximum, sum and O in TMEM, joined at the end of the
 //    piece; so one tile's softmax hides behind the other's products.
-//  * More than 128 rows (large trees, parts of prompts): an item has two row
-//    tiles, the warpgroups take one each, and each key tile is loaded once for
-//    both.
+//  * Between pieces nothing stands still: the next piece's pages and Q rows
+//    load and its first scores are computed while the last one's epilogue runs.
+//  * More than 128 rows (large trees, parts of prompts; kPair): an item has two
+//    row tiles, the warpgroups take one each, and each key tile is loaded once
+//    for both.
 // Pages hold whatever was left in them behind a request's last position:
 // scores there are replaced by -inf, and the V rows, which enter the product
 // with weight 0, are zeroed in shared memory first (0 * NaN is NaN).  Pages
 // that lie wholly behind it are not read.
 //
-// CTA = 384 threads: warp 0 loads, warp 1 owns TMEM and issues the products
-// S_i = Q_i K^T (SS) and O_i += P_i V (TS, P over S in TMEM), warps 4-7 and
-// 8-11 are the warpgroups, one thread per row.  TMEM: S0 [0,128) S1 [128,256)
-// O0 [256,384) O1 [384,512).
+// CTA = 384 threads: warp 0 loads K and V, warps 2 and 3 Q, warp 1 owns TMEM and
+// issues the products S_i = Q_i K^T (SS) and O_i += P_i V (TS, P over S in
+// TMEM), warps 4-7 and 8-11 are the warpgroups, one thread per row.  TMEM: S0
+// [0,128) S1 [128,256) O0 [256,384) O1 [384,512).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -55,16 +59,27 @@ constexpr int kMaxCtas = 160;  // partials are laid out for so many
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 
-template <int D>
+#ifndef ITEMCOST
+#define ITEMCOST 3
+#endif
+#ifndef MINPART
+#define MINPART 1
+#endif
+constexpr int kItemCost = ITEMCOST;  // what starting and ending an item costs, in key tiles
+constexpr int kMinPart = MINPART;   // least part of the line for a CTA
+
+template <int D, bool kPair>
 struct Cfg {
   static constexpr int kHalves = D / 64;
   static constexpr int kTileBytes = kHalves * kBoxBytes;
-  static constexpr int kSlots = D == 128 ? 5 : 10;  // K(x), V(x) take consecutive slots
-  static constexpr int kOffQ = 0;                   // two row tiles
-  static constexpr int kOffRing = 2 * kTileBytes;
+  static constexpr int kRowTiles = kPair ? 2 : 1;
+  static constexpr int kSlots = (D == 128 ? 1 : 2) * (kPair ? 5 : 6);
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffRing = kRowTiles * kTileBytes;
   static constexpr int kOffBar = kOffRing + kSlots * kTileBytes;
-  static constexpr int kBarQ = 0;
-  static constexpr int kBarFull = 1;
+  static constexpr int kBarQFull = 0;
+  static constexpr int kBarQEmpty = 1;
+  static constexpr int kBarFull = 2;
   static constexpr int kBarEmpty = kBarFull + kSlots;
   static constexpr int kBarS = kBarEmpty + kSlots;
   static constexpr int kBarP = kBarS + 2;
@@ -73,8 +88,9 @@ struct Cfg {
   static constexpr int kBarDrain = kBarMeet + 2;
   static constexpr int kNumBars = kBarDrain + 1;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  // The prologue's sums; then (m, l) of both warpgroups.
   static constexpr int kOffSums = (kOffMisc + 16 + 15) / 16 * 16;
-  static constexpr int kSmemBytes = kOffSums + 192 + 1024;  // + slack for 1024-B alignment
+  static constexpr int kSmemBytes = kOffSums + 2 * kT * 8;
 };
 
 __host__ __device__ constexpr uint32_t col_s(int i) { return 128u * (uint32_t)i; }
@@ -97,93 +113,109 @@ __device__ __forceinline__ bool load_req(const TreeArgs& a, int r, Req& x) {
   return ok;
 }
 
-// An item is a kv head of a request and up to two row tiles of `tpt` tokens.
-__device__ __forceinline__ int items_of(const Req& x, int tpt) {
-  return (x.n + 2 * tpt - 1) / (2 * tpt);
-}
+// An item is a kv head of a request and `span` of its tokens.
+__device__ __forceinline__ int items_of(const Req& x, int span) { return (x.n + span - 1) / span; }
 // Key tiles of the request's m-th item (at least one, so that its rows are
 // written); without a tree no row sees behind the item's last token.
-__device__ __forceinline__ int tiles_of(const Req& x, int tpt, bool chain, int m) {
-  const int last = min(x.n, (m + 1) * 2 * tpt);
+__device__ __forceinline__ int tiles_of(const Req& x, int span, bool chain, int m) {
+  const int last = min(x.n, (m + 1) * span);
   const int end = chain ? min(x.total, x.ctx + last) : x.total;
   return end > 0 ? (end + kT - 1) / kT : 1;
 }
-__device__ __forceinline__ long long head_tiles(const Req& x, int tpt, bool chain) {
+// What a kv head of the request counts on the line.
+__device__ __forceinline__ long long head_cost(const Req& x, int span, bool chain) {
   long long s = 0;
-  for (int m = 0, e = items_of(x, tpt); m < e; ++m) s += tiles_of(x, tpt, chain, m);
+  for (int m = 0, e = items_of(x, span); m < e; ++m) s += kItemCost + tiles_of(x, span, chain, m);
   return s;
 }
 
-// Where the c-th CTA's part of T tiles begins, and whose a tile is.
-__device__ __forceinline__ long long part_begin(long long c, long long T, int n) {
-  return c * T / n;
+// The line of length T is cut into n parts, part c beginning at floor(c T / n)
+// = c q + floor(c e / n) with T = q n + e (small numbers but for one division).
+__device__ __forceinline__ long long div_small(long long x, int n) {
+  return x <= 0xffffffffll ? (long long)((uint32_t)x / (uint32_t)n) : x / n;
 }
-__device__ __forceinline__ int part_of(long long t, long long T, int n) {
-  return (int)(((t + 1) * n - 1) / T);
-}
+struct Cuts {
+  long long q;
+  int e, n;
+  __device__ __forceinline__ void init(long long T, int n_) {
+    n = n_;
+    q = n > 0 ? div_small(T, n) : 0;
+    e = (int)(T - q * n);
+  }
+  __device__ __forceinline__ long long begin(int c) const {
+    return c * q + (n > 0 ? c * e / n : 0);
+  }
+  // The part that holds unit t.
+  __device__ __forceinline__ int of(long long t) const {
+    return (int)(((t + 1) * n - 1) / (q * n + e));
+  }
+};
 
 // A run of key tiles [t0, t1) of one item.
 struct Piece {
   Req x;
   int r, g, m, t0, t1, tiles;
-  long long at;  // the line's index of tile t0
-  bool pair;     // two row tiles
+  long long item_at;  // where the item begins on the line
 };
 
 // Walks the pieces of one CTA.
 struct Walk {
   Piece p;
-  long long left;
-  int off;  // tile within the item
+  long long left;  // of the CTA's part
+  int off;         // where it goes on within the item; -1: at the next item
   int items;
 
-  __device__ __forceinline__ void init(const TreeArgs& a, int tpt, int r, long long in_req,
-                                       long long at, long long n) {
-    p.r = r;
-    p.at = at;
+  // The part begins in request r (x), `in_req` behind the request's begin, at
+  // `at` on the line.
+  __device__ __forceinline__ void init(const TreeArgs& a, int span, int r, const Req& x,
+                                       long long in_req, long long at, long long n) {
     left = n;
     if (left <= 0) return;
-    load_req(a, r, p.x);
-    items = items_of(p.x, tpt);
-    const long long per = head_tiles(p.x, tpt, a.tree == nullptr);
-    p.g = (int)(in_req / per);
+    p.r = r;
+    p.x = x;
+    items = items_of(x, span);
+    const long long per = head_cost(x, span, a.tree == nullptr);
+    p.g = per <= 0x7fffffffll ? (int)div_small(in_req, (int)per) : (int)(in_req / per);
     long long rest = in_req - p.g * per;
     p.m = 0;
     while (true) {
-      const int t = tiles_of(p.x, tpt, a.tree == nullptr, p.m);
+      const int t = kItemCost + tiles_of(x, span, a.tree == nullptr, p.m);
       if (rest < t) break;
       rest -= t;
       ++p.m;
     }
     off = (int)rest;
-    p.t1 = off;
-    p.tiles = 0;  // the first call of next() stays on this item
+    p.item_at = at - rest;
+    p.tiles = 0;
   }
-  __device__ __forceinline__ bool next(const TreeArgs& a, int tpt) {
-    if (left <= 0) return false;
-    if (p.tiles != 0 && p.t1 == p.tiles) {
-      off = 0;
-      if (++p.m == items) {
-        p.m = 0;
-        if (++p.g == a.Hkv) {
-          p.g = 0;
-          do {
-            ++p.r;
-            load_req(a, p.r, p.x);
-          } while (p.x.n == 0);
-          items = items_of(p.x, tpt);
+  __device__ __forceinline__ bool next(const TreeArgs& a, int span) {
+    while (left > 0) {
+      if (off < 0) {
+        off = 0;
+        p.item_at += kItemCost + p.tiles;
+        if (++p.m == items) {
+          p.m = 0;
+          if (++p.g == a.Hkv) {
+            p.g = 0;
+            do {
+              ++p.r;
+              load_req(a, p.r, p.x);
+            } while (p.x.n == 0);
+            items = items_of(p.x, span);
+          }
         }
       }
+      p.tiles = tiles_of(p.x, span, a.tree == nullptr, p.m);
+      const int rest = kItemCost + p.tiles - off;
+      const int n = (int)(left < rest ? left : rest);
+      p.t0 = max(0, off - kItemCost);
+      p.t1 = max(0, off + n - kItemCost);
+      left -= n;
+      off = n == rest ? -1 : off + n;
+      if (p.t1 > p.t0) return true;
     }
-    p.tiles = tiles_of(p.x, tpt, a.tree == nullptr, p.m);
-    p.t0 = off;
-    const int n = (int)(left < p.tiles - off ? left : p.tiles - off);
-    p.t1 = off + n;
-    p.pair = p.x.n - p.m * 2 * tpt > tpt;
-    left -= n;
-    return true;
+    return false;
   }
-  __device__ __forceinline__ void done() { p.at += p.t1 - p.t0; }
 };
 
 // The partials: per CTA two places (0: of an item begun by an earlier CTA, 1:
@@ -225,33 +257,40 @@ __device__ __forceinline__ void seen_columns(uint32_t* vis, int k0, int ctx, boo
   vis[3] = (uint32_t)(v >> 96);
 }
 
-template <bool kBf16, int D>
+template <bool kBf16, int D, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                 const TreeArgs a, const Partials w) {
-  using C = Cfg<D>;
+  using C = Cfg<D, kPair>;
   constexpr int kSlots = C::kSlots;
   constexpr uint32_t kIdescQK = idesc_f16(kBf16, 128, 128, false, false);
   constexpr uint32_t kIdescPV = idesc_f16(kBf16, 128, D, false, true);
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  uint8_t* smem = smem_raw + (base - raw);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t base = smem_u32(smem);
+  if (base & 1023u) {  // the swizzled tiles need it; shared memory has no room for slack
+    if (threadIdx.x == 0) {
+      atomicExch(a.err, kErrLaunch);
+      w.cuts[blockIdx.x].last = -1;
+    }
+    return;
+  }
   const uint32_t sQ = base + C::kOffQ, sRing = base + C::kOffRing;
   const uint32_t bars = base + C::kOffBar;
   auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
-  long long* sums = reinterpret_cast<long long*>(smem + C::kOffSums);  // [12] warps, T, in_req, r
+  // [12] of the warps; then where this CTA begins: in_req, r and the request.
+  long long* sums = reinterpret_cast<long long*>(smem + C::kOffSums);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const WaitCtl wc{abort_flag, a.err};
-  const int G = a.H / a.Hkv, tpt = kT / G;
+  const int G = a.H / a.Hkv, tpt = kT / G, span = tpt * C::kRowTiles;
   const bool chain = a.tree == nullptr;
 
   launch_dependents();  // the merge sets itself up; it waits for this kernel's end
   if (threadIdx.x == 0) {
-    mbar_init(bar(C::kBarQ), 256);
+    mbar_init(bar(C::kBarQFull), 64);
+    mbar_init(bar(C::kBarQEmpty), 1);
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(bar(C::kBarFull + s), 1);
       mbar_init(bar(C::kBarEmpty + s), 1);
@@ -277,10 +316,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int r_lo = min(a.R, (int)threadIdx.x * per), r_hi = min(a.R, r_lo + per);
   long long own = 0;
   bool bad = false;
+  Req x;
   for (int r = r_lo; r < r_hi; ++r) {
-    Req x;
     bad |= !load_req(a, r, x);
-    own += head_tiles(x, tpt, chain) * a.Hkv;
+    own += head_cost(x, span, chain) * a.Hkv;
   }
   if (bad && blockIdx.x == 0) atomicExch(a.err, kErrBadTables);
   long long upto = own;
@@ -298,32 +337,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (i == warp) upto += T;
     T += sums[i];
   }
-  const int n_ctas = (int)(T < (long long)gridDim.x ? T : (long long)gridDim.x);
+  const long long parts = (T + kMinPart - 1) / kMinPart;
+  const int n_ctas = (int)(parts < (long long)gridDim.x ? parts : (long long)gridDim.x);
   const int cta = blockIdx.x;
+  Cuts cuts;
+  cuts.init(T, n_ctas);
   long long begin = 0, count = 0;
   if (cta < n_ctas) {
-    begin = part_begin(cta, T, n_ctas);
-    count = part_begin(cta + 1, T, n_ctas) - begin;
+    begin = cuts.begin(cta);
+    count = cuts.begin(cta + 1) - begin;
     if (begin >= upto - own && begin < upto) {
       long long at = upto - own;
-      for (int r = r_lo; r < r_hi; ++r) {
-        Req x;
+      int r = r_lo;
+      while (per > 1) {
         load_req(a, r, x);
-        const long long t = head_tiles(x, tpt, chain) * a.Hkv;
-        if (begin < at + t) {
-          sums[13] = begin - at;
-          sums[14] = r;
-          break;
-        }
+        const long long t = head_cost(x, span, chain) * a.Hkv;
+        if (begin < at + t) break;
         at += t;
+        ++r;
       }
+      sums[13] = begin - at;
+      sums[14] = r;
+      *reinterpret_cast<Req*>(sums + 16) = x;
     }
   }
   if (threadIdx.x == 0) w.cuts[cta].last = -1;
   __syncthreads();
   const uint32_t tmem = *tmem_slot;
   Walk walk;
-  walk.init(a, tpt, (int)sums[14], sums[13], begin, count);
+  walk.init(a, span, (int)sums[14], *reinterpret_cast<const Req*>(sums + 16), sums[13], begin,
+            count);
+  __syncthreads();  // the sums' place is used again
   Piece& p = walk.p;
 
   if (warp == 0) {
@@ -339,16 +383,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tm_v);
     }
     auto wwait = [&](uint32_t bar_addr, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_wait(bar_addr, parity, wc));
+      return __all_sync(0xffffffffu, mbar_wait_short(bar_addr, parity, wc));
     };
-    uint32_t seq = 0, armed[kSlots] = {0};
+    uint32_t seq = 0, armed = 0;
     bool ok = true;
-    while (ok && walk.next(a, tpt)) {
+    while (ok && walk.next(a, span)) {
       const int* table = a.table + (int64_t)p.r * a.table_stride;
       const int used = (p.x.total + P - 1) / P;  // pages that hold positions
       auto page_at = [&](int i) { return i < used ? table[i] : 0; };
       int win = p.t0 * kT / P;
       int now = page_at(win + lane), ahead = page_at(win + 32 + lane);
+      const int c = lane / C::kHalves, half = lane % C::kHalves;
       for (int t = p.t0; ok && t < p.t1; ++t) {
         const int first = t * kT / P;
         if (first + ppt > win + 32) {
@@ -358,21 +403,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           ahead = page_at(win + 32 + lane);
         }
         // Lane c * halves + half issues copy c of the tile, columns 64 * half.
-        const int c = lane / C::kHalves, half = lane % C::kHalves;
         const int id = __shfl_sync(0xffffffffu, now, (first - win + (c < ppt ? c : 0)) & 31);
         const bool mine = c < ppt && first + c < used;
         const bool good = mine && id >= 0 && id < npages;
         if (mine && !good) atomicExch(a.err, kErrBadTables);
         const uint32_t copies = __popc(__ballot_sync(0xffffffffu, good));
         const int row = (t * kT) % P;  // within the page (0 for pages up to a tile)
-        for (int which = 0; which < 2; ++which) {  // K(t), then V(t)
+#pragma unroll 1
+        for (int which = 0; ok && which < 2; ++which) {  // K(t), then V(t)
           const uint32_t n = seq++;
           const int sl = n % kSlots;
-          if (!wwait(bar(C::kBarEmpty + sl), ((n / kSlots) & 1) ^ 1)) {
-            ok = false;
-            break;
-          }
-          ++armed[sl];
+          ok = wwait(bar(C::kBarEmpty + sl), ((n / kSlots) & 1) ^ 1);
+          if (!ok) break;
+          armed |= 1u << sl;
           if (lane == 0) mbar_arrive_expect_tx(bar(C::kBarFull + sl), copies * box * 128);
           __syncwarp();
           if (good)
@@ -380,94 +423,165 @@ __global__ void __launch_bounds__(kThreads, 1)
                         which == 0 ? &tm_k : &tm_v, bar(C::kBarFull + sl), half * 64, p.g, row, id);
         }
       }
-      walk.done();
     }
     if (!ok) {
       // Let the copies already issued land before the CTA exits.
-      for (int s = 0; s < kSlots; ++s)
-        if (armed[s]) mbar_drain(bar(C::kBarFull + s), (armed[s] - 1) & 1);
+      // The last entry of slot s is the last one below seq that falls on it.
+      for (uint32_t s = 0; s < (uint32_t)kSlots; ++s) {
+        if (!(armed >> s & 1)) continue;
+        uint32_t n = seq - 1;
+        while (n % kSlots != s) --n;
+        mbar_drain(bar(C::kBarFull + s), (n / kSlots) & 1);
+      }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA
-    // Row tile i's s-th product takes key tile s of the piece (two row tiles)
-    // or 2 s + i (one row tile, the warpgroups taking turns).
+    // Stream i's s-th step takes key tile s of the piece (two row tiles) or
+    // 2 s + i (one row tile, the warpgroups taking turns).
     const bool leader = elect_one();
     auto wwait = [&](uint32_t bar_addr, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_wait(bar_addr, parity, wc));
+      return __all_sync(0xffffffffu, mbar_wait_short(bar_addr, parity, wc));
     };
     const uint64_t d_q = sdesc_sw128(sQ, 16, 1024);
     const uint64_t d_k = sdesc_sw128(sRing, 16, 1024);
     const uint64_t d_v = sdesc_sw128(sRing, kBoxBytes, 1024);
     auto slot_off = [](uint32_t n) { return (n % kSlots) * (uint32_t)C::kTileBytes; };
-    uint32_t kv = 0, p_ph[2] = {0, 0};
+    struct Run {
+      uint32_t kv;  // ring entries before the piece's
+      int nt;
+      bool pair;
+      __device__ __forceinline__ int steps(int i) const {
+        return pair ? nt : (nt + 1 - i) / 2;
+      }
+    };
+    Run cur{0, 0, false}, nxt;
+    uint32_t entries = 0, p_ph = 0, q_ph = 0;  // p_ph: bit i
     bool ok = true;
-    for (int k = 0; ok && walk.next(a, tpt); ++k) {
-      if (!wwait(bar(C::kBarQ), k & 1)) {
-        ok = false;
-        break;
+    auto next_run = [&](Run& u) {
+      if (!walk.next(a, span)) {
+        u.nt = 0;  // no steps
+        u.pair = false;
+        return false;
       }
+      u.kv = entries;
+      u.nt = p.t1 - p.t0;
+      u.pair = kPair && p.x.n - p.m * span > tpt;
+      entries += 2 * u.nt;
+      return true;
+    };
+    // The piece's key tile x has K in ring entry kv + 2 x and V behind it.
+    auto key_entry = [&](const Run& u, int i, int s) {
+      return u.kv + 2u * (uint32_t)(u.pair ? s : 2 * s + i);
+    };
+    auto full = [&](uint32_t n) { return wwait(bar(C::kBarFull + n % kSlots), (n / kSlots) & 1); };
+    // S_i of step s.  K is freed after its last reader, Q after the piece's last
+    // scores.
+    auto scores = [&](const Run& u, int i, int s) {
+      const uint32_t n = key_entry(u, i, s);
+      if (!full(n)) return false;
       tc_fence_after();
-      const bool pair = p.pair;
-      const int nt = p.t1 - p.t0;
-      const int steps[2] = {pair ? nt : (nt + 1) / 2, pair ? nt : nt / 2};
-      auto key_entry = [&](int i, int s) {
-        return 2 * (kv + (uint32_t)(pair ? s : 2 * s + i));
-      };
-      auto scores = [&](int i, int s) {  // S_i of step s; K is freed after its last reader
-        const uint32_t n = key_entry(i, s);
-        if (!wwait(bar(C::kBarFull + n % kSlots), (n / kSlots) & 1)) return false;
-        tc_fence_after();
-        if (leader) {
-          const uint64_t a0 = sdesc_advance(d_q, pair ? i * C::kTileBytes : 0);
-          const uint64_t b0 = sdesc_advance(d_k, slot_off(n));
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * kBoxBytes + (kk & 3) * 32;
-            mma_ss(tmem + col_s(i), sdesc_advance(a0, off), sdesc_advance(b0, off), kIdescQK,
-                   kk > 0);
-          }
-          mma_commit(bar(C::kBarS + i));
-          if (!pair || i == 1) mma_commit(bar(C::kBarEmpty + n % kSlots));
-        }
-        return true;
-      };
-      for (int i = 0; ok && i < 2; ++i)
-        if (steps[i] > 0) ok = scores(i, 0);
-      for (int s = 0; ok && s < steps[0]; ++s) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (!ok || s >= steps[i]) continue;
-          const uint32_t n = key_entry(i, s) + 1;
-          ok = wwait(bar(C::kBarFull + n % kSlots), (n / kSlots) & 1) &&
-               wwait(bar(C::kBarP + i), p_ph[i]);
-          if (!ok) continue;
-          p_ph[i] ^= 1;
-          tc_fence_after();
-          if (leader) {
-            const uint64_t bv = sdesc_advance(d_v, slot_off(n));
-#pragma unroll
-            for (int kk = 0; kk < kT / 16; ++kk)
-              mma_ts(tmem + col_o(i), tmem + col_s(i) + kk * 8, sdesc_advance(bv, kk * 2048),
-                     kIdescPV, (s > 0) | (kk > 0));
-            if (!pair || i == 1) mma_commit(bar(C::kBarEmpty + n % kSlots));
-          }
-          if (s + 1 < steps[i]) ok = scores(i, s + 1);
-        }
-      }
-      if (!ok) break;
       if (leader) {
-        mma_commit(bar(C::kBarO + 0));
-        if (steps[1] > 0) mma_commit(bar(C::kBarO + 1));
+        const uint64_t a0 = sdesc_advance(d_q, u.pair ? i * C::kTileBytes : 0);
+        const uint64_t b0 = sdesc_advance(d_k, slot_off(n));
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * kBoxBytes + (kk & 3) * 32;
+          mma_ss(tmem + col_s(i), sdesc_advance(a0, off), sdesc_advance(b0, off), kIdescQK,
+                 kk > 0);
+        }
+        mma_commit(bar(C::kBarS + i));
+        if (!u.pair || i == 1) mma_commit(bar(C::kBarEmpty + n % kSlots));
+        if (u.pair ? i == 1 && s + 1 == u.nt : 2 * s + i + 1 == u.nt)
+          mma_commit(bar(C::kBarQEmpty));
       }
-      kv += nt;
-      walk.done();
+      return true;
+    };
+    // O_i += P_i V of the piece's step s; V is freed after its last reader.
+    auto values = [&](const Run& u, int i, int s) {
+      const uint32_t n = key_entry(u, i, s) + 1;
+      if (!full(n) || !wwait(bar(C::kBarP + i), p_ph >> i & 1)) return false;
+      p_ph ^= 1u << i;
+      tc_fence_after();
+      if (leader) {
+        const uint64_t bv = sdesc_advance(d_v, slot_off(n));
+#pragma unroll
+        for (int kk = 0; kk < kT / 16; ++kk)
+          mma_ts(tmem + col_o(i), tmem + col_s(i) + kk * 8, sdesc_advance(bv, kk * 2048), kIdescPV,
+                 (s > 0) | (kk > 0));
+        if (!u.pair || i == 1) mma_commit(bar(C::kBarEmpty + n % kSlots));
+        if (s + 1 == u.steps(i)) mma_commit(bar(C::kBarO + i));
+      }
+      return true;
+    };
+    // Behind each product come the stream's next scores; at a piece's end they
+    // are the next piece's first, which its softmax finds when it leaves the
+    // epilogue.  The walk begins behind an empty piece.  One copy of the code
+    // serves it all: what runs once a piece misses the instruction cache.
+    bool more = next_run(nxt);
+    while (ok && (cur.nt > 0 || more)) {
+      const int steps = cur.steps(0);
+      int s = steps > 0 ? 0 : -1;
+      do {
+        const bool last = s + 1 >= steps;
+        const Run u = last ? nxt : cur;
+        const int ns = last ? 0 : s + 1;
+#pragma unroll 1
+        for (int i = 0; ok && i < 2; ++i) {
+          if (s >= 0 && s < cur.steps(i)) ok = values(cur, i, s);
+          if (last && i == 0 && more) {
+            ok = ok && wwait(bar(C::kBarQFull), q_ph);
+            q_ph ^= 1;
+          }
+          if (ok && ns < u.steps(i)) ok = scores(u, i, ns);
+        }
+        ++s;
+      } while (ok && s < steps);
+      cur = nxt;
+      more = more && next_run(nxt);
     }
     if (!ok) {
       // Let every MMA already issued retire before TMEM is released.
       if (leader) mma_commit(bar(C::kBarDrain));
       mbar_drain(bar(C::kBarDrain), 0);
     }
-  } else if (warp >= 4) {
+  } else if (warp < 4) {
+    // -------------------------------------------------------------------- Q
+    // The rows of each piece, copied by both warps as soon as the scores of
+    // the piece before are done: 16-byte pieces, a row's by neighbouring lanes.
+    constexpr int kPieces = D / 8, U = 8;
+    const int me = threadIdx.x - 64;
+    bool ok = true;
+    for (int k = 0; ok && walk.next(a, span); ++k) {
+      const int tok0 = p.m * span, ntok = min(span, p.x.n - tok0);
+      const int total = ntok * G * kPieces;
+      const uint16_t* src = static_cast<const uint16_t*>(a.q) + p.g * G * D;
+      for (int e0 = me; ok && e0 - me < total; e0 += 64 * U) {
+        uint4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int e = e0 + u * 64, r = e / kPieces, t = r / G;
+          if (e < total)
+            v[u] = *reinterpret_cast<const uint4*>(src + (p.x.q0 + tok0 + t) * a.q_stride +
+                                                   (r - t * G) * D + (e % kPieces) * 8);
+        }
+        if (e0 == me)
+          ok = __all_sync(0xffffffffu, mbar_wait_short(bar(C::kBarQEmpty), (k & 1) ^ 1, wc));
+        if (!ok) break;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int e = e0 + u * 64, r = e / kPieces, c = e % kPieces;
+          if (e < total) {
+            const int tile = kPair && r >= tpt * G ? 1 : 0, row = r - tile * tpt * G;
+            *reinterpret_cast<uint4*>(smem + C::kOffQ + tile * C::kTileBytes + (c >> 3) * kBoxBytes +
+                                      row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v[u];
+          }
+        }
+      }
+      if (!ok) break;
+      fence_async_shared();
+      mbar_arrive(bar(C::kBarQFull));
+    }
+  } else {
     // -------------------------------------------------------------- softmax
     const int ti = (warp - 4) >> 2;
     const int wq = warp & 3;         // TMEM sub-partition = rows 32*wq ..
@@ -475,42 +589,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tl = tmem + ((uint32_t)(wq * 32) << 16);
     const uint32_t colS = col_s(ti), colO = col_o(ti);
     const float sl2 = a.scale_log2;
+    const int g_magic = (65535 + G) / G;  // r / G = r * g_magic >> 16 for r < 256, G <= 128
     const int tok = row / G, head = row - tok * G;
-    // (m, l) of both warpgroups; in the second row tile's place, which has no
-    // use while they share one.
-    float2* ml = reinterpret_cast<float2*>(smem + C::kOffQ + C::kTileBytes);
-    uint32_t s_ph = 0, o_ph[2] = {0, 0}, kv = 0;
+    float2* ml = reinterpret_cast<float2*>(smem + C::kOffSums);  // of both warpgroups
+    uint32_t s_ph = 0, o_ph[2] = {0, 0}, entries = 0;
     bool ok = true;
     auto wwait = [&](uint32_t bar_addr, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_wait(bar_addr, parity, wc));
+      return __all_sync(0xffffffffu, mbar_wait_short(bar_addr, parity, wc));
     };
-    for (int k = 0; ok && walk.next(a, tpt); ++k) {
-      const bool pair = p.pair;
+    bool more = walk.next(a, span);
+    for (int k = 0; ok && more; ++k) {
+      const int item_tok = p.m * span;
+      const bool pair = kPair && p.x.n - item_tok > tpt;
       const int nt = p.t1 - p.t0;
-      const int item_tok = p.m * 2 * tpt;
-      const int mine = (pair ? ti * tpt : 0) + tok;  // token within the item
-      const int token = item_tok + mine;             // within the request
+      const int token = item_tok + (pair ? ti * tpt : 0) + tok;  // within the request
       const bool live = tok < tpt && token < p.x.n;
-      // Q rows: of the shared tile the warpgroups load half the columns each.
-      if (live) {
-        const uint4* src = reinterpret_cast<const uint4*>(
-            static_cast<const uint16_t*>(a.q) + (p.x.q0 + token) * a.q_stride + (p.g * G + head) * D);
-        uint8_t* dst = smem + C::kOffQ + (pair ? ti * C::kTileBytes : 0) + row * 128;
-        constexpr int kHalf = D / 16;
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          if (!pair && c / kHalf != ti) continue;
-          *reinterpret_cast<uint4*>(dst + (c >> 3) * kBoxBytes + (((c & 7) ^ (row & 7)) << 4)) =
-              src[c];
-        }
-      }
       unsigned long long bits = 0;
       if (!chain && live) {
         bits = a.tree[p.x.q0 + token];
         if (p.x.n < 64) bits &= (1ull << p.x.n) - 1;
       }
-      fence_async_shared();
-      mbar_arrive(bar(C::kBarQ));
       const bool warp_live = __any_sync(0xffffffffu, live);
       float m = -INFINITY, l = 0.f;
       const int step = pair ? 1 : 2;
@@ -577,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (rescale && x >= step) {
             // O <- O * 2^(m_old - m_new).  This tile's S barrier also covers the
             // previous product into O; the next is issued after the P barrier.
-#pragma unroll
+#pragma unroll 1
             for (int cc = 0; cc < D / 32; ++cc) {
               uint32_t o[32];
               tmem_ld32(tl + colO + cc * 32, o);
@@ -592,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (valid < kT && (!pair || ti == 0)) {
           // V rows behind the last position.  With two row tiles the first
           // one's warpgroup clears them: the second's product is issued later.
-          const uint32_t n = 2 * (kv + x) + 1;
+          const uint32_t n = entries + 2 * x + 1;
           if (!wwait(bar(C::kBarFull + n % kSlots), (n / kSlots) & 1)) {
             ok = false;
             break;
@@ -616,27 +714,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       // o = (f0 O0 + f1 O1) / L: of one row tile each warpgroup joins and
       // writes half the columns, of two its own rows.
       const bool two = !pair && nt > 1;  // both warpgroups hold a part of the row
+      const Piece q = p;
+      entries += 2 * nt;
+      more = walk.next(a, span);  // the next piece's lengths load meanwhile
       float f0, f1 = 0.f, L, M;
+      if (!pair) ml[ti * kT + row] = make_float2(m, l);
+      mbar_arrive(bar(C::kBarMeet + 0));
+      // Both warpgroups wait for every product, so that both count the phases.
+      ok = wwait(bar(C::kBarMeet + 0), k & 1) && wwait(bar(C::kBarO + 0), o_ph[0]) &&
+           (nt == 1 && !pair || wwait(bar(C::kBarO + 1), o_ph[1]));
+      if (!ok) break;
+      o_ph[0] ^= 1;
+      if (nt > 1 || pair) o_ph[1] ^= 1;
       if (!pair) {
-        ml[ti * kT + row] = make_float2(m, l);
-        mbar_arrive(bar(C::kBarMeet + 0));
-        ok = wwait(bar(C::kBarMeet + 0), k & 1) && wwait(bar(C::kBarO + 0), o_ph[0]) &&
-             (!two || wwait(bar(C::kBarO + 1), o_ph[1]));
-        if (!ok) break;
-        o_ph[0] ^= 1;
-        if (two) o_ph[1] ^= 1;
         const float2 x0 = ml[row], x1 = ml[kT + row];
         M = fmaxf(x0.x, x1.x);
         f0 = x0.x == -INFINITY ? 0.f : ex2(x0.x - M);
         f1 = x1.x == -INFINITY ? 0.f : ex2(x1.x - M);
         L = x0.y * f0 + x1.y * f1;
       } else {
-        mbar_arrive(bar(C::kBarMeet + 0));  // keeps the barriers' phases in step with the pieces
-        // Each warpgroup waits for both products, so that both count the phases.
-        ok = wwait(bar(C::kBarO + 0), o_ph[0]) && wwait(bar(C::kBarO + 1), o_ph[1]);
-        if (!ok) break;
-        o_ph[0] ^= 1;
-        o_ph[1] ^= 1;
         M = m;
         L = l;
         f0 = 1.f;
@@ -646,15 +742,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       f0 *= inv;
       f1 *= inv;
       const float lse2 = L == 0.f ? -INFINITY : M + log2f(L);
-      const bool whole = p.t0 == 0 && p.t1 == p.tiles;
-      const int which = p.t0 == 0 ? 1 : 0;
-      const int64_t place = place_of(w, cta, which, (pair ? ti * tpt * G : 0) + row);
-      const int64_t out_row = (int64_t)(p.x.q0 + token) * a.H + p.g * G + head;
-      const int c_lo = pair ? 0 : ti * (D / 2), c_hi = pair ? D : c_lo + D / 2;
+      const bool whole = q.t0 == 0 && q.t1 == q.tiles;
+      const int which = q.t0 == 0 ? 1 : 0;
+      const int tile_tok = pair ? ti * tpt : 0;  // first token of the tile within the item
+      const int64_t place = place_of(w, cta, which, tile_tok * G);
       if (warp_live) {
+        // After the transpose this lane writes a piece of each of the quad's
+        // four rows; where, and whether they are live.
+        int64_t at[4];
+        bool writes[4];
 #pragma unroll
-        for (int cc = 0; cc < D / 32; ++cc) {
-          if (cc * 32 < c_lo || cc * 32 >= c_hi) continue;
+        for (int j = 0; j < 4; ++j) {
+          const int r = row - (lane & 3) + j, t = (r * g_magic) >> 16;
+          const int64_t to = whole ? (int64_t)(q.x.q0 + item_tok + tile_tok + t) * a.H + q.g * G +
+                                         (r - t * G)
+                                   : place + r;
+          at[j] = to * D;
+          writes[j] = t < tpt && item_tok + tile_tok + t < q.x.n;
+        }
+        const int cc_lo = pair ? 0 : ti * (D / 64), cc_hi = pair ? D / 32 : cc_lo + D / 64;
+#pragma unroll 1
+        for (int cc = cc_lo; cc < cc_hi; ++cc) {
           uint32_t o[32];
           tmem_ld32(tl + (pair ? colO : col_o(0)) + cc * 32, o);
           tmem_wait_ld_regs(o);
@@ -668,48 +776,60 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 32; ++j)
               o[j] = __float_as_uint(fmaf(__uint_as_float(u[j]), f1, __uint_as_float(o[j])));
           }
-          if (live && whole) {
-            uint4* op = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + out_row * D + cc * 32);
+          if (whole) {
+            uint4 v[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              uint4 v;
-              v.x = pack16<kBf16>(__uint_as_float(o[8 * j + 0]), __uint_as_float(o[8 * j + 1]));
-              v.y = pack16<kBf16>(__uint_as_float(o[8 * j + 2]), __uint_as_float(o[8 * j + 3]));
-              v.z = pack16<kBf16>(__uint_as_float(o[8 * j + 4]), __uint_as_float(o[8 * j + 5]));
-              v.w = pack16<kBf16>(__uint_as_float(o[8 * j + 6]), __uint_as_float(o[8 * j + 7]));
-              op[j] = v;
+              v[j].x = pack16<kBf16>(__uint_as_float(o[8 * j + 0]), __uint_as_float(o[8 * j + 1]));
+              v[j].y = pack16<kBf16>(__uint_as_float(o[8 * j + 2]), __uint_as_float(o[8 * j + 3]));
+              v[j].z = pack16<kBf16>(__uint_as_float(o[8 * j + 4]), __uint_as_float(o[8 * j + 5]));
+              v[j].w = pack16<kBf16>(__uint_as_float(o[8 * j + 6]), __uint_as_float(o[8 * j + 7]));
             }
-          } else if (live) {
-            uint4* op = reinterpret_cast<uint4*>(w.o + place * D + cc * 32);
+            quad_transpose(v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              op[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            for (int j = 0; j < 4; ++j)
+              if (writes[j])
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at[j] + cc * 32 +
+                                          (lane & 3) * 8) = v[j];
+          } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint4 v[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int b = h * 16 + j * 4;
+                v[j] = make_uint4(o[b], o[b + 1], o[b + 2], o[b + 3]);
+              }
+              quad_transpose(v);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (writes[j])
+                  *reinterpret_cast<uint4*>(w.o + at[j] + cc * 32 + h * 16 + (lane & 3) * 4) = v[j];
+            }
           }
           __syncwarp();
         }
       }
       if (live && (pair || ti == 0)) {
         if (whole)
-          a.lse[(int64_t)(p.g * G + head) * a.N + p.x.q0 + token] =
+          a.lse[(int64_t)(q.g * G + head) * a.N + q.x.q0 + token] =
               L == 0.f ? -INFINITY : lse2 * kLn2;
         else
-          w.lse[place] = lse2;
+          w.lse[place + row] = lse2;
       }
-      if (!whole && p.t0 == 0 && warp == 4 && lane == 0) {
+      if (!whole && q.t0 == 0 && warp == 4 && lane == 0) {
         Cut c;
-        c.last = part_of(p.at + p.tiles - 1, T, n_ctas);
-        c.token0 = p.x.q0 + item_tok;
-        c.n = min(p.x.n - item_tok, 2 * tpt);
-        c.g = p.g;
+        c.last = cuts.of(q.item_at + kItemCost + q.tiles - 1);
+        c.token0 = q.x.q0 + item_tok;
+        c.n = min(q.x.n - item_tok, span);
+        c.g = q.g;
         w.cuts[cta] = c;
       }
-      // The next piece overwrites Q, (m, l) and O: not before both are through.
+      // The next piece overwrites (m, l) and O: not before both are through.
       tc_fence_before();
       mbar_arrive(bar(C::kBarMeet + 1));
       ok = wwait(bar(C::kBarMeet + 1), k & 1);
       tc_fence_after();
-      kv += nt;
-      walk.done();
     }
   }
 
@@ -723,16 +843,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------------------
 // Joins the partials of each item that was cut: with L = log2 sum_c 2^lse_c,
-// o = sum_c 2^(lse_c - L) o_c.  Block (c, y) takes rows y, y + gridDim.y, ... of
-// the item begun by CTA c; its warps share the row's partials and join theirs
-// through shared memory.
+// o = sum_c 2^(lse_c - L) o_c.  Blocks (c, y) take the rows of the item begun by
+// CTA c.  Up to kFew partials a warp takes a row, eight partials' loads at a
+// time; more (one long context spread over the SMs) are shared by the block's
+// warps and joined through shared memory.
 // ---------------------------------------------------------------------------
-constexpr int kMergeWarps = 8;
+constexpr int kMergeWarps = 4;
+constexpr int kMergeRows = 16;  // blocks of an item at most
+constexpr int kFew = 16;
 
 template <bool kBf16, int D>
 __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const TreeArgs a,
                                                                       const Partials w) {
-  constexpr int E = D / 32;
+  constexpr int E = D / 32, U = 8;
   __shared__ float s_o[kMergeWarps][D], s_m[kMergeWarps], s_l[kMergeWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.H / a.Hkv;
@@ -740,52 +863,92 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const Tree
   const int c0 = blockIdx.x;
   const Cut cut = w.cuts[c0];
   if (cut.last <= c0) return;
-  const int parts = cut.last - c0 + 1;
-  for (int row = blockIdx.y; row < cut.n * G; row += gridDim.y) {
+  const int parts = cut.last - c0 + 1, rows = cut.n * G;
+  const bool few = parts <= kFew;
+  const int step = few ? 1 : kMergeWarps;
+  for (int base = blockIdx.y * (few ? kMergeWarps : 1); base < rows;
+       base += gridDim.y * (few ? kMergeWarps : 1)) {
+    const int row = base + (few ? warp : 0);
     float m = -INFINITY, l = 0.f, o[E] = {};
-    for (int i = warp; i < parts; i += kMergeWarps) {
-      const int64_t at = place_of(w, c0 + i, i == 0 ? 1 : 0, row);
-      const float x = w.lse[at];
-      float v[E];
+    if (row < rows) {
+      for (int i0 = few ? 0 : warp; i0 < parts; i0 += U * step) {
+        float x[U], v[U][E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = w.o[at * D + e * 32 + lane];
-      const float mn = fmaxf(m, x);
-      const float f = m == -INFINITY ? 0.f : ex2(m - mn), g = x == -INFINITY ? 0.f : ex2(x - mn);
-      l = l * f + g;
+        for (int u = 0; u < U; ++u) {
+          const int i = i0 + u * step;
+          x[u] = -INFINITY;
+          if (i < parts) {
+            const int64_t at = place_of(w, c0 + i, i == 0 ? 1 : 0, row);
+            x[u] = w.lse[at];
+            if constexpr (E == 4) {
+              const float4 f = reinterpret_cast<const float4*>(w.o + at * D)[lane];
+              v[u][0] = f.x;
+              v[u][1] = f.y;
+              v[u][2] = f.z;
+              v[u][3] = f.w;
+            } else {
+              const float2 f = reinterpret_cast<const float2*>(w.o + at * D)[lane];
+              v[u][0] = f.x;
+              v[u][1] = f.y;
+            }
+          }
+        }
+        float mn = m;
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = o[e] * f + v[e] * g;
-      m = mn;
+        for (int u = 0; u < U; ++u) mn = fmaxf(mn, x[u]);
+        const float f = m == -INFINITY ? 0.f : ex2(m - mn);
+        l *= f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] *= f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (i0 + u * step >= parts) continue;
+          const float g = x[u] == -INFINITY ? 0.f : ex2(x[u] - mn);
+          l += g;
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] = fmaf(v[u][e], g, o[e]);
+        }
+        m = mn;
+      }
     }
+    if (!few) {
+      __syncthreads();  // the row before is through
 #pragma unroll
-    for (int e = 0; e < E; ++e) s_o[warp][e * 32 + lane] = o[e];
-    if (lane == 0) {
-      s_m[warp] = m;
-      s_l[warp] = l;
-    }
-    __syncthreads();
-    float M = -INFINITY;
-    for (int i = 0; i < kMergeWarps; ++i) M = fmaxf(M, s_m[i]);
-    float L = 0.f, f[kMergeWarps];
+      for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
+      if (lane == 0) {
+        s_m[warp] = m;
+        s_l[warp] = l;
+      }
+      __syncthreads();
+      if (warp != 0) continue;
+      float mn = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kMergeWarps; ++i) {
-      f[i] = s_m[i] == -INFINITY ? 0.f : ex2(s_m[i] - M);
-      L += s_l[i] * f[i];
-    }
-    const int token = cut.token0 + row / G, head = cut.g * G + row % G;
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    if (threadIdx.x < D / 2) {
-      float x = 0.f, y = 0.f;
+      for (int i = 0; i < kMergeWarps; ++i) mn = fmaxf(mn, s_m[i]);
+      l = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = 0.f;
 #pragma unroll
       for (int i = 0; i < kMergeWarps; ++i) {
-        x += s_o[i][2 * threadIdx.x] * f[i];
-        y += s_o[i][2 * threadIdx.x + 1] * f[i];
+        const float f = s_m[i] == -INFINITY ? 0.f : ex2(s_m[i] - mn);
+        l += s_l[i] * f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(s_o[i][lane * E + e], f, o[e]);
       }
-      reinterpret_cast<uint32_t*>(a.out)[((int64_t)token * a.H + head) * (D / 2) + threadIdx.x] =
-          pack16<kBf16>(x * inv, y * inv);
+      m = mn;
     }
-    if (threadIdx.x == 0)
-      a.lse[(int64_t)head * a.N + token] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
-    __syncthreads();
+    if (row < rows) {
+      const int token = cut.token0 + row / G, head = cut.g * G + row % G;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      uint32_t* out = static_cast<uint32_t*>(a.out) + ((int64_t)token * a.H + head) * (D / 2) +
+                      lane * (E / 2);
+      if constexpr (E == 4)
+        *reinterpret_cast<uint2*>(out) = make_uint2(pack16<kBf16>(o[0] * inv, o[1] * inv),
+                                                    pack16<kBf16>(o[2] * inv, o[3] * inv));
+      else
+        *out = pack16<kBf16>(o[0] * inv, o[1] * inv);
+      if (lane == 0)
+        a.lse[(int64_t)head * a.N + token] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    }
   }
 }
 
@@ -806,13 +969,18 @@ bool make_map(CUtensorMap* m, const void* ptr, bool bf16, const CacheShape& c, i
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// Two row tiles an item where the requests have more than a tile's rows (128)
+// on the average; each request is right either way, one row tile reads a large
+// request's keys once for each 128 rows.
+bool use_pairs(int R, int N, int G) { return (int64_t)N * G > (int64_t)R * kT; }
+
 // Rows of a place: an item's, at most two tiles of 128 / G tokens.
 int place_rows(int N, int G) {
   const int64_t most = 2 * (int64_t)(kT / G) * G, have = (int64_t)N * G;
   return (int)(have < most ? have : most);
 }
 
-template <bool kBf16, int D>
+template <bool kBf16, int D, bool kPair>
 cudaError_t run(const TreeArgs& a, cudaStream_t stream) {
   const int G = a.H / a.Hkv;
   CUtensorMap mk, mv;
@@ -824,9 +992,9 @@ cudaError_t run(const TreeArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const int smem = Cfg<D>::kSmemBytes;
-  e = cudaFuncSetAttribute(tree_kernel<kBf16, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           smem);
+  const int smem = Cfg<D, kPair>::kSmemBytes;
+  static DeviceOnce allowed;
+  e = allowed.shared_memory(reinterpret_cast<const void*>(tree_kernel<kBf16, D, kPair>), dev, smem);
   if (e != cudaSuccess) return e;
   Partials w;
   w.rows = place_rows(a.N, G);
@@ -837,11 +1005,11 @@ cudaError_t run(const TreeArgs& a, cudaStream_t stream) {
   ws += align256((size_t)kMaxCtas * 2 * w.rows * sizeof(float));
   w.o = reinterpret_cast<float*>(ws);
   const int grid = sms < kMaxCtas ? sms : kMaxCtas;
-  tree_kernel<kBf16, D><<<grid, kThreads, smem, stream>>>(mk, mv, a, w);
+  tree_kernel<kBf16, D, kPair><<<grid, kThreads, smem, stream>>>(mk, mv, a, w);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, w.rows < 8 ? w.rows : 8);
+  cfg.gridDim = dim3(grid, w.rows < kMergeRows ? w.rows : kMergeRows);
   cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr;
@@ -862,8 +1030,13 @@ size_t tree_workspace_bytes(int N, int H, int Hkv, int D) {
 }
 
 cudaError_t launch_tree_attn(const TreeArgs& a, int dtype, cudaStream_t stream) {
-  if (dtype == CPATTN_BF16) return a.D == 128 ? run<true, 128>(a, stream) : run<true, 64>(a, stream);
-  return a.D == 128 ? run<false, 128>(a, stream) : run<false, 64>(a, stream);
+  const bool pair = use_pairs(a.R, a.N, a.H / a.Hkv);
+  if (dtype == CPATTN_BF16) {
+    if (a.D == 128) return pair ? run<true, 128, true>(a, stream) : run<true, 128, false>(a, stream);
+    return pair ? run<true, 64, true>(a, stream) : run<true, 64, false>(a, stream);
+  }
+  if (a.D == 128) return pair ? run<false, 128, true>(a, stream) : run<false, 128, false>(a, stream);
+  return pair ? run<false, 64, true>(a, stream) : run<false, 64, false>(a, stream);
 }
 
 }  // namespace cpattn

@@ -89,6 +89,27 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const W
   }
 }
 
+// The same wait for chains of short steps: the abort flag and the global timer,
+// whose reading takes longer than such a step, are looked at once in 64 polls.
+__device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, const WaitCtl& w) {
+  if (mbar_test(bar, parity)) return true;
+  uint64_t t0 = 0;
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_test(bar, parity)) return true;
+    if (*w.abort) return false;
+    const uint64_t t = global_timer();
+    if (t0 == 0) {
+      t0 = t;
+    } else if (t - t0 > w.limit_ns) {
+      *w.abort = 1;
+      atomicExch(w.err, 1);
+      return false;
+    }
+  }
+}
+
 // Same, without raising the abort flag: the bounded drain at teardown.
 __device__ __forceinline__ bool mbar_drain(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = global_timer();
@@ -315,6 +336,32 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   } else {
     __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&v);
+  }
+}
+
+// Transposes 4 x 4 16-byte pieces within each quad of lanes: v[j] of lane q
+// becomes what v[q] of the quad's lane j was.  A thread that holds 64
+// consecutive bytes of its own row then holds one piece of four rows, and the
+// quad writes each row's 64 bytes together (8 rows a warp store instead of
+// 32, each of which costs the load/store unit a cycle).
+__device__ __forceinline__ void quad_transpose(uint4 (&v)[4]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int b = 1; b <= 2; b <<= 1) {
+    const bool up = lane & b;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j & b) continue;
+      uint4 x = up ? v[j] : v[j | b];
+      x.x = __shfl_xor_sync(0xffffffffu, x.x, b);
+      x.y = __shfl_xor_sync(0xffffffffu, x.y, b);
+      x.z = __shfl_xor_sync(0xffffffffu, x.z, b);
+      x.w = __shfl_xor_sync(0xffffffffu, x.w, b);
+      if (up)
+        v[j] = x;
+      else
+        v[j | b] = x;
+    }
   }
 }
 
