@@ -75,7 +75,7 @@ SIGNATURES = {
     "cpattn_tree_attn_workspace_bytes": (_sz, [_i] * 4),
     "cpattn_tree_attn": (_i, [_vp, _i64, _vp, _vp, _i64, _i, _i64, _i64, _i64, _vp, _i, _i64]
                          + [_vp] * 5 + [_i] * 6 + [_f, _vp, _sz, _vp]),
-    "cpattn_prompt_attn_workspace_bytes": (_sz, [_i] * 2),
+    "cpattn_prompt_attn_workspace_bytes": (_sz, [_i] * 4),
     "cpattn_prompt_attn": (_i, [_vp, _i64] * 3 + [_vp] * 4 + [_i] * 8 + [_f, _vp, _sz, _vp]),
     "cpattn_tile_counts": (_i, [_i64, _i, _i, _i, _i64, _vp, _vp]),
     "cpattn_device_status": (_i, [_vp]),
@@ -867,7 +867,7 @@ def tree_attention(q, k_cache, v_cache, block_table, ctx_lens, cu, tree=None, sc
 def prompt_attention_workspace(q, cu_q):
     """Scratch for prompt_attention calls with q and offsets of this shape."""
     return _workspace(None, q.device, lib().cpattn_prompt_attn_workspace_bytes, cu_q.numel() - 1,
-                      q.shape[0])
+                      *q.shape)
 
 
 def prompt_attention(q, k, v, cu_q, cu_k=None, causal=True, scale=None, out=None, lse=None,
@@ -890,7 +890,7 @@ def prompt_attention(q, k, v, cu_q, cu_k=None, causal=True, scale=None, out=None
     _on(dev, "cu_q", cu_q, torch.int32)
     _on(dev, "cu_k", cu_k, torch.int32, R + 1)
     out, lse = _answer_outputs(q, Nq, H, D, out, lse, dev)
-    ws = _workspace(workspace, dev, lib().cpattn_prompt_attn_workspace_bytes, R, Nq)
+    ws = _workspace(workspace, dev, lib().cpattn_prompt_attn_workspace_bytes, R, Nq, H, D)
     _launch("cpattn_prompt_attn", dev, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
             cu_q.data_ptr(), cu_k.data_ptr(), out.data_ptr(), lse.data_ptr(), R, Nq, Nk, H, Hkv, D,
             1 if causal else 0, code, _scale(scale), ws.data_ptr(), ws.numel())

@@ -81,6 +81,14 @@ bool encode_tiled(CUtensorMap* m, bool bf16, int rank, const void* ptr, const cu
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool rows_map(CUtensorMap* m, const void* ptr, bool bf16, int heads, int D, int64_t stride,
+              int64_t rows) {
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64, 1, (cuuint32_t)kTcTile};
+  return encode_tiled(m, bf16, 3, ptr, dims, strides, box);
+}
+
 }  // namespace cpattn
 
 extern "C" {
@@ -181,12 +189,15 @@ int cpattn_tree_attn(const void* q, int64_t q_stride, const void* k_cache, const
   a.scale_log2 = a.scale * 1.4426950408889634f;
   a.workspace = workspace;
   a.err = err;
+  a.cu_k = nullptr;
+  a.k_stride = a.v_stride = 0;
+  a.Nk = a.causal = 0;
   return status(launch_tree_attn(a, dtype, (cudaStream_t)stream));
 }
 
-size_t cpattn_prompt_attn_workspace_bytes(int R, int Nq) {
-  if (R < 0 || Nq < 0) return 0;
-  return prompt_workspace_bytes(R, Nq);
+size_t cpattn_prompt_attn_workspace_bytes(int R, int Nq, int H, int D) {
+  if (R < 0 || Nq < 0 || check_heads(H, H, D, CPATTN_BF16) != CPATTN_OK) return 0;
+  return prompt_workspace_bytes(R, Nq, H, D);
 }
 
 int cpattn_prompt_attn(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
@@ -207,7 +218,7 @@ int cpattn_prompt_attn(const void* q, int64_t q_stride, const void* k, int64_t k
     return CPATTN_ERR_INVALID_ARG;
   if (Nk > 0 && (!check_rows(k, k_stride, Hkv, D) || !check_rows(v, v_stride, Hkv, D)))
     return CPATTN_ERR_INVALID_ARG;
-  if (!workspace || !aligned(workspace, 256) || workspace_bytes < prompt_workspace_bytes(R, Nq))
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < prompt_workspace_bytes(R, Nq, H, D))
     return CPATTN_ERR_WORKSPACE;
   int* err = device_error_word();
   if (err == nullptr) return CPATTN_ERR_CUDA;

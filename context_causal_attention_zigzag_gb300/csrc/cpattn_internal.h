@@ -360,6 +360,12 @@ struct TreeArgs {
   float scale, scale_log2;
   void* workspace;
   int* err;
+  // Packed keys instead of a cache (cu_k not null): k_cache, v_cache are rows
+  // k_stride, v_stride apart, request r's are cu_k[r] .. cu_k[r + 1] - 1, and
+  // its new tokens stand at their end (causal) or see them all.
+  const int* cu_k;
+  int64_t k_stride, v_stride;
+  int Nk, causal;
 };
 
 struct PromptArgs {
@@ -409,11 +415,18 @@ struct DeviceOnce {
 bool encode_tiled(CUtensorMap* m, bool bf16, int rank, const void* ptr, const cuuint64_t* dims,
                   const cuuint64_t* strides, const cuuint32_t* box);
 
+// Rows of [heads, D], `stride` elements apart, as a 3-D tensor (d, head, row),
+// box (64, 1, 128).
+bool rows_map(CUtensorMap* m, const void* ptr, bool bf16, int heads, int D, int64_t stride,
+              int64_t rows);
+
 cudaError_t launch_page_tables(const TablesArgs& a, cudaStream_t stream);
 cudaError_t launch_cache_write(const CacheWriteArgs& a, cudaStream_t stream);
 size_t tree_workspace_bytes(int N, int H, int Hkv, int D);
+// The same for any Hkv that divides H.
+size_t line_workspace_bytes(int N, int H, int D);
 cudaError_t launch_tree_attn(const TreeArgs& a, int dtype, cudaStream_t stream);
-size_t prompt_workspace_bytes(int R, int Nq);
+size_t prompt_workspace_bytes(int R, int Nq, int H, int D);
 cudaError_t launch_prompt_attn(const PromptArgs& a, int dtype, cudaStream_t stream);
 
 // One CTA whose bounded mbarrier wait gives up after limit_ns (raising *err).

@@ -23,12 +23,16 @@
 // shared memory by the softmax threads before the product, since 0 * NaN is
 // NaN.  Only a sequence's last tile pays for that.
 //
-// Roles and barriers of a CTA (384 threads) as in the ring forward: warp 0
-// loads (Q pair once per item, K(j), V(j) in consecutive slots of one ring),
-// warp 1 owns TMEM and issues the products S_i = Q_i K^T (SS) and O_i += P_i V
-// (TS, P in TMEM over S), warps 4-7 and 8-11 are the softmax of tile 0 and 1,
-// one thread per row.  MMA order per key tile: PV0(j), S0(j+1), PV1(j),
-// S1(j+1).  The weights are rounded to the input type for the second product
+// Roles of a CTA (384 threads) as in the ring forward: warp 0 loads (Q tiles once
+// per item, K(j), V(j) in consecutive slots of one ring), warp 1 owns TMEM and
+// issues the products S_i = Q_i K^T (SS) and O_i += P_i V (TS, P in TMEM over
+// S), warps 4-7 and 8-11 are the softmax of tile 0 and 1, one thread per row.
+// MMA order per key tile: PV0(j), S0(j+1), PV1(j), S1(j+1), across items too, so
+// that the next item's scores are ready when the softmax leaves the epilogue.
+// (An epilogue in four warps of its own held the products up: at 512 threads
+// the issuing warp has too few registers for its descriptors, and the 16384-token
+// prompt went from 1.31 to 1.46 ms.)
+// The weights are rounded to the input type for the second product
 // (their sum is taken before rounding, in float32): the tensor cores take 16-bit
 // operands, and the rounding is as large as that of the output itself.
 #include <cuda.h>
@@ -180,8 +184,9 @@ __host__ __device__ constexpr uint32_t col_s(int i) { return 128u * (uint32_t)i;
 __host__ __device__ constexpr uint32_t col_o(int i) { return 256u + 128u * (uint32_t)i; }
 
 struct Work {
-  const Plan* plan;   // nullptr: one sequence, decoded in closed form
+  const Plan* plan;   // nullptr: one sequence, decoded in closed form, or direct
   const Block* list;
+  int direct;         // at most an item a CTA: each finds its own
   int rows;           // rows of a block: 128 (two heads an item) or 256 (two row tiles)
   int inner;          // items per block and kv head
 };
@@ -220,6 +225,43 @@ struct Items {
     rows = w.rows;
     inner = w.inner;
     list = w.plan != nullptr ? w.list : nullptr;
+    if (w.direct) {
+      // The warp sums the sequences' blocks, 32 at a time, up to its own.
+      const int lane = threadIdx.x & 31, per = Hkv * inner;
+      const int mine = (int)blockIdx.x / per, sub = (int)blockIdx.x - mine * per;
+      next_g = sub / inner;
+      next_sub = sub - next_g * inner;
+      next_ok = false;
+      k = 1;  // no further item
+      n_items = 0;
+      int before = 0;
+      for (int r0 = 0; r0 < a.R; r0 += 32) {
+        int n = 0, nb = 0;
+        if (r0 + lane < a.R) {
+          packed_rows(a.cu_q, r0 + lane, a.Nq, q0, n);
+          nb = (n + rows - 1) / rows;
+        }
+        int upto = nb;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int u = __shfl_up_sync(0xffffffffu, upto, d);
+          if (lane >= d) upto += u;
+        }
+        const int at = mine - before;
+        const uint32_t found = __ballot_sync(0xffffffffu, at >= upto - nb && at < upto);
+        if (found != 0) {
+          const int src = __ffs(found) - 1;
+          const int skip = __shfl_sync(0xffffffffu, upto - nb, src);
+          packed_rows(a.cu_q, r0 + src, a.Nq, q0, nq);
+          packed_rows(a.cu_k, r0 + src, a.Nk, k0, nk);
+          next_block = make_block(q0, nq, k0, nk, (at - skip) * rows);
+          next_ok = true;
+          return;
+        }
+        before += __shfl_sync(0xffffffffu, upto, 31);
+      }
+      return;
+    }
     if (w.plan != nullptr) {
       nblocks = w.plan->nblocks;
     } else {
@@ -292,10 +334,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   if (w.plan != nullptr) {
     wait_prior_grid();  // the plan
-  } else if (blockIdx.x == 0 && threadIdx.x == 0) {
+  } else if (blockIdx.x == 0) {
     int x, y;
-    if (!packed_rows(a.cu_q, 0, a.Nq, x, y) || !packed_rows(a.cu_k, 0, a.Nk, x, y))
-      atomicExch(a.err, kErrBadTables);
+    for (int r = threadIdx.x; r < a.R; r += kThreads)
+      if (!packed_rows(a.cu_q, r, a.Nq, x, y) || !packed_rows(a.cu_k, r, a.Nk, x, y))
+        atomicExch(a.err, kErrBadTables);
   }
 
   Items items;
@@ -312,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
     }
-    uint32_t seq = 0, q_armed[2] = {0, 0}, armed[kSlots] = {0};
+    uint32_t seq = 0, q_armed[2] = {0, 0};  // ring entries and Q tiles asked for
     bool ok = true;
     items.init(a, w);
     while (ok && items.next(b, g, h0)) {
@@ -334,13 +377,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (int m = 0; ok && m < nt; ++m) {
         for (int which = 0; which < 2; ++which) {  // K(m), then V(m)
-          const uint32_t n = seq++;
+          const uint32_t n = seq;
           const int sl = n % kSlots;
           if (!wwait(bar(C::kBarEmpty + sl), ((n / kSlots) & 1) ^ 1)) {
             ok = false;
             break;
           }
-          ++armed[sl];
+          ++seq;
           if (leader) {
             mbar_arrive_expect_tx(bar(C::kBarFull + sl), C::kTileBytes);
             for (int half = 0; half < C::kHalves; ++half)
@@ -354,8 +397,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Let the copies already issued land before the CTA exits.
       for (int i = 0; i < 2; ++i)
         if (q_armed[i]) mbar_drain(bar(C::kBarQFull + i), (q_armed[i] - 1) & 1);
-      for (int s = 0; s < kSlots; ++s)
-        if (armed[s]) mbar_drain(bar(C::kBarFull + s), (armed[s] - 1) & 1);
+      for (uint32_t n = seq > (uint32_t)kSlots ? seq - kSlots : 0; n < seq; ++n)
+        mbar_drain(bar(C::kBarFull + n % kSlots), (n / kSlots) & 1);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA
@@ -678,44 +721,52 @@ __global__ void __launch_bounds__(kThreads, 1)
 // host side
 // ---------------------------------------------------------------------------
 
-// Rows of [heads, D], `stride` elements apart, as a 3-D tensor (d, head, row),
-// box (64, 1, 128) with 128-byte swizzle.
-bool make_map(CUtensorMap* m, const void* ptr, bool bf16, int heads, int D, int64_t stride,
-              int64_t rows) {
-  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows};
-  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
-  cuuint32_t box[3] = {64, 1, (cuuint32_t)kT};
-  return encode_tiled(m, bf16, 3, ptr, dims, strides, box);
-}
-
 // Blocks that the plan may list: a sequence's last block of `rows` may be short.
 int64_t most_blocks(int R, int Nq) { return (int64_t)Nq / kT + R; }
 
+// How a call is done, from its means (the lengths themselves are on the device).
+//  kDirect: at most an item a CTA; each CTA finds its own, nothing is planned.
+//  kLine: few rows and many keys a sequence; the keys of an item are shared
+//    among CTAs and a kv head's query heads share a row tile (k_tree_tc.cu).
+//  kSorted: the rest.
+// Measured (us, H = 32, Hkv = 8, D = 128; direct or sorted / line), for sequences
+// of nq queries behind 1 to n keys:
+//   1 x   1, n 1000: 10.8 / 12.8    4 x  1, n 1000: 19.0 / 14.2   16 x  1, n 8000: 99 / 54
+//   1 x   1, n 8000: 20.2 / 13.7    4 x 32, n 1000: 18.6 / 18.3   16 x 32, n    1: 17.6 / 15.0
+//   4 x 128, n 8000: 82.5 / 57.5    4 x 64, n 1000: 18.5 / 25.1   16 x 64, n 1000: 29.6 / 42.9
+enum Way { kDirect, kLine, kSorted };
+
+Way way(const PromptArgs& a, int sms) {
+  if (a.Nk == 0) return kSorted;
+  const int G = a.H / a.Hkv;
+  const int64_t items = ((int64_t)a.Nq / kT + a.R) * (G % 2 == 0 ? a.H / 2 : a.H);
+  const int64_t rows = (int64_t)a.Nq * G / a.R, keys = a.Nk / a.R;
+  if (rows <= kT ? keys > 512 || items > sms : rows <= 8 * kT && keys >= 2048 && items <= sms)
+    return kLine;
+  return items <= sms ? kDirect : kSorted;
+}
+
 template <bool kBf16, int D>
-cudaError_t run(const PromptArgs& a, cudaStream_t stream) {
+cudaError_t run(const PromptArgs& a, Way by, int dev, int sms, cudaStream_t stream) {
   const int grp = a.H / a.Hkv;
   Work w;
   w.rows = grp % 2 == 0 ? kT : 2 * kT;
   w.inner = grp % 2 == 0 ? grp / 2 : grp;
   w.plan = nullptr;
   w.list = nullptr;
+  w.direct = 0;
   CUtensorMap mq, mk, mv;
   // No keys at all: every item has no tiles, nothing is read through the maps.
   const bool keys = a.Nk > 0;
-  if (!make_map(&mq, a.q, kBf16, a.H, D, a.q_stride, a.Nq) ||
-      !make_map(&mk, keys ? a.k : a.q, kBf16, keys ? a.Hkv : a.H, D, keys ? a.k_stride : a.q_stride,
+  if (!rows_map(&mq, a.q, kBf16, a.H, D, a.q_stride, a.Nq) ||
+      !rows_map(&mk, keys ? a.k : a.q, kBf16, keys ? a.Hkv : a.H, D, keys ? a.k_stride : a.q_stride,
                 keys ? a.Nk : a.Nq) ||
-      !make_map(&mv, keys ? a.v : a.q, kBf16, keys ? a.Hkv : a.H, D, keys ? a.v_stride : a.q_stride,
+      !rows_map(&mv, keys ? a.v : a.q, kBf16, keys ? a.Hkv : a.H, D, keys ? a.v_stride : a.q_stride,
                 keys ? a.Nk : a.Nq))
     return cudaErrorInvalidValue;
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
   const int smem = Cfg<D>::kSmemBytes;
   static DeviceOnce allowed;
-  e = allowed.shared_memory(reinterpret_cast<const void*>(prompt_kernel<kBf16, D>), dev, smem);
+  cudaError_t e = allowed.shared_memory(reinterpret_cast<const void*>(prompt_kernel<kBf16, D>), dev, smem);
   if (e != cudaSuccess) return e;
   const int64_t most = (a.Nq / w.rows + (int64_t)a.R) * a.Hkv * w.inner;
   cudaLaunchConfig_t cfg = {};
@@ -724,7 +775,9 @@ cudaError_t run(const PromptArgs& a, cudaStream_t stream) {
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr;
-  if (a.R > 1) {
+  if (by == kDirect) {
+    w.direct = 1;
+  } else if (a.R > 1) {
     // The plan goes first; this kernel sets itself up meanwhile.
     Plan* plan = static_cast<Plan*>(a.workspace);
     Block* list = reinterpret_cast<Block*>(plan + 1);
@@ -744,13 +797,49 @@ cudaError_t run(const PromptArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-size_t prompt_workspace_bytes(int R, int Nq) {
-  return sizeof(Plan) + (size_t)most_blocks(R, Nq) * sizeof(Block);
+size_t prompt_workspace_bytes(int R, int Nq, int H, int D) {
+  const size_t plan = sizeof(Plan) + (size_t)most_blocks(R, Nq) * sizeof(Block);
+  const size_t line = line_workspace_bytes(Nq, H, D);
+  return plan > line ? plan : line;
 }
 
 cudaError_t launch_prompt_attn(const PromptArgs& a, int dtype, cudaStream_t stream) {
-  if (dtype == CPATTN_BF16) return a.D == 128 ? run<true, 128>(a, stream) : run<true, 64>(a, stream);
-  return a.D == 128 ? run<false, 128>(a, stream) : run<false, 64>(a, stream);
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const Way by = way(a, sms);
+  if (by == kLine) {
+    TreeArgs t = {};
+    t.q = a.q;
+    t.q_stride = a.q_stride;
+    t.k_cache = a.k;
+    t.v_cache = a.v;
+    t.cu = a.cu_q;
+    t.out = a.out;
+    t.lse = a.lse;
+    t.R = a.R;
+    t.N = a.Nq;
+    t.H = a.H;
+    t.Hkv = a.Hkv;
+    t.D = a.D;
+    t.scale = a.scale;
+    t.scale_log2 = a.scale_log2;
+    t.workspace = a.workspace;
+    t.err = a.err;
+    t.cu_k = a.cu_k;
+    t.k_stride = a.k_stride;
+    t.v_stride = a.v_stride;
+    t.Nk = a.Nk;
+    t.causal = a.causal;
+    return launch_tree_attn(t, dtype, stream);
+  }
+  if (dtype == CPATTN_BF16)
+    return a.D == 128 ? run<true, 128>(a, by, dev, sms, stream)
+                      : run<true, 64>(a, by, dev, sms, stream);
+  return a.D == 128 ? run<false, 128>(a, by, dev, sms, stream)
+                    : run<false, 64>(a, by, dev, sms, stream);
 }
 
 }  // namespace cpattn

@@ -34,7 +34,7 @@
 // with weight 0, are zeroed in shared memory first (0 * NaN is NaN).  Pages
 // that lie wholly behind it are not read.
 //
-// CTA = 384 threads: warp 0 loads K and V, warps 2 and 3 Q, warp 1 owns TMEM and
+// CTA = 384 threads: warp 0 loads K and V, warp 2 Q, warp 1 owns TMEM and
 // issues the products S_i = Q_i K^T (SS) and O_i += P_i V (TS, P over S in
 // TMEM), warps 4-7 and 8-11 are the warpgroups, one thread per row.  TMEM: S0
 // [0,128) S1 [128,256) O0 [256,384) O1 [384,512).
@@ -99,17 +99,25 @@ __host__ __device__ constexpr uint32_t col_o(int i) { return 256u + 128u * (uint
 // What one request asks for, held to the buffers whatever its lengths say.
 struct Req {
   int q0, n;   // its rows of q
-  int ctx;     // positions before them
+  int ctx;     // its new token t sees the positions below ctx + t + 1 (below ctx: not causal)
   int total;   // positions in all
+  int k0;      // packed keys: the row of position 0
 };
 
+template <bool kPaged>
 __device__ __forceinline__ bool load_req(const TreeArgs& a, int r, Req& x) {
   bool ok = packed_rows(a.cu, r, a.N, x.q0, x.n);
-  const int ctx = a.ctx[r];
-  const int cap = a.width * a.cache.page_size;
-  x.ctx = ctx < 0 ? 0 : (ctx > cap ? cap : ctx);
-  ok = ok && ctx >= 0 && (long long)ctx + x.n <= cap && (a.tree == nullptr || x.n <= 64);
-  x.total = (int)((long long)x.ctx + x.n < cap ? (long long)x.ctx + x.n : cap);
+  if constexpr (kPaged) {
+    const int ctx = a.ctx[r];
+    const int cap = a.width * a.cache.page_size;
+    x.ctx = ctx < 0 ? 0 : (ctx > cap ? cap : ctx);
+    ok = ok && ctx >= 0 && (long long)ctx + x.n <= cap && (a.tree == nullptr || x.n <= 64);
+    x.total = (int)((long long)x.ctx + x.n < cap ? (long long)x.ctx + x.n : cap);
+    x.k0 = 0;
+  } else {
+    ok &= packed_rows(a.cu_k, r, a.Nk, x.k0, x.total);
+    x.ctx = a.causal ? x.total - x.n : x.total;
+  }
   return ok;
 }
 
@@ -159,6 +167,7 @@ struct Piece {
 };
 
 // Walks the pieces of one CTA.
+template <bool kPaged>
 struct Walk {
   Piece p;
   long long left;  // of the CTA's part
@@ -199,7 +208,7 @@ struct Walk {
             p.g = 0;
             do {
               ++p.r;
-              load_req(a, p.r, p.x);
+              load_req<kPaged>(a, p.r, p.x);
             } while (p.x.n == 0);
             items = items_of(p.x, span);
           }
@@ -238,35 +247,33 @@ __host__ __device__ inline int64_t place_of(const Partials& w, int cta, int whic
   return ((int64_t)cta * 2 + which) * w.rows + row;
 }
 
-// The 128 columns that a row sees of the key tile at position k0, as a bit mask.
-// Positions below ctx are seen; of the new ones those in `bits` (bit j: the
-// j-th), or without a tree the first `upto` of them.
-__device__ __forceinline__ void seen_columns(uint32_t* vis, int k0, int ctx, bool chain,
-                                             unsigned long long bits, int upto) {
+// The 128 columns that a row sees of the key tile at position k0, as a bit mask:
+// the positions below `limit` and, of those from ctx on, the ones in `bits`.
+__device__ __forceinline__ void seen_columns(uint32_t* vis, int k0, int limit, int ctx,
+                                             unsigned long long bits) {
   typedef unsigned __int128 u128;
-  const u128 ones = ~(u128)0;
-  const int sf = (chain ? ctx + upto : ctx) - k0;  // columns below: seen
-  u128 v = sf >= kT ? ones : (sf <= 0 ? (u128)0 : (((u128)1 << sf) - 1));
-  if (!chain) {
-    if (sf >= 0 && sf < kT) v |= (u128)bits << sf;
-    if (sf < 0 && sf > -64) v |= (u128)(bits >> -sf);
-  }
+  const int lo = limit - k0, sf = ctx - k0;
+  u128 v = lo >= kT ? ~(u128)0 : (lo <= 0 ? (u128)0 : (((u128)1 << lo) - 1));
+  if (sf >= 0 && sf < kT) v |= (u128)bits << sf;
+  if (sf < 0 && sf > -64) v |= (u128)(bits >> -sf);
   vis[0] = (uint32_t)v;
   vis[1] = (uint32_t)(v >> 32);
   vis[2] = (uint32_t)(v >> 64);
   vis[3] = (uint32_t)(v >> 96);
 }
 
-template <bool kBf16, int D, bool kPair>
+template <bool kBf16, int D, bool kPair, bool kPaged>
 __global__ void __launch_bounds__(kThreads, 1)
-    tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                const TreeArgs a, const Partials w) {
+    tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                const TreeArgs a, const Partials w, const int q_box) {
   using C = Cfg<D, kPair>;
   constexpr int kSlots = C::kSlots;
   constexpr uint32_t kIdescQK = idesc_f16(kBf16, 128, 128, false, false);
   constexpr uint32_t kIdescPV = idesc_f16(kBf16, 128, D, false, true);
   extern __shared__ __align__(1024) uint8_t smem[];
-  const uint32_t base = smem_u32(smem);
+  // The compiler is kept from folding the address into every operand descriptor:
+  // with the descriptors as immediates the issuing warp is 2 % slower.
+  const uint32_t base = opaque(smem_u32(smem));
   if (base & 1023u) {  // the swizzled tiles need it; shared memory has no room for slack
     if (threadIdx.x == 0) {
       atomicExch(a.err, kErrLaunch);
@@ -289,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   launch_dependents();  // the merge sets itself up; it waits for this kernel's end
   if (threadIdx.x == 0) {
-    mbar_init(bar(C::kBarQFull), 64);
+    mbar_init(bar(C::kBarQFull), 1);
     mbar_init(bar(C::kBarQEmpty), 1);
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(bar(C::kBarFull + s), 1);
@@ -318,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool bad = false;
   Req x;
   for (int r = r_lo; r < r_hi; ++r) {
-    bad |= !load_req(a, r, x);
+    bad |= !load_req<kPaged>(a, r, x);
     own += head_cost(x, span, chain) * a.Hkv;
   }
   if (bad && blockIdx.x == 0) atomicExch(a.err, kErrBadTables);
@@ -350,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       long long at = upto - own;
       int r = r_lo;
       while (per > 1) {
-        load_req(a, r, x);
+        load_req<kPaged>(a, r, x);
         const long long t = head_cost(x, span, chain) * a.Hkv;
         if (begin < at + t) break;
         at += t;
@@ -364,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) w.cuts[cta].last = -1;
   __syncthreads();
   const uint32_t tmem = *tmem_slot;
-  Walk walk;
+  Walk<kPaged> walk;
   walk.init(a, span, (int)sums[14], *reinterpret_cast<const Req*>(sums + 16), sums[13], begin,
             count);
   __syncthreads();  // the sums' place is used again
@@ -372,12 +379,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA
-    // All lanes hold page numbers (a window of 32 pages, the next one fetched
-    // ahead) and issue the copies of a tile between them.
-    const int P = a.cache.page_size;
-    const int box = P < kT ? P : kT;      // rows of a copy
-    const int ppt = kT / box;             // copies of a tile and 64 columns
-    const int npages = (int)a.cache.num_pages;
     if (lane == 0) {
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
@@ -385,54 +386,69 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wwait = [&](uint32_t bar_addr, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait_short(bar_addr, parity, wc));
     };
-    uint32_t seq = 0, armed = 0;
+    uint32_t seq = 0;  // ring entries asked for
     bool ok = true;
-    while (ok && walk.next(a, span)) {
-      const int* table = a.table + (int64_t)p.r * a.table_stride;
-      const int used = (p.x.total + P - 1) / P;  // pages that hold positions
-      auto page_at = [&](int i) { return i < used ? table[i] : 0; };
-      int win = p.t0 * kT / P;
-      int now = page_at(win + lane), ahead = page_at(win + 32 + lane);
-      const int c = lane / C::kHalves, half = lane % C::kHalves;
-      for (int t = p.t0; ok && t < p.t1; ++t) {
-        const int first = t * kT / P;
-        if (first + ppt > win + 32) {
-          // ppt divides 32 and the window began on a tile, so it ends on one.
-          win += 32;
-          now = ahead;
-          ahead = page_at(win + 32 + lane);
-        }
-        // Lane c * halves + half issues copy c of the tile, columns 64 * half.
-        const int id = __shfl_sync(0xffffffffu, now, (first - win + (c < ppt ? c : 0)) & 31);
-        const bool mine = c < ppt && first + c < used;
-        const bool good = mine && id >= 0 && id < npages;
-        if (mine && !good) atomicExch(a.err, kErrBadTables);
-        const uint32_t copies = __popc(__ballot_sync(0xffffffffu, good));
-        const int row = (t * kT) % P;  // within the page (0 for pages up to a tile)
+    // Fills the next two ring entries, K then V; `copy` issues this lane's share.
+    auto fill = [&](uint32_t bytes, auto copy) {
 #pragma unroll 1
-        for (int which = 0; ok && which < 2; ++which) {  // K(t), then V(t)
-          const uint32_t n = seq++;
-          const int sl = n % kSlots;
-          ok = wwait(bar(C::kBarEmpty + sl), ((n / kSlots) & 1) ^ 1);
-          if (!ok) break;
-          armed |= 1u << sl;
-          if (lane == 0) mbar_arrive_expect_tx(bar(C::kBarFull + sl), copies * box * 128);
-          __syncwarp();
-          if (good)
-            tma_load_4d(sRing + sl * C::kTileBytes + half * kBoxBytes + c * box * 128,
-                        which == 0 ? &tm_k : &tm_v, bar(C::kBarFull + sl), half * 64, p.g, row, id);
+      for (int which = 0; ok && which < 2; ++which) {
+        const uint32_t n = seq;
+        const int sl = n % kSlots;
+        ok = wwait(bar(C::kBarEmpty + sl), ((n / kSlots) & 1) ^ 1);
+        if (!ok) break;
+        ++seq;
+        if (lane == 0) mbar_arrive_expect_tx(bar(C::kBarFull + sl), bytes);
+        __syncwarp();
+        copy(which == 0 ? &tm_k : &tm_v, sRing + sl * C::kTileBytes, bar(C::kBarFull + sl));
+      }
+    };
+    if constexpr (!kPaged) {
+      while (ok && walk.next(a, span))
+        for (int t = p.t0; ok && t < p.t1; ++t)
+          fill(C::kTileBytes, [&](const CUtensorMap* map, uint32_t dst, uint32_t full) {
+            if (lane < C::kHalves)
+              tma_load_3d(dst + lane * kBoxBytes, map, full, lane * 64, p.g, p.x.k0 + t * kT);
+          });
+    } else {
+      // All lanes hold page numbers (a window of 32 pages, the next one fetched
+      // ahead) and issue the copies of a tile between them.
+      const int P = a.cache.page_size;
+      const int box = P < kT ? P : kT;      // rows of a copy
+      const int ppt = kT / box;             // copies of a tile and 64 columns
+      const int npages = (int)a.cache.num_pages;
+      while (ok && walk.next(a, span)) {
+        const int* table = a.table + (int64_t)p.r * a.table_stride;
+        const int used = (p.x.total + P - 1) / P;  // pages that hold positions
+        auto page_at = [&](int i) { return i < used ? table[i] : 0; };
+        int win = p.t0 * kT / P;
+        int now = page_at(win + lane), ahead = page_at(win + 32 + lane);
+        const int c = lane / C::kHalves, half = lane % C::kHalves;
+        for (int t = p.t0; ok && t < p.t1; ++t) {
+          const int first = t * kT / P;
+          if (first + ppt > win + 32) {
+            // ppt divides 32 and the window began on a tile, so it ends on one.
+            win += 32;
+            now = ahead;
+            ahead = page_at(win + 32 + lane);
+          }
+          // Lane c * halves + half issues copy c of the tile, columns 64 * half.
+          const int id = __shfl_sync(0xffffffffu, now, (first - win + (c < ppt ? c : 0)) & 31);
+          const bool mine = c < ppt && first + c < used;
+          const bool good = mine && id >= 0 && id < npages;
+          if (mine && !good) atomicExch(a.err, kErrBadTables);
+          const uint32_t copies = __popc(__ballot_sync(0xffffffffu, good));
+          const int row = (t * kT) % P;  // within the page (0 for pages up to a tile)
+          fill(copies * box * 128, [&](const CUtensorMap* map, uint32_t dst, uint32_t full) {
+            if (good)
+              tma_load_4d(dst + half * kBoxBytes + c * box * 128, map, full, half * 64, p.g, row, id);
+          });
         }
       }
     }
     if (!ok) {
       // Let the copies already issued land before the CTA exits.
-      // The last entry of slot s is the last one below seq that falls on it.
-      for (uint32_t s = 0; s < (uint32_t)kSlots; ++s) {
-        if (!(armed >> s & 1)) continue;
-        uint32_t n = seq - 1;
-        while (n % kSlots != s) --n;
-        mbar_drain(bar(C::kBarFull + s), (n / kSlots) & 1);
-      }
+      for (uint32_t n = seq > (uint32_t)kSlots ? seq - kSlots : 0; n < seq; ++n)
+        mbar_drain(bar(C::kBarFull + n % kSlots), (n / kSlots) & 1);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA
@@ -515,27 +531,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // Behind each product come the stream's next scores; at a piece's end they
     // are the next piece's first, which its softmax finds when it leaves the
-    // epilogue.  The walk begins behind an empty piece.  One copy of the code
-    // serves it all: what runs once a piece misses the instruction cache.
+    // epilogue.  The walk begins behind an empty piece.  The steps within a
+    // piece are unrolled; its end and the next one's begin share one copy of the
+    // code (what runs once a piece misses the instruction cache).
     bool more = next_run(nxt);
     while (ok && (cur.nt > 0 || more)) {
-      const int steps = cur.steps(0);
-      int s = steps > 0 ? 0 : -1;
-      do {
-        const bool last = s + 1 >= steps;
-        const Run u = last ? nxt : cur;
-        const int ns = last ? 0 : s + 1;
-#pragma unroll 1
-        for (int i = 0; ok && i < 2; ++i) {
-          if (s >= 0 && s < cur.steps(i)) ok = values(cur, i, s);
-          if (last && i == 0 && more) {
-            ok = ok && wwait(bar(C::kBarQFull), q_ph);
-            q_ph ^= 1;
-          }
-          if (ok && ns < u.steps(i)) ok = scores(u, i, ns);
+      const int last = cur.steps(0) - 1, steps1 = cur.steps(1);
+      for (int s = 0; s < last; ++s) {
+        if (!values(cur, 0, s) || !scores(cur, 0, s + 1) || !values(cur, 1, s) ||
+            (s + 1 < steps1 && !scores(cur, 1, s + 1))) {
+          ok = false;
+          break;
         }
-        ++s;
-      } while (ok && s < steps);
+      }
+#pragma unroll 1
+      for (int i = 0; ok && i < 2; ++i)
+        if (last >= 0 && last < cur.steps(i)) ok = values(cur, i, last);
+      if (ok && more) {
+        ok = wwait(bar(C::kBarQFull), q_ph);
+        q_ph ^= 1;
+      }
+#pragma unroll 1
+      for (int i = 0; ok && more && i < 2; ++i)
+        if (nxt.steps(i) > 0) ok = scores(nxt, i, 0);
       cur = nxt;
       more = more && next_run(nxt);
     }
@@ -544,44 +562,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (leader) mma_commit(bar(C::kBarDrain));
       mbar_drain(bar(C::kBarDrain), 0);
     }
-  } else if (warp < 4) {
+  } else if (warp == 2) {
     // -------------------------------------------------------------------- Q
-    // The rows of each piece, copied by both warps as soon as the scores of
-    // the piece before are done: 16-byte pieces, a row's by neighbouring lanes.
-    constexpr int kPieces = D / 8, U = 8;
-    const int me = threadIdx.x - 64;
+    // The rows of each piece, as soon as the scores of the piece before are
+    // done: boxes of q_box tokens and 64 columns, one a lane.  A box may reach
+    // into another request's rows; theirs are computed and not stored.
+    if (lane == 0) tma_prefetch_desc(&tm_q);
+    const int box_bytes = q_box * G * 128;
     bool ok = true;
-    for (int k = 0; ok && walk.next(a, span); ++k) {
-      const int tok0 = p.m * span, ntok = min(span, p.x.n - tok0);
-      const int total = ntok * G * kPieces;
-      const uint16_t* src = static_cast<const uint16_t*>(a.q) + p.g * G * D;
-      for (int e0 = me; ok && e0 - me < total; e0 += 64 * U) {
-        uint4 v[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int e = e0 + u * 64, r = e / kPieces, t = r / G;
-          if (e < total)
-            v[u] = *reinterpret_cast<const uint4*>(src + (p.x.q0 + tok0 + t) * a.q_stride +
-                                                   (r - t * G) * D + (e % kPieces) * 8);
-        }
-        if (e0 == me)
-          ok = __all_sync(0xffffffffu, mbar_wait_short(bar(C::kBarQEmpty), (k & 1) ^ 1, wc));
-        if (!ok) break;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int e = e0 + u * 64, r = e / kPieces, c = e % kPieces;
-          if (e < total) {
-            const int tile = kPair && r >= tpt * G ? 1 : 0, row = r - tile * tpt * G;
-            *reinterpret_cast<uint4*>(smem + C::kOffQ + tile * C::kTileBytes + (c >> 3) * kBoxBytes +
-                                      row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v[u];
-          }
-        }
-      }
+    int k = 0;
+    for (; ok && walk.next(a, span); ++k) {
+      ok = __all_sync(0xffffffffu, mbar_wait_short(bar(C::kBarQEmpty), (k & 1) ^ 1, wc));
       if (!ok) break;
-      fence_async_shared();
-      mbar_arrive(bar(C::kBarQFull));
+      const int tok0 = p.m * span, ntok = min(span, p.x.n - tok0);
+      const int boxes = (ntok + q_box - 1) / q_box;  // q_box divides tpt, or one is a tile
+      if (lane == 0) mbar_arrive_expect_tx(bar(C::kBarQFull), boxes * C::kHalves * box_bytes);
+      __syncwarp();
+      for (int e = lane; e < boxes * C::kHalves; e += 32) {
+        const int half = e % C::kHalves, t = e / C::kHalves * q_box;
+        const int tile = kPair && t >= tpt ? 1 : 0;
+        tma_load_3d(sQ + tile * C::kTileBytes + half * kBoxBytes + (t - tile * tpt) * G * 128, &tm_q,
+                    bar(C::kBarQFull), half * 64, p.g * G, p.x.q0 + tok0 + t);
+      }
     }
-  } else {
+    if (!ok && k > 0) mbar_drain(bar(C::kBarQFull), (k - 1) & 1);
+  } else if (warp >= 4) {
     // -------------------------------------------------------------- softmax
     const int ti = (warp - 4) >> 2;
     const int wq = warp & 3;         // TMEM sub-partition = rows 32*wq ..
@@ -609,6 +614,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         bits = a.tree[p.x.q0 + token];
         if (p.x.n < 64) bits &= (1ull << p.x.n) - 1;
       }
+      // Without a tree a row sees the new positions up to itself.
+      const int upto = chain && (kPaged || a.causal) ? token + 1 : 0;
       const bool warp_live = __any_sync(0xffffffffu, live);
       float m = -INFINITY, l = 0.f;
       const int step = pair ? 1 : 2;
@@ -632,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           reg_fence32(r + 96);
           if (k0 + kT > p.x.ctx) {
             uint32_t vis[4];
-            seen_columns(vis, k0, p.x.ctx, chain, bits, token + 1);
+            seen_columns(vis, k0, p.x.ctx + upto, p.x.ctx, bits);
 #pragma unroll
             for (int j = 0; j < 128; ++j)
               if (!(vis[j >> 5] >> (j & 31) & 1)) r[j] = __float_as_uint(-INFINITY);
@@ -967,6 +974,26 @@ bool make_map(CUtensorMap* m, const void* ptr, bool bf16, const CacheShape& c, i
   return encode_tiled(m, bf16, 4, ptr, dims, strides, box);
 }
 
+// Tokens of a box of Q: about what a request has on the average, so that little
+// is read for nothing, but whole swizzle groups of 8 rows and a part of a tile
+// (else a tile).
+int query_box(int R, int N, int G) {
+  const int tpt = kT / G;
+  const int64_t mean = ((int64_t)N + R - 1) / R;
+  for (int t = 1; t < tpt; t *= 2)
+    if (t >= mean && t * G % 8 == 0 && tpt % t == 0) return t;
+  return tpt;
+}
+
+// Q as a 3-D tensor (d, head, token), box 64 columns, the heads of a kv head and
+// `tokens` tokens.
+bool query_map(CUtensorMap* m, const TreeArgs& a, bool bf16, int G, int D, int tokens) {
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.H, (cuuint64_t)a.N};
+  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.q_stride * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)tokens};
+  return encode_tiled(m, bf16, 3, a.q, dims, strides, box);
+}
+
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Two row tiles an item where the requests have more than a tile's rows (128)
@@ -980,13 +1007,21 @@ int place_rows(int N, int G) {
   return (int)(have < most ? have : most);
 }
 
-template <bool kBf16, int D, bool kPair>
+template <bool kBf16, int D, bool kPair, bool kPaged>
 cudaError_t run(const TreeArgs& a, cudaStream_t stream) {
   const int G = a.H / a.Hkv;
-  CUtensorMap mk, mv;
-  if (!make_map(&mk, a.k_cache, kBf16, a.cache, a.Hkv, D) ||
-      !make_map(&mv, a.v_cache, kBf16, a.cache, a.Hkv, D))
-    return cudaErrorInvalidValue;
+  CUtensorMap mq, mk, mv;
+  const int box = query_box(a.R, a.N, G);
+  if (!query_map(&mq, a, kBf16, G, D, box)) return cudaErrorInvalidValue;
+  if constexpr (kPaged) {
+    if (!make_map(&mk, a.k_cache, kBf16, a.cache, a.Hkv, D) ||
+        !make_map(&mv, a.v_cache, kBf16, a.cache, a.Hkv, D))
+      return cudaErrorInvalidValue;
+  } else {
+    if (!rows_map(&mk, a.k_cache, kBf16, a.Hkv, D, a.k_stride, a.Nk) ||
+        !rows_map(&mv, a.v_cache, kBf16, a.Hkv, D, a.v_stride, a.Nk))
+      return cudaErrorInvalidValue;
+  }
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -994,7 +1029,7 @@ cudaError_t run(const TreeArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int smem = Cfg<D, kPair>::kSmemBytes;
   static DeviceOnce allowed;
-  e = allowed.shared_memory(reinterpret_cast<const void*>(tree_kernel<kBf16, D, kPair>), dev, smem);
+  e = allowed.shared_memory(reinterpret_cast<const void*>(tree_kernel<kBf16, D, kPair, kPaged>), dev, smem);
   if (e != cudaSuccess) return e;
   Partials w;
   w.rows = place_rows(a.N, G);
@@ -1005,7 +1040,7 @@ cudaError_t run(const TreeArgs& a, cudaStream_t stream) {
   ws += align256((size_t)kMaxCtas * 2 * w.rows * sizeof(float));
   w.o = reinterpret_cast<float*>(ws);
   const int grid = sms < kMaxCtas ? sms : kMaxCtas;
-  tree_kernel<kBf16, D, kPair><<<grid, kThreads, smem, stream>>>(mk, mv, a, w);
+  tree_kernel<kBf16, D, kPair, kPaged><<<grid, kThreads, smem, stream>>>(mq, mk, mv, a, w, box);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -1022,21 +1057,43 @@ cudaError_t run(const TreeArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-size_t tree_workspace_bytes(int N, int H, int Hkv, int D) {
-  const size_t rows = (size_t)place_rows(N, H / Hkv);
+namespace {
+size_t places_bytes(size_t rows, int D) {
   return align256(kMaxCtas * sizeof(Cut)) +
          align256((size_t)kMaxCtas * 2 * rows * sizeof(float)) +
          align256((size_t)kMaxCtas * 2 * rows * D * sizeof(float));
 }
+}  // namespace
+
+size_t tree_workspace_bytes(int N, int H, int Hkv, int D) {
+  return places_bytes((size_t)place_rows(N, H / Hkv), D);
+}
+
+size_t line_workspace_bytes(int N, int H, int D) {
+  const int64_t have = (int64_t)N * H;
+  return places_bytes((size_t)(have < 2 * kT ? have : 2 * kT), D);
+}
 
 cudaError_t launch_tree_attn(const TreeArgs& a, int dtype, cudaStream_t stream) {
   const bool pair = use_pairs(a.R, a.N, a.H / a.Hkv);
-  if (dtype == CPATTN_BF16) {
-    if (a.D == 128) return pair ? run<true, 128, true>(a, stream) : run<true, 128, false>(a, stream);
-    return pair ? run<true, 64, true>(a, stream) : run<true, 64, false>(a, stream);
+#define CPATTN_TREE(paged)                                                          \
+  if (dtype == CPATTN_BF16) {                                                       \
+    if (a.D == 128)                                                                 \
+      return pair ? run<true, 128, true, paged>(a, stream)                          \
+                  : run<true, 128, false, paged>(a, stream);                        \
+    return pair ? run<true, 64, true, paged>(a, stream)                             \
+                : run<true, 64, false, paged>(a, stream);                           \
+  }                                                                                 \
+  if (a.D == 128)                                                                   \
+    return pair ? run<false, 128, true, paged>(a, stream)                           \
+                : run<false, 128, false, paged>(a, stream);                         \
+  return pair ? run<false, 64, true, paged>(a, stream)                              \
+              : run<false, 64, false, paged>(a, stream)
+  if (a.cu_k == nullptr) {
+    CPATTN_TREE(true);
   }
-  if (a.D == 128) return pair ? run<false, 128, true>(a, stream) : run<false, 128, false>(a, stream);
-  return pair ? run<false, 64, true>(a, stream) : run<false, 64, false>(a, stream);
+  CPATTN_TREE(false);
+#undef CPATTN_TREE
 }
 
 }  // namespace cpattn

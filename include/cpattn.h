@@ -646,7 +646,7 @@ CPATTN_API int cpattn_tree_attn(const void* q, int64_t q_stride, const void* k_c
  * workspace: device, at least cpattn_prompt_attn_workspace_bytes, 256-byte
  * aligned, scratch (calls whose execution overlaps need one each).
  */
-CPATTN_API size_t cpattn_prompt_attn_workspace_bytes(int R, int Nq);
+CPATTN_API size_t cpattn_prompt_attn_workspace_bytes(int R, int Nq, int H, int D);
 CPATTN_API int cpattn_prompt_attn(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                                   const void* v, int64_t v_stride, const int32_t* cu_q,
                                   const int32_t* cu_k, void* out, float* lse, int R, int Nq,

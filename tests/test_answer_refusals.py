@@ -84,8 +84,8 @@ def test_workspace_is_checked():
     assert need > 0 and lib.cpattn_tree_attn_workspace_bytes(-1, 4, 2, 64) == 0
     for bad in (dict(ws=null), dict(ws=ctypes.c_void_p(0x1010)), dict(wb=need - 1)):
         assert call("cpattn_tree_attn", TREE, **bad) == W
-    need = lib.cpattn_prompt_attn_workspace_bytes(2, 4)
-    assert need > 0 and lib.cpattn_prompt_attn_workspace_bytes(-1, 4) == 0
+    need = lib.cpattn_prompt_attn_workspace_bytes(2, 4, 4, 64)
+    assert need > 0 and lib.cpattn_prompt_attn_workspace_bytes(-1, 4, 4, 64) == 0
     for bad in (dict(ws=null), dict(ws=ctypes.c_void_p(0x1010)), dict(wb=need - 1)):
         assert call("cpattn_prompt_attn", PROMPT, **bad) == W
 

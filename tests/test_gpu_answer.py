@@ -110,6 +110,10 @@ PROMPTS = [
     ([40, 200, 3, 1], [39, 10, 0, 1], 4, 4, 128),     # rows that see nothing
     ([1] * 70, None, 4, 1, 64),
     ([1030], [2100], 2, 2, 128),
+    ([5, 0, 33, 1], [3000, 700, 2000, 5], 8, 2, 64),        # few rows, many keys
+    ([37, 2, 130] * 44, None, 16, 8, 64),                    # many sequences, sorted
+    ([37, 0, 130] * 44, [20, 5, 140] * 44, 12, 12, 128),
+    ([3700], None, 64, 32, 64),                              # one long one
 ]
 
 
