@@ -420,6 +420,38 @@ bool encode_tiled(CUtensorMap* m, bool bf16, int rank, const void* ptr, const cu
 bool rows_map(CUtensorMap* m, const void* ptr, bool bf16, int heads, int D, int64_t stride,
               int64_t rows);
 
+// What one request asks for, held to the buffers whatever its lengths say.
+struct Req {
+  int q0, n;   // its rows of q
+  int ctx;     // its new token t sees the positions below ctx + t + 1 (below ctx: not causal)
+  int total;   // positions in all
+  int k0;      // packed keys: the row of position 0
+};
+
+template <bool kPaged>
+__device__ __forceinline__ bool load_req(const TreeArgs& a, int r, Req& x) {
+  bool ok = packed_rows(a.cu, r, a.N, x.q0, x.n);
+  if constexpr (kPaged) {
+    const int ctx = a.ctx[r];
+    const int cap = a.width * a.cache.page_size;
+    x.ctx = ctx < 0 ? 0 : (ctx > cap ? cap : ctx);
+    ok = ok && ctx >= 0 && (long long)ctx + x.n <= cap && (a.tree == nullptr || x.n <= 64);
+    x.total = (int)((long long)x.ctx + x.n < cap ? (long long)x.ctx + x.n : cap);
+    x.k0 = 0;
+  } else {
+    ok &= packed_rows(a.cu_k, r, a.Nk, x.k0, x.total);
+    x.ctx = a.causal ? x.total - x.n : x.total;
+  }
+  return ok;
+}
+
+// One block per token and kv head on CUDA cores, and what it and the tensor
+// cores' cut line take for `keys` keys a request (us, estimated).
+cudaError_t launch_small_attn(const TreeArgs& a, int dtype, int sms, cudaStream_t stream);
+float small_attn_us(const TreeArgs& a, int64_t keys, int sms);
+float line_attn_us(const TreeArgs& a, int64_t keys);
+// The tensor cores' cut line (k_tree_tc.cu).
+cudaError_t launch_line_attn(const TreeArgs& a, int dtype, int dev, int sms, cudaStream_t stream);
 cudaError_t launch_page_tables(const TablesArgs& a, cudaStream_t stream);
 cudaError_t launch_cache_write(const CacheWriteArgs& a, cudaStream_t stream);
 size_t tree_workspace_bytes(int N, int H, int Hkv, int D);

@@ -725,6 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 int64_t most_blocks(int R, int Nq) { return (int64_t)Nq / kT + R; }
 
 // How a call is done, from its means (the lengths themselves are on the device).
+//  kSmall: a block a token and kv head on CUDA cores (k_answer_small.cu).
 //  kDirect: at most an item a CTA; each CTA finds its own, nothing is planned.
 //  kLine: few rows and many keys a sequence; the keys of an item are shared
 //    among CTAs and a kv head's query heads share a row tile (k_tree_tc.cu).
@@ -734,16 +735,27 @@ int64_t most_blocks(int R, int Nq) { return (int64_t)Nq / kT + R; }
 //   1 x   1, n 1000: 10.8 / 12.8    4 x  1, n 1000: 19.0 / 14.2   16 x  1, n 8000: 99 / 54
 //   1 x   1, n 8000: 20.2 / 13.7    4 x 32, n 1000: 18.6 / 18.3   16 x 32, n    1: 17.6 / 15.0
 //   4 x 128, n 8000: 82.5 / 57.5    4 x 64, n 1000: 18.5 / 25.1   16 x 64, n 1000: 29.6 / 42.9
-enum Way { kDirect, kLine, kSorted };
+// and without keys in front (small / direct, line or sorted):
+//   1 x 16:  5.3 /  9.4    8 x  4:  5.3 / 10.8    64 x  4: 15 / 28
+//   1 x 64:  9.2 /  9.4    8 x 16:  9.6 / 10.8    64 x 16: 49 / 31
+enum Way { kSmall, kDirect, kLine, kSorted };
 
-Way way(const PromptArgs& a, int sms) {
+Way way(const PromptArgs& a, const TreeArgs& t, int sms) {
   if (a.Nk == 0) return kSorted;
   const int G = a.H / a.Hkv;
   const int64_t items = ((int64_t)a.Nq / kT + a.R) * (G % 2 == 0 ? a.H / 2 : a.H);
   const int64_t rows = (int64_t)a.Nq * G / a.R, keys = a.Nk / a.R;
-  if (rows <= kT ? keys > 512 || items > sms : rows <= 8 * kT && keys >= 2048 && items <= sms)
-    return kLine;
-  return items <= sms ? kDirect : kSorted;
+  Way by = items <= sms ? kDirect : kSorted;
+  const float tiles = (float)(keys / kT + 1);
+  float us = by == kDirect ? 8.f + 1.5f * tiles : 14.f + items * (3.f + 1.6f * tiles) / sms;
+  if (rows <= kT ? keys > 512 || items > sms : rows <= 8 * kT && keys >= 2048 && items <= sms) {
+    by = kLine;
+    us = line_attn_us(t, keys);
+  }
+  // Under the causal rule a row sees about the keys in front of its sequence's
+  // queries and half of those among them.
+  const int64_t seen = a.causal ? (a.Nk > a.Nq ? (a.Nk - a.Nq / 2) / a.R : keys / 2) : keys;
+  return small_attn_us(t, seen + 1, sms) < us ? kSmall : by;
 }
 
 template <bool kBf16, int D>
@@ -809,32 +821,31 @@ cudaError_t launch_prompt_attn(const PromptArgs& a, int dtype, cudaStream_t stre
   if (e != cudaSuccess) return e;
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const Way by = way(a, sms);
-  if (by == kLine) {
-    TreeArgs t = {};
-    t.q = a.q;
-    t.q_stride = a.q_stride;
-    t.k_cache = a.k;
-    t.v_cache = a.v;
-    t.cu = a.cu_q;
-    t.out = a.out;
-    t.lse = a.lse;
-    t.R = a.R;
-    t.N = a.Nq;
-    t.H = a.H;
-    t.Hkv = a.Hkv;
-    t.D = a.D;
-    t.scale = a.scale;
-    t.scale_log2 = a.scale_log2;
-    t.workspace = a.workspace;
-    t.err = a.err;
-    t.cu_k = a.cu_k;
-    t.k_stride = a.k_stride;
-    t.v_stride = a.v_stride;
-    t.Nk = a.Nk;
-    t.causal = a.causal;
-    return launch_tree_attn(t, dtype, stream);
-  }
+  TreeArgs t = {};
+  t.q = a.q;
+  t.q_stride = a.q_stride;
+  t.k_cache = a.k;
+  t.v_cache = a.v;
+  t.cu = a.cu_q;
+  t.out = a.out;
+  t.lse = a.lse;
+  t.R = a.R;
+  t.N = a.Nq;
+  t.H = a.H;
+  t.Hkv = a.Hkv;
+  t.D = a.D;
+  t.scale = a.scale;
+  t.scale_log2 = a.scale_log2;
+  t.workspace = a.workspace;
+  t.err = a.err;
+  t.cu_k = a.cu_k;
+  t.k_stride = a.k_stride;
+  t.v_stride = a.v_stride;
+  t.Nk = a.Nk;
+  t.causal = a.causal;
+  const Way by = way(a, t, sms);
+  if (by == kSmall) return launch_small_attn(t, dtype, sms, stream);
+  if (by == kLine) return launch_line_attn(t, dtype, dev, sms, stream);
   if (dtype == CPATTN_BF16)
     return a.D == 128 ? run<true, 128>(a, by, dev, sms, stream)
                       : run<true, 64>(a, by, dev, sms, stream);

@@ -96,31 +96,6 @@ struct Cfg {
 __host__ __device__ constexpr uint32_t col_s(int i) { return 128u * (uint32_t)i; }
 __host__ __device__ constexpr uint32_t col_o(int i) { return 256u + 128u * (uint32_t)i; }
 
-// What one request asks for, held to the buffers whatever its lengths say.
-struct Req {
-  int q0, n;   // its rows of q
-  int ctx;     // its new token t sees the positions below ctx + t + 1 (below ctx: not causal)
-  int total;   // positions in all
-  int k0;      // packed keys: the row of position 0
-};
-
-template <bool kPaged>
-__device__ __forceinline__ bool load_req(const TreeArgs& a, int r, Req& x) {
-  bool ok = packed_rows(a.cu, r, a.N, x.q0, x.n);
-  if constexpr (kPaged) {
-    const int ctx = a.ctx[r];
-    const int cap = a.width * a.cache.page_size;
-    x.ctx = ctx < 0 ? 0 : (ctx > cap ? cap : ctx);
-    ok = ok && ctx >= 0 && (long long)ctx + x.n <= cap && (a.tree == nullptr || x.n <= 64);
-    x.total = (int)((long long)x.ctx + x.n < cap ? (long long)x.ctx + x.n : cap);
-    x.k0 = 0;
-  } else {
-    ok &= packed_rows(a.cu_k, r, a.Nk, x.k0, x.total);
-    x.ctx = a.causal ? x.total - x.n : x.total;
-  }
-  return ok;
-}
-
 // An item is a kv head of a request and `span` of its tokens.
 __device__ __forceinline__ int items_of(const Req& x, int span) { return (x.n + span - 1) / span; }
 // Key tiles of the request's m-th item (at least one, so that its rows are
@@ -1008,7 +983,7 @@ int place_rows(int N, int G) {
 }
 
 template <bool kBf16, int D, bool kPair, bool kPaged>
-cudaError_t run(const TreeArgs& a, cudaStream_t stream) {
+cudaError_t run(const TreeArgs& a, int dev, int sms, cudaStream_t stream) {
   const int G = a.H / a.Hkv;
   CUtensorMap mq, mk, mv;
   const int box = query_box(a.R, a.N, G);
@@ -1022,14 +997,9 @@ cudaError_t run(const TreeArgs& a, cudaStream_t stream) {
         !rows_map(&mv, a.v_cache, kBf16, a.Hkv, D, a.v_stride, a.Nk))
       return cudaErrorInvalidValue;
   }
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
   const int smem = Cfg<D, kPair>::kSmemBytes;
   static DeviceOnce allowed;
-  e = allowed.shared_memory(reinterpret_cast<const void*>(tree_kernel<kBf16, D, kPair, kPaged>), dev, smem);
+  cudaError_t e = allowed.shared_memory(reinterpret_cast<const void*>(tree_kernel<kBf16, D, kPair, kPaged>), dev, smem);
   if (e != cudaSuccess) return e;
   Partials w;
   w.rows = place_rows(a.N, G);
@@ -1074,26 +1044,41 @@ size_t line_workspace_bytes(int N, int H, int D) {
   return places_bytes((size_t)(have < 2 * kT ? have : 2 * kT), D);
 }
 
-cudaError_t launch_tree_attn(const TreeArgs& a, int dtype, cudaStream_t stream) {
+cudaError_t launch_line_attn(const TreeArgs& a, int dtype, int dev, int sms, cudaStream_t stream) {
   const bool pair = use_pairs(a.R, a.N, a.H / a.Hkv);
 #define CPATTN_TREE(paged)                                                          \
   if (dtype == CPATTN_BF16) {                                                       \
     if (a.D == 128)                                                                 \
-      return pair ? run<true, 128, true, paged>(a, stream)                          \
-                  : run<true, 128, false, paged>(a, stream);                        \
-    return pair ? run<true, 64, true, paged>(a, stream)                             \
-                : run<true, 64, false, paged>(a, stream);                           \
+      return pair ? run<true, 128, true, paged>(a, dev, sms, stream)                          \
+                  : run<true, 128, false, paged>(a, dev, sms, stream);                        \
+    return pair ? run<true, 64, true, paged>(a, dev, sms, stream)                             \
+                : run<true, 64, false, paged>(a, dev, sms, stream);                           \
   }                                                                                 \
   if (a.D == 128)                                                                   \
-    return pair ? run<false, 128, true, paged>(a, stream)                           \
-                : run<false, 128, false, paged>(a, stream);                         \
-  return pair ? run<false, 64, true, paged>(a, stream)                              \
-              : run<false, 64, false, paged>(a, stream)
+    return pair ? run<false, 128, true, paged>(a, dev, sms, stream)                           \
+                : run<false, 128, false, paged>(a, dev, sms, stream);                         \
+  return pair ? run<false, 64, true, paged>(a, dev, sms, stream)                              \
+              : run<false, 64, false, paged>(a, dev, sms, stream)
   if (a.cu_k == nullptr) {
     CPATTN_TREE(true);
   }
   CPATTN_TREE(false);
 #undef CPATTN_TREE
+}
+
+// The keys of a request are only bounded here (the table's width): a table much
+// wider than its requests sends small calls to the tensor cores, which costs
+// what the table in k_answer_small.cu says.
+cudaError_t launch_tree_attn(const TreeArgs& a, int dtype, cudaStream_t stream) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int64_t keys = (int64_t)a.width * a.cache.page_size;
+  if (small_attn_us(a, keys, sms) < line_attn_us(a, keys))
+    return launch_small_attn(a, dtype, sms, stream);
+  return launch_line_attn(a, dtype, dev, sms, stream);
 }
 
 }  // namespace cpattn

@@ -142,22 +142,33 @@ def test_prompt_attention_of_a_fused_projection_with_scale_and_large_scores():
     check(lse, l, tl, "lse")
 
 
-def test_prompt_attention_keeps_sequences_apart_and_rows_behind_the_last():
-    # The rows of one sequence, and those behind the last, are NaN or infinite:
-    # no other sequence's result changes, and rows behind stay as they were.
+@pytest.mark.parametrize("nq,nk", [
+    ([3, 5, 2, 4], None),                                    # a block a token
+    ([100, 60, 140, 30], None),                              # an item a CTA
+    ([2, 1, 3, 1], [600, 900, 700, 800]),                    # keys shared among CTAs
+    ([100, 60, 140, 30] * 30, None),                         # sorted
+    ([100, 60, 140, 30] * 30, [150, 70, 140, 200] * 30),
+])
+def test_prompt_attention_keeps_sequences_apart_and_rows_behind_the_last(nq, nk):
+    # The rows of the second sequence, and those behind the last, are NaN or
+    # infinite: no other sequence's result changes, and rows behind stay as they
+    # were.
     H, Hkv, D = 4, 2, 128
-    nq, tail = [100, 60, 140, 30], 37
+    tail = 37
+    nk = nq if nk is None else nk
     q = normal(1, sum(nq) + tail, H, D, dtype=torch.bfloat16)
-    k, v = (normal(s, sum(nq) + tail, Hkv, D, dtype=torch.bfloat16) for s in (2, 3))
-    cu = ints(offsets(nq))
-    want, wlse = cpa.prompt_attention(q, k, v, cu)
-    bad = slice(100, 160)
-    for t, x in ((q, math.nan), (k, math.inf), (v, math.nan)):
-        t[bad] = x
-        t[sum(nq):] = x
+    k, v = (normal(s, sum(nk) + tail, Hkv, D, dtype=torch.bfloat16) for s in (2, 3))
+    cu_q, cu_k = ints(offsets(nq)), ints(offsets(nk))
+    want, wlse = cpa.prompt_attention(q, k, v, cu_q, cu_k)
+    bad, bad_k = slice(nq[0], nq[0] + nq[1]), slice(nk[0], nk[0] + nk[1])
+    for t, x, b, n in ((q, math.nan, bad, nq), (k, math.inf, bad_k, nk), (v, math.nan, bad_k, nk)):
+        t[b] = x
+        t[sum(n):] = x
     out, lse = torch.full_like(want, 7.0), torch.full_like(wlse, 7.0)
-    cpa.prompt_attention(q, k, v, cu, out=out, lse=lse)
-    good = torch.cat([torch.arange(0, 100), torch.arange(160, sum(nq))]).to(DEV)
+    cpa.prompt_attention(q, k, v, cu_q, cu_k, out=out, lse=lse)
+    good = torch.ones(sum(nq), dtype=torch.bool, device=DEV)
+    good[bad] = False
+    good = good.nonzero()[:, 0]
     assert torch.equal(out[good], want[good]) and torch.equal(lse[:, good], wlse[:, good])
     assert bool((out[sum(nq):] == 7).all()) and bool((lse[:, sum(nq):] == 7).all())
     assert bool(torch.isnan(out[bad]).all())
@@ -180,13 +191,13 @@ def test_prompt_attention_reports_broken_offsets():
 class Cache:
     """A paged cache with pages dealt at random, filled with `fill` elsewhere."""
 
-    def __init__(self, ctx, new, Hkv, D, P, dtype, order="tokens", fill=math.nan, seed=11):
+    def __init__(self, ctx, new, Hkv, D, P, dtype, order="tokens", fill=math.nan, seed=11, wider=1):
         self.ctx, self.new, self.P = ctx, new, P
         need = [-(-(c + n) // P) for c, n in zip(ctx, new)]
         pages = sum(need) + 2
         g = torch.Generator().manual_seed(seed)
         ids = torch.randperm(pages, generator=g, dtype=torch.int32)
-        width = max(need + [1]) + 1
+        width = max(need + [1]) + wider
         table = torch.full((len(ctx), width), -7, dtype=torch.int32)
         first = offsets(need)
         for r, n in enumerate(need):
@@ -260,10 +271,11 @@ TREES = [
 ]
 
 
+@pytest.mark.parametrize("wider", [1, 4000])  # a wide table is answered by the tensor cores
 @pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("ctx,new,H,Hkv,D,P,tree", TREES)
-def test_tree_attention(ctx, new, H, Hkv, D, P, tree, dtype):
-    cache = Cache(ctx, new, Hkv, D, P, TYPES[dtype])
+def test_tree_attention(ctx, new, H, Hkv, D, P, tree, dtype, wider):
+    cache = Cache(ctx, new, Hkv, D, P, TYPES[dtype], wider=wider)
     q = normal(9, sum(new), H, D, dtype=TYPES[dtype])
     words = [w for r, n in enumerate(new) for w in random_tree(r, n)] if tree else None
     out, lse = run_tree(q, cache, words)
@@ -273,9 +285,10 @@ def test_tree_attention(ctx, new, H, Hkv, D, P, tree, dtype):
     check(lse, l, tl, "lse")
 
 
+@pytest.mark.parametrize("wider", [1, 300])
 @pytest.mark.parametrize("order", ["heads", "interleaved"])
-def test_tree_attention_other_cache_orders_strides_and_scale(order):
-    cache = Cache([200, 77], [9, 3], 2, 128, 32, torch.bfloat16, order)
+def test_tree_attention_other_cache_orders_strides_and_scale(order, wider):
+    cache = Cache([200, 77], [9, 3], 2, 128, 32, torch.bfloat16, order, wider=wider)
     wide = normal(4, 12, 12, 128, dtype=torch.bfloat16)
     q = wide[:, 2:10]
     words = random_tree(1, 9) + random_tree(2, 3)
@@ -285,8 +298,9 @@ def test_tree_attention_other_cache_orders_strides_and_scale(order):
     check(lse, l, tl, "lse")
 
 
-def test_tree_attention_rows_that_see_nothing_and_bits_behind_the_last_token():
-    cache = Cache([0, 0, 50], [3, 2, 4], 2, 64, 16, torch.float16)
+@pytest.mark.parametrize("wider", [1, 300])  # small: CUDA cores; wide: tensor cores
+def test_tree_attention_rows_that_see_nothing_and_bits_behind_the_last_token(wider):
+    cache = Cache([0, 0, 50], [3, 2, 4], 2, 64, 16, torch.float16, wider=wider)
     q = normal(4, 9, 4, 64, dtype=torch.float16)
     words = [0, 0b10, 0b111, 0, 0, 0b1 | 1 << 40, 0b10 | 1 << 63, 0b100, 0]
     out, lse = run_tree(q, cache, words)
@@ -297,11 +311,12 @@ def test_tree_attention_rows_that_see_nothing_and_bits_behind_the_last_token():
     assert cpa.device_status() == 0
 
 
-def test_tree_attention_leaves_rows_behind_the_last_and_ignores_other_pages():
+@pytest.mark.parametrize("wider", [1, 300])  # small: CUDA cores; wide: tensor cores
+def test_tree_attention_leaves_rows_behind_the_last_and_ignores_other_pages(wider):
     # Pages of other requests and unused parts of pages hold NaN (the cache's
     # fill) or infinities; q has padded rows.
     for fill in (math.nan, math.inf):
-        cache = Cache([130, 20], [3, 2], 2, 128, 64, torch.bfloat16, fill=fill)
+        cache = Cache([130, 20], [3, 2], 2, 128, 64, torch.bfloat16, fill=fill, wider=wider)
         q = normal(4, 12, 8, 128, dtype=torch.bfloat16)
         q[5:] = fill
         out, lse = torch.full_like(q, 7.0), torch.full((8, 12), 7.0, device=DEV)
@@ -312,8 +327,9 @@ def test_tree_attention_leaves_rows_behind_the_last_and_ignores_other_pages():
         assert bool((out[5:] == 7).all()) and bool((lse[:, 5:] == 7).all())
 
 
-def test_tree_attention_reports_bad_pages_and_lengths():
-    cache = Cache([130, 20], [3, 2], 2, 128, 64, torch.bfloat16, fill=0.0)
+@pytest.mark.parametrize("wider", [1, 300])  # small: CUDA cores; wide: tensor cores
+def test_tree_attention_reports_bad_pages_and_lengths(wider):
+    cache = Cache([130, 20], [3, 2], 2, 128, 64, torch.bfloat16, fill=0.0, wider=wider)
     q = normal(4, 5, 8, 128, dtype=torch.bfloat16)
     ctx, cu, good = ints([130, 20]), ints([0, 3, 5]), cache.table.clone()
     o, l, to, tl = tree_reference(q, cache)
@@ -323,12 +339,12 @@ def test_tree_attention_reports_bad_pages_and_lengths():
         out, lse = cpa.tree_attention(q, cache.k, cache.v, table, ctx, cu)
         assert cpa.device_status() == -1, page
         check(out[3:], o[3:], to[3:], "the other request")
-    for ctx_, cu_ in (([-5, 20], [0, 3, 5]), ([10000, 20], [0, 3, 5]), ([130, 20], [0, 4, 3]),
+    for ctx_, cu_ in (([-5, 20], [0, 3, 5]), ([100000, 20], [0, 3, 5]), ([130, 20], [0, 4, 3]),
                       ([130, 20], [0, 3, 6]), ([2 ** 31 - 1, 20], [0, 3, 5])):
         cpa.tree_attention(q, cache.k, cache.v, good, ints(ctx_), ints(cu_))
         assert cpa.device_status() == -1, (ctx_, cu_)
     wide = normal(4, 65, 8, 128, dtype=torch.bfloat16)
-    big = Cache([10], [65], 2, 128, 64, torch.bfloat16)
+    big = Cache([10], [65], 2, 128, 64, torch.bfloat16, wider=wider)
     cpa.tree_attention(wide, big.k, big.v, big.table, ints([10]), ints([0, 65]),
                        torch.zeros(65, dtype=torch.int64, device=DEV))
     assert cpa.device_status() == -1
