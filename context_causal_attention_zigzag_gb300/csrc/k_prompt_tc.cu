@@ -171,17 +171,39 @@ struct Cfg {
   static constexpr int kBarQEmpty = 2;  // [2]
   static constexpr int kBarFull = 4;
   static constexpr int kBarEmpty = kBarFull + kSlots;
+  // Per query tile.  With a third S buffer a tile's scores and weights run one
+  // step ahead of their product, so two barriers take turns: a single one could
+  // pass two phases before they are seen.
+  static constexpr int kTurns = D == 128 ? 1 : 2;
   static constexpr int kBarS = kBarEmpty + kSlots;
-  static constexpr int kBarP = kBarS + 2;
-  static constexpr int kBarO = kBarP + 2;
+  static constexpr int kBarP = kBarS + 2 * kTurns;
+  static constexpr int kBarO = kBarP + 2 * kTurns;
   static constexpr int kBarDrain = kBarO + 2;
   static constexpr int kNumBars = kBarDrain + 1;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kSmemBytes = kOffMisc + 16 + 1024;  // + slack for 1024-B alignment
+
+  // Barrier and parity of query tile i's c-th step.
+  static __device__ __forceinline__ int turn(int bar0, int i, uint32_t c) {
+    return bar0 + i * kTurns + (kTurns == 2 ? (int)(c & 1) : 0);
+  }
+  static __device__ __forceinline__ uint32_t parity(uint32_t c) {
+    return kTurns == 2 ? c >> 1 & 1 : c & 1;
+  }
 };
 
-__host__ __device__ constexpr uint32_t col_s(int i) { return 128u * (uint32_t)i; }
-__host__ __device__ constexpr uint32_t col_o(int i) { return 256u + 128u * (uint32_t)i; }
+// TMEM.  D = 128: S0 [0,128) S1 [128,256) O0 [256,384) O1 [384,512).  D = 64
+// leaves room for a third S buffer: the scores of step n = 2 * (key tile) +
+// (query tile) go to buffer n % 3, which lets a tile's next scores be computed
+// while its softmax still runs (O0 [384,448) O1 [448,512)).
+template <int D>
+__host__ __device__ constexpr uint32_t col_s(int i, uint32_t step) {
+  return D == 128 ? 128u * (uint32_t)i : 128u * ((2 * step + (uint32_t)i) % 3);
+}
+template <int D>
+__host__ __device__ constexpr uint32_t col_o(int i) {
+  return D == 128 ? 256u + 128u * (uint32_t)i : 384u + 64u * (uint32_t)i;
+}
 
 struct Work {
   const Plan* plan;   // nullptr: one sequence, decoded in closed form, or direct
@@ -316,8 +338,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(C::kBarQFull + i), 1);
       mbar_init(bar(C::kBarQEmpty + i), 1);
-      mbar_init(bar(C::kBarS + i), 1);
-      mbar_init(bar(C::kBarP + i), 128);
+      for (int t = 0; t < C::kTurns; ++t) {
+        mbar_init(bar(C::turn(C::kBarS, i, t)), 1);
+        mbar_init(bar(C::turn(C::kBarP, i, t)), 128);
+      }
       mbar_init(bar(C::kBarO + i), 1);
     }
     mbar_init(bar(C::kBarDrain), 1);
@@ -406,28 +430,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wwait = [&](uint32_t bar_addr, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait_short(bar_addr, parity, wc));
     };
-    uint32_t kv_it = 0, p_ph[2] = {0, 0}, q_ph[2] = {0, 0};
+    uint32_t kv_it = 0, s_n[2] = {0, 0}, p_n[2] = {0, 0}, q_ph[2] = {0, 0};
     bool ok = true;
     // Operand descriptors, computed once and advanced by byte offsets.
     const uint64_t d_q = sdesc_sw128(sQ, 16, 1024);
     const uint64_t d_k = sdesc_sw128(sRing, 16, 1024);
     const uint64_t d_v = sdesc_sw128(sRing, kBoxBytes, 1024);
     auto slot_off = [](uint32_t n) { return (n % kSlots) * (uint32_t)C::kTileBytes; };
-    auto scores = [&](int i, uint32_t kn) {  // S_i = Q_i K^T, K in ring entry kn
+    // S_i = Q_i K^T, K in ring entry kn (key tile kn / 2 of all).
+    auto scores = [&](int i, uint32_t kn) {
+      const uint32_t d = tmem + col_s<D>(i, kn / 2);
       const uint64_t a0 = sdesc_advance(d_q, i * C::kTileBytes);
       const uint64_t b0 = sdesc_advance(d_k, slot_off(kn));
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t off = (kk >> 2) * kBoxBytes + (kk & 3) * 32;
-        mma_ss(tmem + col_s(i), sdesc_advance(a0, off), sdesc_advance(b0, off), kIdescQK, kk > 0);
+        mma_ss(d, sdesc_advance(a0, off), sdesc_advance(b0, off), kIdescQK, kk > 0);
       }
-      mma_commit(bar(C::kBarS + i));
+      mma_commit(bar(C::turn(C::kBarS, i, s_n[i])));
     };
     auto values = [&](int i, uint32_t vn, uint32_t accumulate) {  // O_i += P_i V
       const uint64_t bv = sdesc_advance(d_v, slot_off(vn));
+      const uint32_t p = tmem + col_s<D>(i, vn / 2);
 #pragma unroll
       for (int kk = 0; kk < kT / 16; ++kk)
-        mma_ts(tmem + col_o(i), tmem + col_s(i) + kk * 8, sdesc_advance(bv, kk * 2048), kIdescPV,
+        mma_ts(tmem + col_o<D>(i), p + kk * 8, sdesc_advance(bv, kk * 2048), kIdescPV,
                accumulate | (kk > 0));
     };
     auto full = [&](uint32_t n) { return wwait(bar(C::kBarFull + n % kSlots), (n / kSlots) & 1); };
@@ -441,6 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         scores(i, kn);
         if (nti == 1) mma_commit(bar(C::kBarQEmpty + i));
       }
+      ++s_n[i];
       return true;
     };
     // The next item with keys, as the tiles its two query tiles see.
@@ -462,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && leader) mma_commit(bar(C::kBarEmpty + 0));
     }
     // K(m) is ring entry 2 * kv_it, V(m) entry 2 * kv_it + 1.  Behind each query
-    // tile's product come its next scores.
+    // tile's product come its next scores (D = 64: before it).
     while (ok && have) {
       const bool more = next_item(nxt);
       const int nt = max(cur[0], cur[1]);
@@ -474,25 +502,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         bool k_ready = false;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        auto product = [&](int i) {
           if (m < cur[i]) {
-            if (!wwait(bar(C::kBarP + i), p_ph[i])) {
-              ok = false;
-              break;
+            if (!wwait(bar(C::turn(C::kBarP, i, p_n[i])), C::parity(p_n[i]))) {
+              return false;
             }
-            p_ph[i] ^= 1;
+            ++p_n[i];
             tc_fence_after();
             if (leader) {
               values(i, vn, m > 0);
-              if (m + 1 == cur[i]) mma_commit(bar(C::kBarO + i));
+              if (D == 64 || m + 1 == cur[i]) mma_commit(bar(C::kBarO + i));
             }
           }
+          return true;
+        };
+        auto next_scores = [&](int i) {
           if (m + 1 < cur[i]) {
             if (!k_ready) {
               if (!full(nkn)) {
-                ok = false;
-                break;
+                return false;
               }
               tc_fence_after();
               k_ready = true;
@@ -501,7 +529,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               scores(i, nkn);
               if (m + 2 == cur[i]) mma_commit(bar(C::kBarQEmpty + i));
             }
+            ++s_n[i];
           }
+          return true;
+        };
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          ok = D == 128 ? product(i) && next_scores(i) : next_scores(i) && product(i);
+          if (!ok) break;
         }
         if (!ok) break;
         if (leader) {
@@ -518,8 +553,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         if (ok && nt == cur[i]) {
-          ok = wwait(bar(C::kBarP + i), p_ph[i]);
-          p_ph[i] ^= 1;
+          ok = wwait(bar(C::turn(C::kBarP, i, p_n[i])), C::parity(p_n[i]));
+          ++p_n[i];
           tc_fence_after();
           if (ok && leader) {
             values(i, vn, nt > 1);
@@ -548,9 +583,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int wq = warp & 3;         // TMEM sub-partition = rows 32*wq ..
     const int row = wq * 32 + lane;  // row within the tile
     const uint32_t tl = tmem + ((uint32_t)(wq * 32) << 16);
-    const uint32_t colS = col_s(ti), colO = col_o(ti);
+    const uint32_t colO = col_o<D>(ti);
     const float sl2 = a.scale_log2;
-    uint32_t s_ph = 0, o_ph = 0, kv_it = 0;
+    uint32_t step = 0, o_ph = 0, kv_it = 0;
     bool ok = true;
     items.init(a, w);
     while (ok && items.next(b, g, h0)) {
@@ -561,11 +596,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -INFINITY, l = 0.f;
       for (int t = 0; t < nt; ++t) {
         const int see = end - t * kT;  // visible columns of the tile
-        if (!__all_sync(0xffffffffu, mbar_wait_short(bar(C::kBarS + ti), s_ph, wc))) {
+        const uint32_t colS = col_s<D>(ti, kv_it + t);
+        if (!__all_sync(0xffffffffu, mbar_wait_short(bar(C::turn(C::kBarS, ti, step)),
+                                                     C::parity(step), wc))) {
           ok = false;
           break;
         }
-        s_ph ^= 1;
         tc_fence_after();
         uint32_t r[128];
         tmem_ld32(tl + colS + 0, r + 0);
@@ -619,8 +655,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         l += l0 + l1;
         if (rescale && t > 0) {
           // Softmax-state correction: O <- O * 2^(m_old - m_new).  The S
-          // barrier of this tile also covers the previous P V product, and the
+          // barrier of this tile also covers the previous P V product (D = 64:
+          // it does not, and O's barrier completes with every product), and the
           // next one is issued only after the P barrier below.
+          if (D == 64) {
+            if (!__all_sync(0xffffffffu,
+                            mbar_wait_short(bar(C::kBarO + ti), (step - 1) & 1, wc))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+          }
 #pragma unroll 1
           for (int cc = 0; cc < D / 32; ++cc) {
             uint32_t o[32];
@@ -654,7 +699,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(bar(C::kBarP + ti));
+        mbar_arrive(bar(C::turn(C::kBarP, ti, step)));
+        ++step;
       }
       if (!ok) break;
       kv_it += max(nt0, nt1);
@@ -672,6 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         continue;
       }
+      if (D == 64) o_ph = (step - 1) & 1;
       if (!__all_sync(0xffffffffu, mbar_wait_short(bar(C::kBarO + ti), o_ph, wc))) {
         ok = false;
         break;
