@@ -706,25 +706,28 @@ def _answer_dtype(t):
 
 def _heads_rows(t, name):
     """The token stride of [tokens, heads, D] whose heads lie back to back."""
-    if t.dim() != 3:
+    shape = t.shape
+    if len(shape) != 3:
         raise ValueError(f"{name} must be [tokens, heads, D]")
     s0, s1, s2 = t.stride()
-    n, h, d = t.shape
+    n, h, d = shape
     if (s2 != 1 and d > 1) or (s1 != d and h > 1):
         raise ValueError(f"a token's heads must lie back to back in {name} (strides {t.stride()})")
     return s0 if n > 1 else h * d
 
 
-def _on(device, name, t, dtype=None, numel=None):
+def _on(device, name, t, dtype, numel=None):
     """Refuses an operand that is not contiguous, on `device`, of this type and size."""
+    if t.dtype is dtype and t.get_device() == device.index and t.is_contiguous() \
+            and (numel is None or t.numel() == numel):
+        return
     if t.device != device:
         raise ValueError(f"{name} must be on {device}")
-    if dtype is not None and t.dtype != dtype:
+    if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if numel is not None and t.numel() != numel:
-        raise ValueError(f"{name} must hold {numel} values")
+    raise ValueError(f"{name} must hold {numel} values")
 
 
 def _cuda_device(t):
@@ -734,12 +737,14 @@ def _cuda_device(t):
 
 
 def _table_args(table, R, device):
-    if table.dim() != 2 or table.shape[0] != R or table.dtype != torch.int32 \
-            or table.device != device:
+    shape = table.shape
+    if len(shape) != 2 or shape[0] != R or table.dtype != torch.int32 \
+            or table.get_device() != device.index:
         raise ValueError(f"block_table must be int32 [{R}, width] on {device}")
-    if table.stride(1) != 1 and table.shape[1] > 1:
+    width, strides = shape[1], table.stride()
+    if strides[1] != 1 and width > 1:
         raise ValueError("block_table's rows must be contiguous")
-    return table.shape[1], (table.stride(0) if R > 1 else table.shape[1])
+    return width, (strides[0] if R > 1 else width)
 
 
 def _cache_args(k_cache, v_cache, Hkv, D, dtype, device):
@@ -752,7 +757,7 @@ def _cache_args(k_cache, v_cache, Hkv, D, dtype, device):
         raise ValueError(f"the cache must hold {Hkv} heads of {D} contiguous values")
     if k_cache.dtype != dtype or v_cache.dtype != dtype:
         raise TypeError(f"the cache must be {dtype}")
-    if k_cache.device != device or v_cache.device != device:
+    if k_cache.get_device() != device.index or v_cache.get_device() != device.index:
         raise ValueError(f"the cache must be on {device}")
     return shape[0], shape[1], strides[0], strides[1], strides[2]
 
@@ -761,12 +766,12 @@ def _launch(name, device, *args):
     """Calls the library on `device`'s current stream.  These calls are short
     enough for their way through Python to count: pointers go as plain numbers,
     and the device is switched only if it has to be."""
-    fn = getattr(_lib or lib(), name)
-    if torch.cuda.current_device() == device.index:
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    fn, index = getattr(_lib or lib(), name), device.index
+    if torch._C._cuda_getDevice() == index:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if rc != OK:
         raise CpattnError(name, rc)
 
@@ -878,7 +883,7 @@ def prompt_attention(q, k, v, cu_q, cu_k=None, causal=True, scale=None, out=None
     dev = _cuda_device(q)
     cu_k = cu_q if cu_k is None else cu_k
     if k.shape != v.shape or k.dtype != q.dtype or v.dtype != q.dtype \
-            or k.device != dev or v.device != dev:
+            or k.get_device() != dev.index or v.get_device() != dev.index:
         raise ValueError("k and v must share a shape, and q's dtype and device")
     code, qs, ks, vs = (_answer_dtype(q), _heads_rows(q, "q"), _heads_rows(k, "k"),
                         _heads_rows(v, "v"))
