@@ -44,6 +44,10 @@ bool check_cache(const void* k, const void* v, const CacheShape& c, int D) {
   return true;
 }
 
+// Rows of a packed tensor: an item then takes less than the kernels' bounded
+// waits allow (2 s).
+constexpr int kMostRows = 1 << 27;
+
 bool scale_ok(float s) { return s <= 0.f || isfinite(s); }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -207,7 +211,7 @@ int cpattn_prompt_attn(const void* q, int64_t q_stride, const void* k, int64_t k
                        size_t workspace_bytes, cpattn_stream_t stream) {
   int rc = check_heads(H, Hkv, D, dtype);
   if (rc != CPATTN_OK) return rc;
-  if (R < 0 || R > (1 << 24) || Nq < 0 || Nk < 0 || Nq > (1 << 30) || Nk > (1 << 30) ||
+  if (R < 0 || R > (1 << 24) || Nq < 0 || Nk < 0 || Nq > kMostRows || Nk > kMostRows ||
       (causal != 0 && causal != 1) || !scale_ok(softmax_scale))
     return CPATTN_ERR_INVALID_ARG;
   // Work items are numbered in an int.

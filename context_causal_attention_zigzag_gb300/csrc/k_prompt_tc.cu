@@ -82,7 +82,8 @@ constexpr int kBins = 1024;
 
 struct Plan {
   int nblocks;
-  int pad[63];
+  int next;  // items that CTAs have taken after their first
+  int pad[62];
 };
 
 __device__ __forceinline__ Block make_block(int q0, int nq, int k0, int nk, int at) {
@@ -102,7 +103,10 @@ __global__ void __launch_bounds__(1024) prompt_plan_kernel(const PromptArgs a, i
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   launch_dependents();
   s_bin[tid] = 0;
-  if (tid == 0) s_most = 1;
+  if (tid == 0) {
+    s_most = 1;
+    plan->next = 0;
+  }
   __syncthreads();
   int q0, nq, k0, nk, most = 1;
   bool bad = false;
@@ -159,6 +163,9 @@ __global__ void __launch_bounds__(1024) prompt_plan_kernel(const PromptArgs a, i
 // ---------------------------------------------------------------------------
 // The attention kernel.
 // ---------------------------------------------------------------------------
+constexpr int kFeed = 2;      // items handed out ahead
+constexpr int kReaders = 10;  // warps that read them
+
 template <int D>
 struct Cfg {
   static constexpr int kHalves = D / 64;
@@ -178,10 +185,13 @@ struct Cfg {
   static constexpr int kBarS = kBarEmpty + kSlots;
   static constexpr int kBarP = kBarS + 2 * kTurns;
   static constexpr int kBarO = kBarP + 2 * kTurns;
-  static constexpr int kBarDrain = kBarO + 2;
+  static constexpr int kBarFeedFull = kBarO + 2;           // [kFeed]
+  static constexpr int kBarFeedEmpty = kBarFeedFull + kFeed;
+  static constexpr int kBarDrain = kBarFeedEmpty + kFeed;
   static constexpr int kNumBars = kBarDrain + 1;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr int kSmemBytes = kOffMisc + 16 + 1024;  // + slack for 1024-B alignment
+  static constexpr int kOffFeed = (kOffMisc + 16 + 15) / 16 * 16;  // items, 32 bytes each
+  static constexpr int kSmemBytes = kOffFeed + kFeed * 32 + 1024;  // + slack for 1024-B alignment
 
   // Barrier and parity of query tile i's c-th step.
   static __device__ __forceinline__ int turn(int bar0, int i, uint32_t c) {
@@ -213,96 +223,107 @@ struct Work {
   int inner;          // items per block and kv head
 };
 
-// Walks the items of one CTA; the next item's block is fetched an item ahead.
-struct Items {
-  int nblocks, n_items, k, grp, Hkv, rows, inner;
-  const Block* list;
-  int q0, nq, k0, nk;  // the single sequence
-  Block next_block;
-  int next_g, next_sub;
-  bool next_ok;
-
-  __device__ __forceinline__ void fetch() {
-    const int grid = (int)gridDim.x, cta = (int)blockIdx.x;
-    const long long idx = (long long)k * grid + ((k & 1) ? (grid - 1 - cta) : cta);
-    next_ok = idx < n_items;
-    if (!next_ok) return;
-    int rank;
-    banded_item((int)idx, Hkv, nblocks, inner, grid, 0, next_g, rank, next_sub);
-    if (list != nullptr) {
-      const int4* p = reinterpret_cast<const int4*>(list + rank);
-      const int4 x = p[0];
-      next_block.qrow = x.x;
-      next_block.nrows = x.y;
-      next_block.krow = x.z;
-      next_block.nk = x.w;
-      next_block.diag = p[1].x;
-    } else {
-      next_block = make_block(q0, nq, k0, nk, (nblocks - 1 - rank) * rows);
+// The only item of a direct call's CTA: the warp sums the sequences' blocks, 32 at
+// a time, up to its own.
+__device__ __forceinline__ bool find_direct(const PromptArgs& a, const Work& w, Block& b, int& g,
+                                            int& h0) {
+  const int lane = threadIdx.x & 31, per = a.Hkv * w.inner;
+  const int mine = (int)blockIdx.x / per, sub = (int)blockIdx.x - mine * per;
+  g = sub / w.inner;
+  h0 = g * (a.H / a.Hkv) + (sub - g * w.inner) * (w.rows == kT ? 2 : 1);
+  int before = 0;
+  for (int r0 = 0; r0 < a.R; r0 += 32) {
+    int q0, k0, nk, n = 0, nb = 0;
+    if (r0 + lane < a.R) {
+      packed_rows(a.cu_q, r0 + lane, a.Nq, q0, n);
+      nb = (n + w.rows - 1) / w.rows;
     }
-  }
-  __device__ __forceinline__ void init(const PromptArgs& a, const Work& w) {
-    Hkv = a.Hkv;
-    grp = a.H / a.Hkv;
-    rows = w.rows;
-    inner = w.inner;
-    list = w.plan != nullptr ? w.list : nullptr;
-    if (w.direct) {
-      // The warp sums the sequences' blocks, 32 at a time, up to its own.
-      const int lane = threadIdx.x & 31, per = Hkv * inner;
-      const int mine = (int)blockIdx.x / per, sub = (int)blockIdx.x - mine * per;
-      next_g = sub / inner;
-      next_sub = sub - next_g * inner;
-      next_ok = false;
-      k = 1;  // no further item
-      n_items = 0;
-      int before = 0;
-      for (int r0 = 0; r0 < a.R; r0 += 32) {
-        int n = 0, nb = 0;
-        if (r0 + lane < a.R) {
-          packed_rows(a.cu_q, r0 + lane, a.Nq, q0, n);
-          nb = (n + rows - 1) / rows;
-        }
-        int upto = nb;
+    int upto = nb;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int u = __shfl_up_sync(0xffffffffu, upto, d);
-          if (lane >= d) upto += u;
-        }
-        const int at = mine - before;
-        const uint32_t found = __ballot_sync(0xffffffffu, at >= upto - nb && at < upto);
-        if (found != 0) {
-          const int src = __ffs(found) - 1;
-          const int skip = __shfl_sync(0xffffffffu, upto - nb, src);
-          packed_rows(a.cu_q, r0 + src, a.Nq, q0, nq);
-          packed_rows(a.cu_k, r0 + src, a.Nk, k0, nk);
-          next_block = make_block(q0, nq, k0, nk, (at - skip) * rows);
-          next_ok = true;
-          return;
-        }
-        before += __shfl_sync(0xffffffffu, upto, 31);
-      }
-      return;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += u;
     }
+    const int at = mine - before;
+    const uint32_t found = __ballot_sync(0xffffffffu, at >= upto - nb && at < upto);
+    if (found != 0) {
+      const int src = __ffs(found) - 1;
+      const int skip = __shfl_sync(0xffffffffu, upto - nb, src);
+      packed_rows(a.cu_q, r0 + src, a.Nq, q0, n);
+      packed_rows(a.cu_k, r0 + src, a.Nk, k0, nk);
+      b = make_block(q0, n, k0, nk, (at - skip) * w.rows);
+      return true;
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return false;
+}
+
+// One warp finds the items of a CTA and hands them to the others through shared
+// memory: finding one takes several divisions and dependent loads, which would
+// otherwise stand between two items of every role.
+struct Items {
+  const PromptArgs& a;
+  const Work& w;
+  int nblocks, n_items, k;
+  int band_size, band_items;   // the cost bands of banded_item
+  int q0, nq, k0, nk;          // the single sequence
+
+  __device__ __forceinline__ Items(const PromptArgs& a_, const Work& w_) : a(a_), w(w_) {
+    k = 0;
+    const int per = a.Hkv * w.inner;
     if (w.plan != nullptr) {
       nblocks = w.plan->nblocks;
     } else {
       packed_rows(a.cu_q, 0, a.Nq, q0, nq);
       packed_rows(a.cu_k, 0, a.Nk, k0, nk);
-      nblocks = (nq + rows - 1) / rows;
+      nblocks = (nq + w.rows - 1) / w.rows;
     }
-    n_items = nblocks * Hkv * inner;
-    k = 0;
-    fetch();
+    n_items = nblocks * per;
+    if (n_items > 0) {
+      const int nb = cost_band_count(nblocks * w.inner, nblocks, gridDim.x, 0);
+      band_size = (nblocks + nb - 1) / nb;
+      band_items = band_size * per;
+    }
   }
-  // The item: its block, kv head g and, per query tile i, head and first row.
+  // The next item: its block, kv head g and first query head h0.  A planned call
+  // takes them in turn, largest first, whichever CTA is free; a single sequence
+  // is dealt in snake order (its items' costs fall evenly).
   __device__ __forceinline__ bool next(Block& b, int& g, int& h0) {
-    if (!next_ok) return false;
-    b = next_block;
-    g = next_g;
-    h0 = next_g * grp + next_sub * (rows == kT ? 2 : 1);
-    ++k;
-    fetch();
+    const int grp = a.H / a.Hkv, heads = w.rows == kT ? 2 : 1;
+    int idx;
+    if (w.plan != nullptr) {
+      idx = blockIdx.x;
+      if (k++ > 0) {
+        if ((threadIdx.x & 31) == 0) idx = gridDim.x + atomicAdd(&const_cast<Plan*>(w.plan)->next, 1);
+        idx = __shfl_sync(0xffffffffu, idx, 0);
+      }
+    } else {
+      const long long x = (long long)k * gridDim.x +
+                          ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      ++k;
+      idx = x < n_items ? (int)x : n_items;
+    }
+    if (idx >= n_items) return false;
+    const int band = idx / band_items;
+    int rest = idx - band * band_items;
+    const int here = min(band_size, nblocks - band * band_size) * w.inner;  // of a kv head
+    g = rest / here;
+    rest -= g * here;
+    const int r = rest / w.inner;
+    const int rank = band * band_size + r;
+    h0 = g * grp + (rest - r * w.inner) * heads;
+    if (w.plan != nullptr) {
+      const int4* p = reinterpret_cast<const int4*>(w.list + rank);
+      const int4 x = p[0];
+      b.qrow = x.x;
+      b.nrows = x.y;
+      b.krow = x.z;
+      b.nk = x.w;
+      b.diag = p[1].x;
+    } else {
+      b = make_block(q0, nq, k0, nk, (nblocks - 1 - rank) * w.rows);
+    }
     return true;
   }
 };
@@ -344,6 +365,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       mbar_init(bar(C::kBarO + i), 1);
     }
+    for (int f = 0; f < kFeed; ++f) {
+      mbar_init(bar(C::kBarFeedFull + f), 1);
+      mbar_init(bar(C::kBarFeedEmpty + f), kReaders);
+    }
     mbar_init(bar(C::kBarDrain), 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -365,9 +390,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         atomicExch(a.err, kErrBadTables);
   }
 
-  Items items;
+  int4* slots = reinterpret_cast<int4*>(smem + C::kOffFeed);
   Block b;
   int g, h0;
+  // The next item, for one of the reading warps: from the shared ring, until one
+  // that says there is none; of a direct call each warp finds the only one.
+  uint32_t fed = 0;
+  auto next_item = [&](bool& ok) {
+    if (w.direct) return fed++ == 0 && find_direct(a, w, b, g, h0);
+    const uint32_t s = fed % kFeed;
+    if (!__all_sync(0xffffffffu,
+                    mbar_wait_short(bar(C::kBarFeedFull + s), (fed / kFeed) & 1, wc))) {
+      ok = false;
+      return false;
+    }
+    ++fed;
+    const int4 x = slots[2 * s], y = slots[2 * s + 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(C::kBarFeedEmpty + s));
+    b.qrow = x.x;
+    b.nrows = x.y;
+    b.krow = x.z;
+    b.nk = x.w;
+    b.diag = y.x;
+    g = y.y;
+    h0 = y.z;
+    return y.w != 0;
+  };
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA
     const bool leader = elect_one();
@@ -381,8 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     uint32_t seq = 0, q_armed[2] = {0, 0};  // ring entries and Q tiles asked for
     bool ok = true;
-    items.init(a, w);
-    while (ok && items.next(b, g, h0)) {
+    while (ok && next_item(ok)) {
       int nt = 0;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -450,8 +498,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma_commit(bar(C::turn(C::kBarS, i, s_n[i])));
     };
     auto values = [&](int i, uint32_t vn, uint32_t accumulate) {  // O_i += P_i V
-      const uint64_t bv = sdesc_advance(d_v, slot_off(vn));
       const uint32_t p = tmem + col_s<D>(i, vn / 2);
+      const uint64_t bv = sdesc_advance(d_v, slot_off(vn));
 #pragma unroll
       for (int kk = 0; kk < kT / 16; ++kk)
         mma_ts(tmem + col_o<D>(i), p + kk * 8, sdesc_advance(bv, kk * 2048), kIdescPV,
@@ -473,9 +521,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // The next item with keys, as the tiles its two query tiles see.
     int cur[2], nxt[2] = {0, 0};
-    items.init(a, w);
-    auto next_item = [&](int (&nt)[2]) {
-      while (items.next(b, g, h0)) {
+    auto next_tiles = [&](int (&nt)[2]) {
+      while (next_item(ok)) {
         nt[0] = key_tiles(b, a.causal, 0, kT);
         nt[1] = key_tiles(b, a.causal, row_step, kT);
         if (nt[0] > 0 || nt[1] > 0) return true;
@@ -483,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       nt[0] = nt[1] = 0;
       return false;
     };
-    bool have = next_item(cur);
+    bool have = next_tiles(cur);
     if (have) {
       for (int i = 0; ok && i < 2; ++i)
         if (cur[i] > 0) ok = first_scores(i, 0, cur[i]);
@@ -492,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // K(m) is ring entry 2 * kv_it, V(m) entry 2 * kv_it + 1.  Behind each query
     // tile's product come its next scores (D = 64: before it).
     while (ok && have) {
-      const bool more = next_item(nxt);
+      const bool more = next_tiles(nxt);
       const int nt = max(cur[0], cur[1]);
       for (int m = 0; m + 1 < nt; ++m) {
         const uint32_t vn = 2 * kv_it + 1, nkn = 2 * kv_it + 2;
@@ -577,6 +624,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (leader) mma_commit(bar(C::kBarDrain));
       mbar_drain(bar(C::kBarDrain), 0);
     }
+  } else if (warp == 2 && !w.direct) {
+    // ---------------------------------------------------------------- items
+    Items items(a, w);
+    bool some = true;
+    for (uint32_t k = 0; some; ++k) {
+      const uint32_t s = k % kFeed;
+      if (!__all_sync(0xffffffffu, mbar_wait_short(bar(C::kBarFeedEmpty + s),
+                                                   ((k / kFeed) & 1) ^ 1, wc)))
+        break;
+      some = items.next(b, g, h0);
+      if (lane == 0) {
+        slots[2 * s] = make_int4(b.qrow, b.nrows, b.krow, b.nk);
+        slots[2 * s + 1] = make_int4(b.diag, g, h0, some);
+        mbar_arrive(bar(C::kBarFeedFull + s));
+      }
+      __syncwarp();
+    }
   } else if (warp >= 4) {
     // -------------------------------------------------------------- softmax
     const int ti = (warp - 4) >> 2;  // query tile of this warpgroup
@@ -587,8 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sl2 = a.scale_log2;
     uint32_t step = 0, o_ph = 0, kv_it = 0;
     bool ok = true;
-    items.init(a, w);
-    while (ok && items.next(b, g, h0)) {
+    while (ok && next_item(ok)) {
       const int nt0 = key_tiles(b, a.causal, 0, kT), nt1 = key_tiles(b, a.causal, row_step, kT);
       const int nt = ti == 0 ? nt0 : nt1;
       const int at = ti * row_step + row;  // row within the block
