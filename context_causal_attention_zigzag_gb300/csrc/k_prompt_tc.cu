@@ -856,11 +856,21 @@ Way way(const PromptArgs& a, const TreeArgs& t, int sms) {
   const int64_t items = ((int64_t)a.Nq / kT + a.R) * (G % 2 == 0 ? a.H / 2 : a.H);
   const int64_t rows = (int64_t)a.Nq * G / a.R, keys = a.Nk / a.R;
   Way by = items <= sms ? kDirect : kSorted;
-  const float tiles = (float)(keys / kT + 1);
+  const float tiles = (float)(keys / kT + 1);  // of the longest rows
   float us = by == kDirect ? 8.f + 1.5f * tiles : 14.f + items * (3.f + 1.6f * tiles) / sms;
-  if (rows <= kT ? keys > 512 || items > sms : rows <= 8 * kT && keys >= 2048 && items <= sms) {
-    by = kLine;
-    us = line_attn_us(t, keys);
+  if (rows <= kT) {
+    if (keys > 512 || items > sms) {
+      by = kLine;
+      us = line_attn_us(t, keys);
+    }
+  } else if (by == kDirect) {
+    // Whether the CTAs without an item would help more than the sharing costs.
+    const float mean = a.causal && a.Nk == a.Nq ? 0.5f * tiles : tiles;
+    const float line = 20.f + 1.7f * mean * a.Nq * a.H / (2 * kT) / sms;
+    if (line < us) {
+      by = kLine;
+      us = line;
+    }
   }
   // Under the causal rule a row sees about the keys in front of its sequence's
   // queries and half of those among them.
