@@ -519,28 +519,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++s_n[i];
       return true;
     };
-    // The next item with keys, as the tiles its two query tiles see.
-    int cur[2], nxt[2] = {0, 0};
+    // An item as the tiles its two query tiles see.  Items without keys are met
+    // in turn like the others: looking past them for the next one would wait for
+    // roles that are still at this one.
+    int cur[2], nxt[2];
     auto next_tiles = [&](int (&nt)[2]) {
-      while (next_item(ok)) {
-        nt[0] = key_tiles(b, a.causal, 0, kT);
-        nt[1] = key_tiles(b, a.causal, row_step, kT);
-        if (nt[0] > 0 || nt[1] > 0) return true;
-      }
-      nt[0] = nt[1] = 0;
-      return false;
+      const bool some = next_item(ok);
+      nt[0] = some ? key_tiles(b, a.causal, 0, kT) : 0;
+      nt[1] = some ? key_tiles(b, a.causal, row_step, kT) : 0;
+      return some;
     };
-    bool have = next_tiles(cur);
-    if (have) {
-      for (int i = 0; ok && i < 2; ++i)
-        if (cur[i] > 0) ok = first_scores(i, 0, cur[i]);
-      if (ok && leader) mma_commit(bar(C::kBarEmpty + 0));
-    }
+    bool have = next_tiles(cur), started = false;  // started: cur's first scores are issued
     // K(m) is ring entry 2 * kv_it, V(m) entry 2 * kv_it + 1.  Behind each query
     // tile's product come its next scores (D = 64: before it).
     while (ok && have) {
       const bool more = next_tiles(nxt);
       const int nt = max(cur[0], cur[1]);
+      if (nt > 0 && !started) {
+        const uint32_t kn = 2 * kv_it;
+        for (int i = 0; ok && i < 2; ++i)
+          if (cur[i] > 0) ok = first_scores(i, kn, cur[i]);
+        if (ok && leader) mma_commit(bar(C::kBarEmpty + kn % kSlots));
+        if (!ok) break;
+      }
+      started = nt > 0 && max(nxt[0], nxt[1]) > 0;
       for (int m = 0; m + 1 < nt; ++m) {
         const uint32_t vn = 2 * kv_it + 1, nkn = 2 * kv_it + 2;
         if (!full(vn)) {
@@ -593,28 +595,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++kv_it;
       }
       if (!ok) break;
-      // The item's last key tile: behind its products come the next item's first
-      // scores, so that the softmax finds them when it leaves the epilogue.
-      const uint32_t vn = 2 * kv_it + 1, nkn = 2 * kv_it + 2;
-      ok = full(vn);
+      if (nt > 0) {
+        // The item's last key tile: behind its products come the next item's first
+        // scores, so that the softmax finds them when it leaves the epilogue.
+        const uint32_t vn = 2 * kv_it + 1, nkn = 2 * kv_it + 2;
+        ok = full(vn);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (ok && nt == cur[i]) {
-          ok = wwait(bar(C::turn(C::kBarP, i, p_n[i])), C::parity(p_n[i]));
-          ++p_n[i];
-          tc_fence_after();
-          if (ok && leader) {
-            values(i, vn, nt > 1);
-            mma_commit(bar(C::kBarO + i));
+        for (int i = 0; i < 2; ++i) {
+          if (ok && nt == cur[i]) {
+            ok = wwait(bar(C::turn(C::kBarP, i, p_n[i])), C::parity(p_n[i]));
+            ++p_n[i];
+            tc_fence_after();
+            if (ok && leader) {
+              values(i, vn, nt > 1);
+              mma_commit(bar(C::kBarO + i));
+            }
           }
+          if (ok && nxt[i] > 0) ok = first_scores(i, nkn, nxt[i]);
         }
-        if (ok && nxt[i] > 0) ok = first_scores(i, nkn, nxt[i]);
+        if (ok && leader) {
+          mma_commit(bar(C::kBarEmpty + vn % kSlots));
+          if (started) mma_commit(bar(C::kBarEmpty + nkn % kSlots));
+        }
+        ++kv_it;
       }
-      if (ok && leader) {
-        mma_commit(bar(C::kBarEmpty + vn % kSlots));
-        if (more) mma_commit(bar(C::kBarEmpty + nkn % kSlots));
-      }
-      ++kv_it;
       cur[0] = nxt[0];
       cur[1] = nxt[1];
       have = more;

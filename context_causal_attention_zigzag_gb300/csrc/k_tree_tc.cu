@@ -182,7 +182,10 @@ struct Walk {
           if (++p.g == a.Hkv) {
             p.g = 0;
             do {
-              ++p.r;
+              if (++p.r >= a.R) {  // only if the lengths changed under the call
+                left = 0;
+                return false;
+              }
               load_req<kPaged>(a, p.r, p.x);
             } while (p.x.n == 0);
             items = items_of(p.x, span);

@@ -114,6 +114,11 @@ PROMPTS = [
     ([37, 2, 130] * 44, None, 16, 8, 64),                    # many sequences, sorted
     ([37, 0, 130] * 44, [20, 5, 140] * 44, 12, 12, 128),
     ([3700], None, 64, 32, 64),                              # one long one
+    ([100] * 64, [0, 0, 0, 90] * 16, 16, 8, 64),             # runs of items without keys
+    ([300] * 40, [40, 0, 0, 0] * 10, 16, 16, 128),
+    ([5], [0], 4, 2, 128),
+    ([70, 0, 3], [0, 0, 0], 4, 4, 64),
+    ([0, 0, 7] + [0] * 3000 + [20, 1], None, 4, 2, 64),      # mostly empty sequences
 ]
 
 
@@ -268,6 +273,9 @@ TREES = [
     ([20000], [3], 4, 2, 128, 128, True),
     ([5] * 200, [1] * 200, 2, 1, 64, 16, False),
     ([40000], [1], 2, 1, 64, 384, False),
+    ([300, 7, 900, 0, 64], [1, 0, 2, 0, 5], 8, 2, 128, 32, True),   # requests without new tokens
+    ([60] * 30, [0, 3] * 15, 4, 2, 64, 16, False),
+    ([400] * 40, [64] * 40, 8, 2, 64, 64, True),
 ]
 
 
@@ -587,6 +595,60 @@ def test_two_captured_steps_replay_with_new_lengths():
         a.check(ca)
         b.check(cb)
     assert cpa.device_status() == 0
+
+
+def test_a_planned_call_captured_once_replays_with_other_lengths():
+    H, Hkv, D, R = 16, 8, 64, 130
+    cu = ints([0] * (R + 1))
+    q = normal(1, 4000, H, D, dtype=torch.float16)
+    k, v = (normal(s, 4000, Hkv, D, dtype=torch.float16) for s in (2, 3))
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.stream(stream):
+        cpa.prompt_attention(q, k, v, cu)
+    stream.synchronize()
+    with torch.cuda.graph(graph, stream=stream):
+        out, lse = cpa.prompt_attention(q, k, v, cu)
+    for seed in range(3):
+        g = torch.Generator().manual_seed(seed)
+        lens = torch.randint(0, 31, (R,), generator=g).tolist()
+        if seed == 1:
+            lens = [0] * 100 + [133] * 30
+        cu.copy_(ints(offsets(lens)))
+        n = sum(lens)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        o, l, to, tl = prompt_reference(q[:n], k[:n], v[:n], lens, lens, True)
+        check(out[:n], o, to, "out")
+        check(lse[:, :n], l, tl, "lse")
+    assert cpa.device_status() == 0
+
+
+@pytest.mark.parametrize("wider", [1, 20000])  # small: CUDA cores; wide: tensor cores
+def test_a_cache_whose_offsets_pass_32_bits(wider):
+    # Pages 2^25 values apart: the last ones lie more than 2^32 bytes, and more
+    # than 2^31 values, from the first.
+    H, Hkv, D, P, pages, stride = 8, 2, 128, 16, 80, 1 << 25
+    rows = P * Hkv * D
+    buffers = [torch.empty((pages - 1) * stride + rows, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    kc, vc = (b.as_strided((pages, P, Hkv, D), (stride, Hkv * D, D, 1)) for b in buffers)
+    ctx, new = [1200, 5], [1, 1]
+    k, v = (normal(s, 1201 + 6, Hkv, D, dtype=torch.bfloat16) for s in (2, 3))
+    ids = torch.randperm(pages, generator=torch.Generator().manual_seed(3), dtype=torch.int32)[:78].tolist()
+    table = torch.full((2, 77 + wider), -1, dtype=torch.int32)
+    table[0, :76], table[1, 0] = torch.tensor(ids[:76], dtype=torch.int32), ids[76]
+    table = table.to(DEV)
+    slots = torch.cat([table[r].long()[pos // P] * P + pos % P
+                       for r, pos in enumerate((torch.arange(1201, device=DEV), torch.arange(6, device=DEV)))])
+    cpa.cache_write(k, v, kc, vc, slots)
+    q = normal(4, 2, H, D, dtype=torch.bfloat16)
+    out, lse = cpa.tree_attention(q, kc, vc, table, ints(ctx), ints([0, 1, 2]))
+    assert cpa.device_status() == 0
+    for r, at in enumerate((slice(0, 1201), slice(1201, 1207))):
+        n = at.stop - at.start
+        o, l, to, tl = plain(q[r:r + 1], k[at], v[at], torch.ones(1, n, dtype=torch.bool, device=DEV))
+        check(out[r:r + 1], o, to, "out")
+        check(lse[:, r:r + 1], l, tl, "lse")
 
 
 def test_results_do_not_change_from_run_to_run():
