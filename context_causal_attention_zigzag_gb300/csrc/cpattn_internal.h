@@ -386,7 +386,7 @@ struct PromptArgs {
 // Rows [first, first + n) of one sequence from its offsets, held to [0, total]
 // whatever they say; false when they break the rules (0 first, never falling,
 // never past the end).
-__device__ __forceinline__ bool packed_rows(const int* cu, int r, int total, int& first, int& n) {
+__host__ __device__ inline bool packed_rows(const int* cu, int r, int total, int& first, int& n) {
   const int a = cu[r], b = cu[r + 1];
   const bool ok = a >= 0 && b >= a && b <= total && (r > 0 || a == 0);
   first = a < 0 ? 0 : (a > total ? total : a);
@@ -429,7 +429,7 @@ struct Req {
 };
 
 template <bool kPaged>
-__device__ __forceinline__ bool load_req(const TreeArgs& a, int r, Req& x) {
+__host__ __device__ inline bool load_req(const TreeArgs& a, int r, Req& x) {
   bool ok = packed_rows(a.cu, r, a.N, x.q0, x.n);
   if constexpr (kPaged) {
     const int ctx = a.ctx[r];
