@@ -66,7 +66,7 @@ __device__ __forceinline__ void block_sums(long long& a, long long& b, long long
 }
 
 // Last index i in [0, n) with pre[i] <= x (pre[0] <= x, non-decreasing).
-__device__ __forceinline__ int last_at_or_below(const long long* pre, int n, long long x) {
+__device__ __forceinline__ int last_at_or_below(const uint32_t* pre, int n, uint32_t x) {
   int lo = 0, hi = n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -80,7 +80,9 @@ __device__ __forceinline__ int last_at_or_below(const long long* pre, int n, lon
 
 __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const TablesArgs a) {
   __shared__ long long part[3][32];
-  __shared__ long long s_tok[kTabThreads], s_page[kTabThreads];  // exclusive sums of the chunk
+  // Exclusive sums within the chunk, in 32 bits (sums that pass them are an
+  // error already; they stay in order).
+  __shared__ uint32_t s_tok[kTabThreads], s_page[kTabThreads];
   __shared__ int s_ctx[kTabThreads];
   const int tid = threadIdx.x;
   const long long P = a.page_size;
@@ -102,8 +104,8 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const TablesAr
     }
     long long tok = n, page = (ctx + n + P - 1) / P - (ctx + P - 1) / P, ntok, npage;
     block_sums(tok, page, part, ntok, npage);
-    s_tok[tid] = tok0 + tok;
-    s_page[tid] = page0 + page;
+    s_tok[tid] = (uint32_t)(tok < 0xffffffffll ? tok : 0xffffffffll);
+    s_page[tid] = (uint32_t)(page < 0xffffffffll ? page : 0xffffffffll);
     s_ctx[tid] = (int)ctx;
     if (blockIdx.x == 0 && r < a.R)
       a.cu[r] = (int)(tok0 + tok < INT_MAX ? tok0 + tok : INT_MAX);
@@ -112,8 +114,9 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const TablesAr
     long long x = mine < page0 ? mine + (page0 - mine + stride - 1) / stride * stride : mine;
     const long long page_end = page0 + npage < a.num_free ? page0 + npage : a.num_free;
     for (; x < page_end; x += stride) {
-      const int i = last_at_or_below(s_page, nr, x);
-      const long long col = (s_ctx[i] + P - 1) / P + (x - s_page[i]);
+      const int i = last_at_or_below(s_page, nr, (uint32_t)(x - page0));
+      const long long col =
+          ((uint32_t)s_ctx[i] + (uint32_t)P - 1) / (uint32_t)P + (x - page0 - s_page[i]);
       if (col < a.width)
         a.table[(int64_t)(r0 + i) * a.table_stride + col] = a.free_pages[x];
       else
@@ -124,20 +127,20 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const TablesAr
     x = mine < tok0 ? mine + (tok0 - mine + stride - 1) / stride * stride : mine;
     const long long tok_end = tok0 + ntok < a.num_slots ? tok0 + ntok : a.num_slots;
     for (; x < tok_end; x += stride) {
-      const int i = last_at_or_below(s_tok, nr, x);
-      const long long c = s_ctx[i], pos = c + (x - s_tok[i]);
-      const long long col = pos / P, have = (c + P - 1) / P;
+      const int i = last_at_or_below(s_tok, nr, (uint32_t)(x - tok0));
+      const uint32_t c = s_ctx[i], pos = c + ((uint32_t)(x - tok0) - s_tok[i]);
+      const uint32_t p = (uint32_t)P, col = pos / p, have = (c + p - 1) / p;
       long long id = -1;
-      if (col < a.width) {
+      if (col < (uint32_t)a.width) {
         if (col < have) {
           id = a.table[(int64_t)(r0 + i) * a.table_stride + col];
         } else {
-          const long long f = s_page[i] + (col - have);
+          const long long f = page0 + s_page[i] + (col - have);
           if (f < a.num_free) id = a.free_pages[f];
         }
       }
       if (id < 0) bad = true;
-      a.slots[x] = id < 0 ? -1 : id * P + (pos - col * P);
+      a.slots[x] = id < 0 ? -1 : id * P + (pos - col * p);
     }
     tok0 += ntok;
     page0 += npage;
@@ -206,7 +209,7 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const CacheWriteArgs a
 }  // namespace
 
 cudaError_t launch_page_tables(const TablesArgs& a, cudaStream_t stream) {
-  const int64_t want = (a.num_slots + 4 * kTabThreads - 1) / (4 * kTabThreads);
+  const int64_t want = (a.num_slots + kTabThreads - 1) / kTabThreads;
   const int sms = sm_count();
   const int grid = (int)(want < 1 ? 1 : (want < sms ? want : sms));
   page_tables_kernel<<<grid, kTabThreads, 0, stream>>>(a);
