@@ -31,6 +31,14 @@ bool check_rows(const void* p, int64_t stride, int heads, int D) {
          stride < ((int64_t)1 << 38);
 }
 
+// Whether `rows` rows of [heads, D] 16-bit values, `stride` apart, and n bytes
+// at `out` share memory.
+bool overlaps(const void* p, int64_t stride, int64_t rows, int heads, int D, const void* out,
+              int64_t n) {
+  const char *a = static_cast<const char*>(p), *b = static_cast<const char*>(out);
+  return a < b + n && b < a + 2 * ((rows - 1) * stride + (int64_t)heads * D);
+}
+
 bool page_size_ok(int P) {
   return P == 16 || P == 32 || P == 64 || (P >= 128 && P <= 1024 && P % 128 == 0);
 }
@@ -165,6 +173,7 @@ int cpattn_tree_attn(const void* q, int64_t q_stride, const void* k_cache, const
   if (!aligned(block_table, 4) || !aligned(ctx_lens, 4) || !aligned(cu_new, 4) ||
       !aligned(tree, 8))
     return CPATTN_ERR_INVALID_ARG;
+  if (overlaps(q, q_stride, N, H, D, out, 2 * (int64_t)N * H * D)) return CPATTN_ERR_INVALID_ARG;
   if (!workspace || !aligned(workspace, 256) ||
       workspace_bytes < tree_workspace_bytes(N, H, Hkv, D))
     return CPATTN_ERR_WORKSPACE;
@@ -221,6 +230,11 @@ int cpattn_prompt_attn(const void* q, int64_t q_stride, const void* k, int64_t k
       !aligned(lse, 4) || !cu_q || !cu_k || !aligned(cu_q, 4) || !aligned(cu_k, 4))
     return CPATTN_ERR_INVALID_ARG;
   if (Nk > 0 && (!check_rows(k, k_stride, Hkv, D) || !check_rows(v, v_stride, Hkv, D)))
+    return CPATTN_ERR_INVALID_ARG;
+  const int64_t out_bytes = 2 * (int64_t)Nq * H * D;
+  if (overlaps(q, q_stride, Nq, H, D, out, out_bytes) ||
+      (Nk > 0 && (overlaps(k, k_stride, Nk, Hkv, D, out, out_bytes) ||
+                  overlaps(v, v_stride, Nk, Hkv, D, out, out_bytes))))
     return CPATTN_ERR_INVALID_ARG;
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < prompt_workspace_bytes(R, Nq, H, D))
     return CPATTN_ERR_WORKSPACE;

@@ -13,9 +13,17 @@
 // neighbouring heads: both see the same keys, so no tile is loaded or
 // multiplied for one of them alone, and an item is as small as 128 rows (a
 // short prompt fills it).  With an odd number they are 256 rows of one head.
-// Items are sorted by their number of key tiles (prompt_plan_kernel; a single
-// sequence needs no sorting) and dealt in cost bands in snake order, as in the
-// ring forward (banded_item).
+// Items are sorted by their number of key tiles (prompt_plan_kernel) and taken in
+// that order, in the cost bands of the ring forward (banded_item), by whichever
+// CTA is free; one sequence needs no sorting and is dealt in snake order; a call
+// of no more items than SMs is neither (way()).
+//
+// What bounds it: from some hundred tokens on the rate of the tensor cores'
+// instructions (16 SS and 16 TS of 128 x 128 x 16 per key tile and item, 1.52 us at
+// 1.9 GHz against 1.57-1.62 measured per tile), below that what an item costs
+// around its tiles (about 2.5 us: the last product, the epilogue, the first
+// softmax) and the start (6-8 us).  16384 tokens, H = 32, Hkv = 8, D = 128: 1.33-1.43
+// ms (1.54-1.65 PFLOP/s); 16 prompts of 100-2000: 0.223 ms (1.07 PFLOP/s).
 //
 // Sequences start at any row: TMA takes any first row, and a tile's rows
 // behind the sequence's end belong to others.  Their scores are replaced by
@@ -26,7 +34,8 @@
 // Roles of a CTA (384 threads) as in the ring forward: warp 0 loads (Q tiles once
 // per item, K(j), V(j) in consecutive slots of one ring), warp 1 owns TMEM and
 // issues the products S_i = Q_i K^T (SS) and O_i += P_i V (TS, P in TMEM over
-// S), warps 4-7 and 8-11 are the softmax of tile 0 and 1, one thread per row.
+// S), warp 2 finds the items, warps 4-7 and 8-11 are the softmax of tile 0 and 1,
+// one thread per row.
 // MMA order per key tile: PV0(j), S0(j+1), PV1(j), S1(j+1), across items too, so
 // that the next item's scores are ready when the softmax leaves the epilogue.
 // (An epilogue in four warps of its own held the products up: at 512 threads

@@ -564,6 +564,11 @@ CPATTN_API int cpattn_attention_host_docs(const void* q, const void* k, const vo
  * page_size] at p % page_size; the slot of that position is page * page_size
  * + p % page_size.  16-byte aligned pointers, strides multiples of 8, page_size *
  * num_pages below 2^31.
+ *
+ * Outputs and workspace overlap no input (an out that overlaps q, k or v is
+ * refused).  A call's kernels follow one another on its stream, and can be
+ * captured into a graph whose replays see the lengths and tables of their time;
+ * make the first such call on a device before any capture.
  */
 
 /*

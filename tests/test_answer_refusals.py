@@ -21,10 +21,11 @@ TABLES = dict(ctx=fake, new=fake, R=2, P=16, free=fake, num_free=4, table=fake, 
 CACHE = dict(pages=8, P=16, ps=16 * 2 * 64, ts=2 * 64, hs=64)
 WRITE = dict(k=fake, ks=128, v=fake, vs=128, slots=fake, N=4, kc=fake, vc=fake, **CACHE, Hkv=2, D=64,
              dtype=1, stream=null)
+far = ctypes.c_void_p(0x10000)
 TREE = dict(q=fake, qs=256, kc=fake, vc=fake, **CACHE, table=fake, width=4, stride=4, ctx=fake,
-            cu=fake, tree=null, out=fake, lse=fake, R=2, N=4, H=4, Hkv=2, D=64, dtype=1, scale=0.0,
+            cu=fake, tree=null, out=far, lse=fake, R=2, N=4, H=4, Hkv=2, D=64, dtype=1, scale=0.0,
             ws=fake, wb=1 << 30, stream=null)
-PROMPT = dict(q=fake, qs=256, k=fake, ks=128, v=fake, vs=128, cu_q=fake, cu_k=fake, out=fake,
+PROMPT = dict(q=fake, qs=256, k=fake, ks=128, v=fake, vs=128, cu_q=fake, cu_k=fake, out=far,
               lse=fake, R=2, Nq=4, Nk=4, H=4, Hkv=2, D=64, causal=1, dtype=1, scale=0.0, ws=fake,
               wb=1 << 30, stream=null)
 
@@ -65,6 +66,14 @@ def test_tree_attention_refuses(changes):
     dict(out=null), dict(lse=null), dict(scale=float("nan"))])
 def test_prompt_attention_refuses(changes):
     assert call("cpattn_prompt_attn", PROMPT, **changes) == E
+
+
+def test_outputs_that_overlap_inputs_are_refused():
+    big, end = ctypes.c_void_p(0x100000), ctypes.c_void_p(0x100000 + 2 * 3 * 256 + 2 * 4 * 64 - 16)
+    assert call("cpattn_tree_attn", TREE, q=big, out=end) == E
+    assert call("cpattn_tree_attn", TREE, q=big, out=big) == E
+    for name, last in (("q", end), ("k", ctypes.c_void_p(0x100000 + 2 * 4 * 128 - 16)), ("v", big)):
+        assert call("cpattn_prompt_attn", PROMPT, **{name: big, "out": last}) == E, name
 
 
 def test_float32_is_unsupported():

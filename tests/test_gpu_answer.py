@@ -359,6 +359,25 @@ def test_tree_attention_reports_bad_pages_and_lengths(wider):
     assert cpa.device_status() == 0
 
 
+@pytest.mark.parametrize("wider", [1, 300])
+def test_requests_that_share_pages(wider):
+    # Two requests with the same first pages (a common prompt), each with its own
+    # behind them; the same request twice gives the same result twice.
+    cache = Cache([100, 100, 100], [3, 3, 3], 2, 128, 16, torch.bfloat16, wider=wider)
+    cache.table[1, :4] = cache.table[0, :4]
+    cache.table[2] = cache.table[0]
+    for own in (cache.K, cache.V):
+        own[1][:64] = own[0][:64]
+        own[2] = own[0]
+    q = normal(4, 9, 8, 128, dtype=torch.bfloat16)
+    q[6:] = q[:3]
+    out, lse = run_tree(q, cache)
+    o, l, to, tl = tree_reference(q, cache)
+    check(out, o, to, "out")
+    check(lse, l, tl, "lse")
+    assert cpa.device_status() == 0
+
+
 @pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("N,Hkv,D,P,order", [(1, 8, 128, 64, "tokens"), (37, 2, 64, 16, "heads"),
                                              (300, 3, 128, 384, "interleaved"), (1000, 1, 64, 128, "tokens")])
