@@ -189,12 +189,12 @@ struct Cfg {
   static constexpr int kBarEmpty = kBarFull + kSlots;
   // Per query tile.  With a third S buffer a tile's scores and weights run one
   // step ahead of their product, so two barriers take turns: a single one could
-  // pass two phases before they are seen.
+  // be a phase behind or ahead, and its parity pass for the one waited for.
   static constexpr int kTurns = D == 128 ? 1 : 2;
   static constexpr int kBarS = kBarEmpty + kSlots;
   static constexpr int kBarP = kBarS + 2 * kTurns;
   static constexpr int kBarO = kBarP + 2 * kTurns;
-  static constexpr int kBarFeedFull = kBarO + 2;           // [kFeed]
+  static constexpr int kBarFeedFull = kBarO + 2 * kTurns;  // [kFeed]
   static constexpr int kBarFeedEmpty = kBarFeedFull + kFeed;
   static constexpr int kBarDrain = kBarFeedEmpty + kFeed;
   static constexpr int kNumBars = kBarDrain + 1;
@@ -371,8 +371,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = 0; t < C::kTurns; ++t) {
         mbar_init(bar(C::turn(C::kBarS, i, t)), 1);
         mbar_init(bar(C::turn(C::kBarP, i, t)), 128);
+        mbar_init(bar(C::turn(C::kBarO, i, t)), 1);
       }
-      mbar_init(bar(C::kBarO + i), 1);
     }
     for (int f = 0; f < kFeed; ++f) {
       mbar_init(bar(C::kBarFeedFull + f), 1);
@@ -569,7 +569,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             if (leader) {
               values(i, vn, m > 0);
-              if (D == 64 || m + 1 == cur[i]) mma_commit(bar(C::kBarO + i));
+              if (D == 64 || m + 1 == cur[i])
+                mma_commit(bar(C::turn(C::kBarO, i, p_n[i] - 1)));
             }
           }
           return true;
@@ -617,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             if (ok && leader) {
               values(i, vn, nt > 1);
-              mma_commit(bar(C::kBarO + i));
+              mma_commit(bar(C::turn(C::kBarO, i, p_n[i] - 1)));
             }
           }
           if (ok && nxt[i] > 0) ok = first_scores(i, nkn, nxt[i]);
@@ -669,6 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int nt = ti == 0 ? nt0 : nt1;
       const int at = ti * row_step + row;  // row within the block
       const int end = a.causal ? min(b.nk, b.diag + at) : b.nk;  // keys that the row sees
+      const bool live = at < b.nrows;
       float m = -INFINITY, l = 0.f;
       for (int t = 0; t < nt; ++t) {
         const int see = end - t * kT;  // visible columns of the tile
@@ -704,7 +706,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float m_tile = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * sl2;
         const float m_new = fmaxf(m, m_tile);
-        const bool need = m_new > m + kRescaleThreshold;
+        // Only the sequence's own rows have a say: a rescale changes the rounding.
+        const bool need = live && m_new > m + kRescaleThreshold;
         const bool rescale = __any_sync(0xffffffffu, need);
         float alpha = 1.f;
         if (rescale) {
@@ -736,7 +739,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           // next one is issued only after the P barrier below.
           if (D == 64) {
             if (!__all_sync(0xffffffffu,
-                            mbar_wait_short(bar(C::kBarO + ti), (step - 1) & 1, wc))) {
+                            mbar_wait_short(bar(C::turn(C::kBarO, ti, step - 1)),
+                                            C::parity(step - 1), wc))) {
               ok = false;
               break;
             }
@@ -781,7 +785,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       kv_it += max(nt0, nt1);
       // ------------------------------------------------------------ epilogue
-      const bool live = at < b.nrows;
       const int64_t qrow = b.qrow + at;
       const int head = h0 + ti * head_step;
       uint4* op = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
@@ -794,8 +797,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         continue;
       }
-      if (D == 64) o_ph = (step - 1) & 1;
-      if (!__all_sync(0xffffffffu, mbar_wait_short(bar(C::kBarO + ti), o_ph, wc))) {
+      // D = 64: of the last product.
+      if (!__all_sync(0xffffffffu,
+                      mbar_wait_short(bar(C::turn(C::kBarO, ti, step - 1)),
+                                      D == 128 ? o_ph : C::parity(step - 1), wc))) {
         ok = false;
         break;
       }

@@ -524,7 +524,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const float m_tile = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * sl2;
           const float m_new = fmaxf(m, m_tile);
-          const bool rescale = __any_sync(0xffffffffu, m_new > m + kRescaleThreshold);
+          // Only rows that are stored have a say: what the others hold may change
+          // from call to call, and a rescale changes the rounding.
+          const bool rescale = __any_sync(0xffffffffu, live && m_new > m + kRescaleThreshold);
           float alpha = 1.f;
           if (rescale) {
             // A row that has seen no key yet keeps m = -inf and alpha = 1.

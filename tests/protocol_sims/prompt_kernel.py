@@ -11,8 +11,8 @@ last V tile), writes P over S_i; at the item's end it waits for O_i and reads it
 
 buffers = 3 (64-wide heads): the scores of step n = 2 * (key tile) + (query
 tile) go to buffer n % 3 and are issued before the product of the step before;
-S_i and P_i have two barriers in turn, and O_i is committed with every product,
-which a rescale waits for.
+S_i, P_i and O_i have two barriers in turn, and O_i is committed with every
+product, which a rescale waits for.
 
 mutation 1: Q_i released before its last scores are issued.
 mutation 2: P V_i issued without waiting for P_i.
@@ -21,6 +21,8 @@ mutation 6: items without keys skipped when the next item is looked for (the
             roles that are still at this item hold their slots).
 mutation 4: (buffers = 3) one barrier each for S_i and P_i.
 mutation 5: (buffers = 3) a rescale that does not wait for the product.
+mutation 7: (buffers = 3) one barrier for O_i: the last product but one, still
+            under way, has the parity that passes for the last.
 """
 from .engine import Engine
 
@@ -31,10 +33,12 @@ def run(items, seed, mutation=0, buffers=2, slots=5):
     """items: (key tiles of query tile 0, of query tile 1)."""
     e = Engine(seed)
     turns = 2 if buffers == 3 and mutation != 4 else 1
+    o_turns = 2 if buffers == 3 and mutation != 7 else 1
     for i in range(2):
         e.bar(f"QFull{i}", 1)
         e.bar(f"QEmpty{i}", 1)
-        e.bar(f"O{i}", 1)
+        for t in range(o_turns):
+            e.bar(f"O{i}{t}", 1)
         for t in range(turns):
             e.bar(f"S{i}{t}", 1)
             e.bar(f"P{i}{t}", 128)
@@ -47,6 +51,9 @@ def run(items, seed, mutation=0, buffers=2, slots=5):
 
     def turn(c):
         return (c & 1, c >> 1 & 1) if turns == 2 else (0, c & 1)
+
+    def o_turn(c):
+        return (c & 1, c >> 1 & 1) if o_turns == 2 else (0, c & 1)
 
     def buf(i, step):
         return f"S{i}" if buffers == 2 else f"S{(2 * step + i) % 3}"
@@ -138,8 +145,10 @@ def run(items, seed, mutation=0, buffers=2, slots=5):
             if m:
                 reads.append((f"O{i}", ("O", k, i, m)))
             e.mma(reads, [(f"O{i}", ("O", k, i, m + 1))])
-            if buffers == 3 or m + 1 == it[i]:
-                e.commit(f"O{i}")
+            if buffers == 3:
+                e.commit(f"O{i}{o_turn(p_n[i] - 1)[0]}")
+            elif m + 1 == it[i]:
+                e.commit(f"O{i}0")
 
         cur = yield from next_tiles()
         started = False  # the item's first scores are issued
@@ -182,14 +191,15 @@ def run(items, seed, mutation=0, buffers=2, slots=5):
             if it is None:
                 return
             for m in range(it[ti]):
-                t, par = turn(c)
                 b = buf(ti, kv + m)
+                t, par = turn(c)
                 yield ("wait", f"S{ti}{t}", par)
                 e.expect(b, ("S", k, ti, m))
                 yield ("step",)
-                if m:  # rescale O
+                if m and e.rnd.random() < 0.5:  # rescale O: only where the maximum grew
                     if buffers == 3 and mutation != 5:
-                        yield ("wait", f"O{ti}", (c - 1) & 1)
+                        t, par = o_turn(c - 1)
+                        yield ("wait", f"O{ti}{t}", par)
                     e.expect(f"O{ti}", ("O", k, ti, m))
                     yield ("step",)
                     e.expect(f"O{ti}", ("O", k, ti, m))
@@ -200,11 +210,15 @@ def run(items, seed, mutation=0, buffers=2, slots=5):
                     e.mem[f"slot{n % slots}"] = ("Vc", k, m)
                 e.expect(b, ("S", k, ti, m))
                 e.mem[b] = ("P", k, ti, m)
-                e.bars[f"P{ti}{t}"].arrive(128)
+                e.bars[f"P{ti}{turn(c)[0]}"].arrive(128)
                 c += 1
             kv += max(it)
             if it[ti]:
-                yield ("wait", f"O{ti}", (c - 1) & 1 if buffers == 3 else o_n & 1)
+                if buffers == 3:
+                    t, par = o_turn(c - 1)
+                    yield ("wait", f"O{ti}{t}", par)
+                else:
+                    yield ("wait", f"O{ti}0", o_n & 1)
                 o_n += 1
                 e.expect(f"O{ti}", ("O", k, ti, it[ti]))
                 yield ("step",)

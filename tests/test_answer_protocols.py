@@ -14,7 +14,7 @@ PIECES = [(1, False), (2, False), (3, False), (4, False), (7, False)]
 PAIRED = PIECES + [(1, True), (2, True), (3, True), (5, True)]
 MODELS = {
     "prompt": (prompt_kernel.run, ITEMS, dict(buffers=2, slots=5), (1, 2, 3, 6)),
-    "prompt_64": (prompt_kernel.run, ITEMS, dict(buffers=3, slots=8), (1, 2, 3, 4, 5, 6)),
+    "prompt_64": (prompt_kernel.run, ITEMS, dict(buffers=3, slots=8), (1, 2, 3, 4, 5, 6, 7)),
     "tree": (tree_kernel.run, PIECES, dict(slots=6), (1, 3)),
     "tree_pair": (tree_kernel.run, PAIRED, dict(slots=5), (1, 2, 3)),
 }

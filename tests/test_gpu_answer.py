@@ -117,6 +117,8 @@ PROMPTS = [
     ([100] * 64, [0, 0, 0, 90] * 16, 16, 8, 64),             # runs of items without keys
     ([300] * 40, [40, 0, 0, 0] * 10, 16, 16, 128),
     ([5], [0], 4, 2, 128),
+    ([1025, 33, 600, 700], [3300, 1500, 2900, 3100], 32, 8, 64),   # many key tiles an item
+    ([900, 130], [1900, 2100], 32, 8, 128),
     ([70, 0, 3], [0, 0, 0], 4, 4, 64),
     ([0, 0, 7] + [0] * 3000 + [20, 1], None, 4, 2, 64),      # mostly empty sequences
 ]
@@ -668,6 +670,23 @@ def test_a_cache_whose_offsets_pass_32_bits(wider):
         o, l, to, tl = plain(q[r:r + 1], k[at], v[at], torch.ones(1, n, dtype=torch.bool, device=DEV))
         check(out[r:r + 1], o, to, "out")
         check(lse[:, r:r + 1], l, tl, "lse")
+
+
+@pytest.mark.parametrize("ctx,new,H,Hkv,D,P", [([45000, 0, 30000], [16, 1, 3], 14, 2, 64, 256),
+                                               ([87000], [1], 32, 8, 128, 16),
+                                               ([2867] * 37, [1] * 37, 16, 16, 128, 64)])
+def test_tree_results_do_not_depend_on_what_ran_before(ctx, new, H, Hkv, D, P):
+    # Rows of a tile that no token fills hold whatever shared memory held.
+    cache = Cache(ctx, new, Hkv, D, P, torch.bfloat16)
+    q = normal(9, sum(new), H, D, dtype=torch.bfloat16)
+    first = run_tree(q, cache)
+    other = normal(8, 700, 8, 128, dtype=torch.bfloat16) * 50
+    k = normal(4, 700, 2, 128, dtype=torch.bfloat16) * 50
+    for n in range(6):
+        cpa.prompt_attention(other[:700 - n], k[:700 - n], k[:700 - n], ints([0, 200, 700 - n]))
+        big = Cache([300 + n] * 40, [30] * 40, 2, 128, 64, torch.bfloat16)
+        run_tree(normal(n, 1200, 8, 128, dtype=torch.bfloat16) * 50, big)
+        assert all(torch.equal(a, b) for a, b in zip(run_tree(q, cache), first))
 
 
 def test_results_do_not_change_from_run_to_run():
