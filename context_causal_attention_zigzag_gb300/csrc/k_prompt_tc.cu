@@ -199,8 +199,8 @@ struct Cfg {
   static constexpr int kBarDrain = kBarFeedEmpty + kFeed;
   static constexpr int kNumBars = kBarDrain + 1;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr int kOffFeed = (kOffMisc + 16 + 15) / 16 * 16;  // items, 32 bytes each
-  static constexpr int kSmemBytes = kOffFeed + kFeed * 32 + 1024;  // + slack for 1024-B alignment
+  static constexpr int kOffFeed = (kOffMisc + 16 + 15) / 16 * 16;  // items, 48 bytes each
+  static constexpr int kSmemBytes = kOffFeed + kFeed * 48 + 1024;  // + slack for 1024-B alignment
 
   // Barrier and parity of query tile i's c-th step.
   static __device__ __forceinline__ int turn(int bar0, int i, uint32_t c) {
@@ -401,12 +401,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   int4* slots = reinterpret_cast<int4*>(smem + C::kOffFeed);
   Block b;
-  int g, h0;
+  int g, h0, nt0, nt1;  // nt0, nt1: key tiles that the two query tiles see
   // The next item, for one of the reading warps: from the shared ring, until one
   // that says there is none; of a direct call each warp finds the only one.
   uint32_t fed = 0;
   auto next_item = [&](bool& ok) {
-    if (w.direct) return fed++ == 0 && find_direct(a, w, b, g, h0);
+    if (w.direct) {
+      if (fed++ != 0 || !find_direct(a, w, b, g, h0)) return false;
+      nt0 = key_tiles(b, a.causal, 0, kT);
+      nt1 = key_tiles(b, a.causal, row_step, kT);
+      return true;
+    }
     const uint32_t s = fed % kFeed;
     if (!__all_sync(0xffffffffu,
                     mbar_wait_short(bar(C::kBarFeedFull + s), (fed / kFeed) & 1, wc))) {
@@ -414,7 +419,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       return false;
     }
     ++fed;
-    const int4 x = slots[2 * s], y = slots[2 * s + 1];
+    const int4 x = slots[3 * s], y = slots[3 * s + 1];
+    const int2 z = *reinterpret_cast<const int2*>(slots + 3 * s + 2);
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(C::kBarFeedEmpty + s));
     b.qrow = x.x;
@@ -424,6 +430,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     b.diag = y.x;
     g = y.y;
     h0 = y.z;
+    nt0 = z.x;
+    nt1 = z.y;
     return y.w != 0;
   };
   if (warp == 0) {
@@ -440,12 +448,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t seq = 0, q_armed[2] = {0, 0};  // ring entries and Q tiles asked for
     bool ok = true;
     while (ok && next_item(ok)) {
-      int nt = 0;
+      const int nt = max(nt0, nt1);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int nti = key_tiles(b, a.causal, i * row_step, kT);
-        if (!ok || nti == 0) continue;  // a tile without keys is not multiplied
-        nt = max(nt, nti);
+        if (!ok || (i == 0 ? nt0 : nt1) == 0) continue;  // a tile without keys is not multiplied
         ok = wwait(bar(C::kBarQEmpty + i), (q_armed[i] & 1) ^ 1);
         if (!ok) continue;
         ++q_armed[i];
@@ -534,8 +540,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int cur[2], nxt[2];
     auto next_tiles = [&](int (&nt)[2]) {
       const bool some = next_item(ok);
-      nt[0] = some ? key_tiles(b, a.causal, 0, kT) : 0;
-      nt[1] = some ? key_tiles(b, a.causal, row_step, kT) : 0;
+      nt[0] = some ? nt0 : 0;
+      nt[1] = some ? nt1 : 0;
       return some;
     };
     bool have = next_tiles(cur), started = false;  // started: cur's first scores are issued
@@ -649,8 +655,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       some = items.next(b, g, h0);
       if (lane == 0) {
-        slots[2 * s] = make_int4(b.qrow, b.nrows, b.krow, b.nk);
-        slots[2 * s + 1] = make_int4(b.diag, g, h0, some);
+        slots[3 * s] = make_int4(b.qrow, b.nrows, b.krow, b.nk);
+        slots[3 * s + 1] = make_int4(b.diag, g, h0, some);
+        slots[3 * s + 2] = make_int4(key_tiles(b, a.causal, 0, kT),
+                                     key_tiles(b, a.causal, row_step, kT), 0, 0);
         mbar_arrive(bar(C::kBarFeedFull + s));
       }
       __syncwarp();
@@ -666,7 +674,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t step = 0, o_ph = 0, kv_it = 0;
     bool ok = true;
     while (ok && next_item(ok)) {
-      const int nt0 = key_tiles(b, a.causal, 0, kT), nt1 = key_tiles(b, a.causal, row_step, kT);
       const int nt = ti == 0 ? nt0 : nt1;
       const int at = ti * row_step + row;  // row within the block
       const int end = a.causal ? min(b.nk, b.diag + at) : b.nk;  // keys that the row sees
