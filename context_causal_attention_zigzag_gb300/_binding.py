@@ -749,10 +749,14 @@ def _table_args(table, R, device):
 
 def _cache_args(k_cache, v_cache, Hkv, D, dtype, device):
     """(num_pages, page_size, strides) of a cache [pages, page_size, Hkv, D]."""
-    shape, strides = k_cache.shape, k_cache.stride()
-    if len(shape) != 4 or shape != v_cache.shape or strides != v_cache.stride():
-        raise ValueError("k_cache and v_cache must be [pages, page_size, Hkv, D] of one shape "
-                         "and strides")
+    shape, strides, v_strides = k_cache.shape, k_cache.stride(), v_cache.stride()
+    if len(shape) != 4 or shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache must be [pages, page_size, Hkv, D] of one shape")
+    if 1 in shape:  # the stride of an axis of one says nothing
+        strides, v_strides = (tuple(s if n > 1 else D for n, s in zip(shape[:3], t)) + t[3:]
+                              for t in (strides, v_strides))
+    if strides != v_strides:
+        raise ValueError("k_cache and v_cache must have one shape and strides")
     if shape[2] != Hkv or shape[3] != D or strides[3] != 1:
         raise ValueError(f"the cache must hold {Hkv} heads of {D} contiguous values")
     if k_cache.dtype != dtype or v_cache.dtype != dtype:

@@ -117,3 +117,16 @@ def test_binding_refuses_host_tensors():
         cp_attn.page_tables(i, i, i[None], i, 16, 8)
     with pytest.raises(ValueError):
         cp_attn.tree_attention(x, x[None], x[None], i[None], i, i)
+
+
+@pytest.mark.parametrize("pages,heads", [(1, 2), (4, 1), (4, 2)])
+def test_binding_refuses_caches_with_gaps_between_values(pages, heads):
+    class Host:
+        index = -1
+
+    wide = torch.zeros(pages, 16, heads, 128, dtype=torch.float16)
+    whole = torch.zeros(pages, 16, heads, 64, dtype=torch.float16)
+    for k, v in ((wide[..., ::2], wide[..., ::2]), (whole, wide[..., ::2])):
+        with pytest.raises(ValueError):
+            _binding._cache_args(k, v, heads, 64, torch.float16, Host)
+    assert _binding._cache_args(whole, whole, heads, 64, torch.float16, Host)[1] == 16

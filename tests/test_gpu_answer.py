@@ -361,6 +361,29 @@ def test_tree_attention_reports_bad_pages_and_lengths(wider):
     assert cpa.device_status() == 0
 
 
+@pytest.mark.parametrize("N", [1, 300])
+def test_caches_of_one_head_or_page_with_meaningless_strides(N):
+    kc, vc = (normal(s, 8, 64, 64, dtype=torch.float16) for s in (1, 2))
+    k1 = kc.as_strided((8, 64, 1, 64), (4096, 64, 8, 1))
+    v1 = vc.as_strided((8, 64, 1, 64), (4096, 64, 0, 1))
+    q = normal(3, N, 4, 64, dtype=torch.float16)
+    pages = [2, 0, 1, 7, 5, 3, 6, 4]
+    out, lse = cpa.tree_attention(q, k1, v1, ints([pages]), ints([150]), ints([0, N]))
+    K, V = (x[pages].reshape(-1, 1, 64)[:150 + N] for x in (kc, vc))
+    at = torch.arange(150 + N, device=DEV)
+    o, l, to, tl = plain(q, K, V, at[None] <= 150 + at[:N, None])
+    check(out, o, to, "out")
+    check(lse, l, tl, "lse")
+    page = normal(5, 16, 2, 64, dtype=torch.float16)
+    one = page.as_strided((1, 16, 2, 64), (3, 128, 64, 1))
+    other = torch.zeros_like(page)
+    x = normal(6, 2, 2, 64, dtype=torch.float16)
+    cpa.cache_write(x, x, one, other.as_strided((1, 16, 2, 64), (0, 128, 64, 1)),
+                    ints([3, 9], torch.int64))
+    assert torch.equal(page[[3, 9]], x) and torch.equal(other[[3, 9]], x)
+    assert cpa.device_status() == 0
+
+
 @pytest.mark.parametrize("wider", [1, 300])
 def test_requests_that_share_pages(wider):
     # Two requests with the same first pages (a common prompt), each with its own
