@@ -126,7 +126,11 @@ __global__ void __launch_bounds__(1024) prompt_plan_kernel(const PromptArgs a, i
   }
   atomicMax(&s_most, most);
   if (bad) atomicExch(a.err, kErrBadTables);
-  __syncthreads();
+  // Broken offsets may name the same rows over and over: nothing is computed then.
+  if (__syncthreads_or(bad)) {
+    if (tid == 0) plan->nblocks = 0;
+    return;
+  }
   most = s_most;
   // Largest cost first: bin 0 holds the blocks with the most key tiles.
   auto bin_of = [&](const Block& b) {
@@ -140,7 +144,7 @@ __global__ void __launch_bounds__(1024) prompt_plan_kernel(const PromptArgs a, i
       for (int at = lane * rows; at < nq; at += 32 * rows) {
         const Block b = make_block(q0, nq, k0, nk, at);
         const int x = atomicAdd(&s_bin[bin_of(b)], 1);
-        if (pass == 1 && x < cap) list[x] = b;  // broken offsets may name more than fit
+        if (pass == 1 && x < cap) list[x] = b;  // more only if the offsets changed under the call
       }
     }
     __syncthreads();

@@ -187,17 +187,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // Where this CTA's part of the line begins: each thread sums a run of
   // requests, the block sums the threads, and the thread whose run holds the
-  // beginning finds the request.
+  // beginning finds the request.  Lengths that break the rules could name the
+  // same rows over and over: nothing is computed then.
   const int per = (a.R + kThreads - 1) / kThreads;
   const int r_lo = min(a.R, (int)threadIdx.x * per), r_hi = min(a.R, r_lo + per);
   long long own = 0;
   bool bad = false;
   Req x;
-  for (int r = r_lo; r < r_hi; ++r) {
-    bad |= !load_req<kPaged>(a, r, x);
-    own += head_cost(x, span, chain) * a.Hkv;
-  }
+  for (int r = r_lo; r < r_hi; ++r) bad |= !load_req<kPaged>(a, r, x);
   if (bad && blockIdx.x == 0) atomicExch(a.err, kErrBadTables);
+  if (!__syncthreads_or(bad)) {
+    for (int r = r_lo; r < r_hi; ++r) {
+      if (per > 1) load_req<kPaged>(a, r, x);
+      own += head_cost(x, span, chain) * a.Hkv;
+    }
+  }
   long long upto = own;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {

@@ -191,6 +191,27 @@ def test_prompt_attention_reports_broken_offsets():
     assert cpa.device_status() == 0
 
 
+# 4 rows a sequence on the average and many keys (the cut line), 262 (sorted blocks).
+@pytest.mark.parametrize("H,nq,nk", [(1, 1 << 14, 1 << 21), (2, 1 << 20, 1 << 20)])
+def test_offsets_that_name_the_same_rows_over_and_over(H, nq, nk):
+    # Every other sequence claims all rows: far more work than the tensors hold.
+    q = normal(1, nq, H, 64, dtype=torch.bfloat16)
+    k = normal(2, nk, H, 64, dtype=torch.bfloat16)
+    cu_q, cu_k = (ints([0, n] * 2000 + [0, n]) for n in (nq, nk))
+    begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    begin.record()
+    cpa.prompt_attention(q, k, k, cu_q, cu_k)
+    end.record()
+    assert cpa.device_status() == -1
+    assert begin.elapsed_time(end) < 1000
+    pages = normal(3, 8, 16, H, 64, dtype=torch.bfloat16)
+    table = torch.zeros(4001, 2000, dtype=torch.int32, device=DEV)
+    cpa.tree_attention(q, pages, pages, table, ints([100] * 4001), cu_q)
+    assert cpa.device_status() == -1
+    cpa.prompt_attention(q[:300], q[:300], q[:300], ints([0, 300]))
+    assert cpa.device_status() == 0
+
+
 # ---------------------------------------------------------------------------
 # the cache
 # ---------------------------------------------------------------------------
