@@ -52,9 +52,14 @@ bool check_cache(const void* k, const void* v, const CacheShape& c, int D) {
   return true;
 }
 
-// Rows of a packed tensor: an item then takes less than the kernels' bounded
-// waits allow (2 s).
+// Rows of a packed tensor, positions of a request in the cache and requests (the
+// empty ones are passed one by one): within these an item, and the way to it, take
+// less than the kernels' bounded waits allow (2 s).  A key tile takes 1.6 us of
+// packed keys; in pages of 16 at most 3 us (64 KB at the 3.4 TB/s that 16 drafted
+// trees reach, their start and merge included).
 constexpr int kMostRows = 1 << 27;
+constexpr int kMostPositions = 1 << 26;
+constexpr int kMostRequests = 1 << 20;
 
 bool scale_ok(float s) { return s <= 0.f || isfinite(s); }
 
@@ -160,11 +165,11 @@ int cpattn_tree_attn(const void* q, int64_t q_stride, const void* k_cache, const
                      size_t workspace_bytes, cpattn_stream_t stream) {
   int rc = check_heads(H, Hkv, D, dtype);
   if (rc != CPATTN_OK) return rc;
-  if (R < 0 || N < 0 || N > (1 << 30) || !scale_ok(softmax_scale)) return CPATTN_ERR_INVALID_ARG;
+  if (R < 0 || R > kMostRequests || N < 0 || N > (1 << 30) || !scale_ok(softmax_scale))
+    return CPATTN_ERR_INVALID_ARG;
   CacheShape c = {num_pages, page_size, page_stride, token_stride, head_stride};
   if (!check_cache(k_cache, v_cache, c, D)) return CPATTN_ERR_INVALID_ARG;
-  // Positions of a request stay within an int.
-  if (table_width < 0 || table_stride < table_width || table_width > INT32_MAX / 2 / page_size)
+  if (table_width < 0 || table_stride < table_width || table_width > kMostPositions / page_size)
     return CPATTN_ERR_INVALID_ARG;
   if (R == 0 || N == 0) return CPATTN_OK;
   if (!check_rows(q, q_stride, H, D) || !check_rows(out, (int64_t)H * D, H, D) || !lse ||
@@ -220,11 +225,11 @@ int cpattn_prompt_attn(const void* q, int64_t q_stride, const void* k, int64_t k
                        size_t workspace_bytes, cpattn_stream_t stream) {
   int rc = check_heads(H, Hkv, D, dtype);
   if (rc != CPATTN_OK) return rc;
-  if (R < 0 || R > (1 << 24) || Nq < 0 || Nk < 0 || Nq > kMostRows || Nk > kMostRows ||
+  if (R < 0 || R > kMostRequests || Nq < 0 || Nk < 0 || Nq > kMostRows || Nk > kMostRows ||
       (causal != 0 && causal != 1) || !scale_ok(softmax_scale))
     return CPATTN_ERR_INVALID_ARG;
-  // Work items are numbered in an int.
-  if (((int64_t)Nq / 128 + R) * H > INT32_MAX) return CPATTN_ERR_INVALID_ARG;
+  // Work items are numbered in an int, with room for the CTAs that ask past the end.
+  if (((int64_t)Nq / 128 + R) * H > INT32_MAX / 2) return CPATTN_ERR_INVALID_ARG;
   if (R == 0 || Nq == 0) return CPATTN_OK;
   if (!check_rows(q, q_stride, H, D) || !check_rows(out, (int64_t)H * D, H, D) || !lse ||
       !aligned(lse, 4) || !cu_q || !cu_k || !aligned(cu_q, 4) || !aligned(cu_k, 4))

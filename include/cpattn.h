@@ -617,6 +617,7 @@ CPATTN_API int cpattn_cache_write(const void* k, int64_t k_stride, const void* v
  *   request's j-th new token (a drafted tree: itself and its ancestors; at
  *   most 64 new tokens a request, more are an error).
  *   q [N, H, D], tokens q_stride apart; out [N, H, D]; lse [H, N] float32.
+ *   R at most 2^20, table_width * page_size at most 2^26, N at most 2^30.
  * A token that sees nothing gets out = 0 and lse = -inf.  Rows of out and lse
  * behind cu_new[R] are left as they were.  What lies in the cache behind a
  * request's last position, or in another request's pages, does not reach it,
@@ -643,7 +644,8 @@ CPATTN_API int cpattn_tree_attn(const void* q, int64_t q_stride, const void* k_c
  * j <= i + nk - nq -- the last query sees every key, so that keys of a part
  * answered earlier may stand in front -- or (causal = 0) all nk.
  *   q [Nq, H, D], k, v [Nk, Hkv, D], tokens q_stride, k_stride, v_stride apart;
- *   out [Nq, H, D]; lse [H, Nq] float32.  Nq, Nk at most 2^27.
+ *   out [Nq, H, D]; lse [H, Nq] float32.  Nq, Nk at most 2^27, R at most 2^20,
+ *   (Nq / 128 + R) * H below 2^30.
  * A query that sees nothing gets out = 0 and lse = -inf.  Rows of out and lse
  * behind cu_q[R] are left as they were; what lies in rows of other sequences
  * does not reach a sequence, NaN included (a value that is not finite may

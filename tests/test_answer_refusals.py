@@ -130,3 +130,15 @@ def test_binding_refuses_caches_with_gaps_between_values(pages, heads):
         with pytest.raises(ValueError):
             _binding._cache_args(k, v, heads, 64, torch.float16, Host)
     assert _binding._cache_args(whole, whole, heads, 64, torch.float16, Host)[1] == 16
+
+
+def test_sizes_whose_work_could_outlast_the_bounded_waits_are_refused():
+    most = 1 << 20
+    assert call("cpattn_tree_attn", TREE, R=most + 1) == E
+    for P in (16, 128, 1024):
+        width = (1 << 26) // P
+        assert call("cpattn_tree_attn", TREE, P=P, width=width + 1, stride=width + 1) == E
+        assert call("cpattn_tree_attn", TREE, P=P, width=width, stride=width, ws=null) == W
+    assert call("cpattn_prompt_attn", PROMPT, R=most + 1) == E
+    assert call("cpattn_prompt_attn", PROMPT, R=most, H=1024, Hkv=512, qs=1024 * 64, ks=512 * 64,
+                vs=512 * 64) == E
