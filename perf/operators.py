@@ -314,24 +314,26 @@ def run(s):
         return {"prompt": _prompt, "tree": _tree, "write": _write, "tables": _tables}[op](s)
     import context_causal_attention_zigzag_gb300 as cpa
     # Outputs and scratch are made on the first pass and kept, as a serving loop keeps them.
-    keep = s.setdefault("keep", {})
     if op == "prompt":
-        if not keep:
-            keep["workspace"] = cpa.prompt_attention_workspace(s["q"], s["cu_q"])
-        keep["out"], keep["lse"] = cpa.prompt_attention(s["q"], s["k"], s["v"], s["cu_q"], s["cu_k"], **keep)
-        return keep["out"], keep["lse"]
+        if "keep" not in s:
+            out, lse = cpa.prompt_attention(s["q"], s["k"], s["v"], s["cu_q"], s["cu_k"])
+            s["keep"] = dict(out=out, lse=lse, workspace=cpa.prompt_attention_workspace(s["q"], s["cu_q"]))
+        return cpa.prompt_attention(s["q"], s["k"], s["v"], s["cu_q"], s["cu_k"], **s["keep"])
     if op == "tree":
-        if not keep:
-            keep["workspace"] = cpa.tree_attention_workspace(s["q"], s["k_cache"], s["cu"])
+        args = (s["q"], s["k_cache"], s["v_cache"], s["table"], s["ctx"], s["cu"])
         tree = s["masks"] if s["case"]["tree"] else None
-        keep["out"], keep["lse"] = cpa.tree_attention(s["q"], s["k_cache"], s["v_cache"], s["table"], s["ctx"],
-                                                      s["cu"], tree, **keep)
-        return keep["out"], keep["lse"]
+        if "keep" not in s:
+            out, lse = cpa.tree_attention(*args, tree)
+            s["keep"] = dict(out=out, lse=lse, workspace=cpa.tree_attention_workspace(s["q"], s["k_cache"], s["cu"]))
+        return cpa.tree_attention(*args, tree, **s["keep"])
     if op == "write":
         return cpa.cache_write(s["k"], s["v"], s["k_cache"], s["v_cache"], s["slots"])
-    keep["slots"], keep["cu"], keep["used"] = cpa.page_tables(s["ctx"], s["new"], s["table"], s["free"],
-                                                             s["case"]["page"], s["tokens"], **keep)
-    return s["table"], keep["slots"], keep["cu"], keep["used"]
+    if "keep" not in s:
+        s["keep"] = dict(zip(("slots", "cu", "used"),
+                             cpa.page_tables(s["ctx"], s["new"], s["table"], s["free"],
+                                             s["case"]["page"], s["tokens"])))
+    return (s["table"], *cpa.page_tables(s["ctx"], s["new"], s["table"], s["free"],
+                                         s["case"]["page"], s["tokens"], **s["keep"]))
 
 
 # ---------------------------------------------------------------------------
