@@ -43,7 +43,8 @@
 // prompt went from 1.31 to 1.46 ms.)
 // The weights are rounded to the input type for the second product
 // (their sum is taken before rounding, in float32): the tensor cores take 16-bit
-// operands, and the rounding is as large as that of the output itself.
+// operands, and the rounding is as large as that of the output itself (float16's
+// smallest step: kWeightLag in tc_ptx.cuh).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -62,7 +63,6 @@ constexpr int kT = 128;  // tile edge (rows, keys)
 constexpr int kBoxBytes = kT * 64 * 2;
 constexpr int kThreads = 384;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRescaleThreshold = 8.0f;  // log2 units
 
 // One block of query rows of a sequence, as the plan lists it.
 struct __align__(16) Block {
@@ -715,13 +715,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           mx2 = fmaxf(mx2, __uint_as_float(r[j + 2]));
           mx3 = fmaxf(mx3, __uint_as_float(r[j + 3]));
         }
-        const float m_tile = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * sl2;
-        const float m_new = fmaxf(m, m_tile);
+        const float m_tile =
+            best_score<kBf16>(fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)), sl2);
         // Only the sequence's own rows have a say: a rescale changes the rounding.
-        const bool need = live && m_new > m + kRescaleThreshold;
+        const bool need = live && m_tile - m > kWeightLag<kBf16>;
         const bool rescale = __any_sync(0xffffffffu, need);
         float alpha = 1.f;
         if (rescale) {
+          const float m_new = fmaxf(m, new_reference<kBf16>(m_tile));
           // A row that has seen no key yet keeps m = -inf and alpha = 1.
           alpha = m_new == -INFINITY ? 1.f : ex2(m - m_new);
           l *= alpha;

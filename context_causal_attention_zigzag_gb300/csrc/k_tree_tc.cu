@@ -66,7 +66,6 @@ constexpr int kBoxBytes = kT * 64 * 2;
 constexpr int kThreads = 384;
 constexpr int kMaxCtas = 160;  // partials are laid out for so many
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRescaleThreshold = 8.0f;  // log2 units
 
 template <int D, bool kPair>
 struct Cfg {
@@ -526,13 +525,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             mx2 = fmaxf(mx2, __uint_as_float(r[j + 2]));
             mx3 = fmaxf(mx3, __uint_as_float(r[j + 3]));
           }
-          const float m_tile = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * sl2;
-          const float m_new = fmaxf(m, m_tile);
+          const float m_tile =
+              best_score<kBf16>(fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)), sl2);
           // Only rows that are stored have a say: what the others hold may change
           // from call to call, and a rescale changes the rounding.
-          const bool rescale = __any_sync(0xffffffffu, live && m_new > m + kRescaleThreshold);
+          const bool rescale = __any_sync(0xffffffffu, live && m_tile - m > kWeightLag<kBf16>);
           float alpha = 1.f;
           if (rescale) {
+            const float m_new = fmaxf(m, new_reference<kBf16>(m_tile));
             // A row that has seen no key yet keeps m = -inf and alpha = 1.
             alpha = m_new == -INFINITY ? 1.f : ex2(m - m_new);
             l *= alpha;

@@ -345,6 +345,28 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   }
 }
 
+// The reference m of the softmax weights 2^(s - m), in log2, is corrected when a
+// tile's best score passes it by more than kWeightLag; it then becomes that score
+// (bfloat16), or 7 less (float16).  float16 weights so reach from 2^15 down to the
+// type's smallest step: the row's largest is 2^7 at least, one keeps its 11 bits down
+// to 2^-21 of the largest and has a step of 2^-31 below that.  With the score itself
+// as the reference, those below 2^-25 vanished from O while the float32 sum of the
+// weights kept them (16383 keys 17 nats below the row's best: O 44 % off).
+// In float16 the score and the reference are rounded up, so that no weight passes
+// 2^15 whatever the scores' size: beyond 2^24 their own rounding would make one
+// overflow.
+template <bool kBf16>
+constexpr float kWeightLag = kBf16 ? 8.f : 15.f;
+
+template <bool kBf16>
+__device__ __forceinline__ float best_score(float max, float sl2) {
+  return kBf16 ? max * sl2 : __fmul_ru(max, sl2);
+}
+template <bool kBf16>
+__device__ __forceinline__ float new_reference(float best) {
+  return kBf16 ? best : __fadd_ru(best, -7.f);
+}
+
 // Transposes 4 x 4 16-byte pieces within each quad of lanes: v[j] of lane q
 // becomes what v[q] of the quad's lane j was.  A thread that holds 64
 // consecutive bytes of its own row then holds one piece of four rows, and the
