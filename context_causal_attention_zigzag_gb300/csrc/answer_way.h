@@ -1,0 +1,89 @@
+// Which kernel answers a call, from its sizes (the lengths themselves are on the
+// device), and what the kernels are estimated to take.  Host only; its choices are
+// checked without a GPU.
+#pragma once
+
+#include <math.h>
+#include <stdint.h>
+
+#include "cpattn_internal.h"
+
+namespace cpattn {
+
+// The CUDA-core kernel.  Few blocks: eight warps a block, two heads and four keys' loads at a time.
+// Many: four warps, four heads (fewer blocks read a key twice), two keys.
+inline bool few_blocks(const TreeArgs& a, int sms) {
+  const int G = a.H / a.Hkv;
+  return (int64_t)a.N * a.Hkv * ((G + 1) / 2) <= 2 * sms;
+}
+
+// What it and the tensor cores' cut line take for `keys` keys a request (us,
+// estimated).  Measured, one token a request, H = 32, Hkv = 8, D = 128 (us, CUDA cores
+// / cut line), by requests and keys:
+//            1 key        16          64         256        1000
+//     1    4.5 / 11.8  4.8 / 11.4  6.2 / 11.4  11 / 13    29 / 13
+//     8    5.0 / 13.8  5.7 / 13.5  7.0 / 13.5  12 / 17    34 / 21
+//    64    5.8 / 28    7.7 / 27     13 / 28    34 / 41   109 / 60
+//   256     16 / 79     23 / 77     44 / 77   121 / 119  418 / 181
+// The estimates below follow these within a fifth.
+inline float small_attn_us(const TreeArgs& a, int64_t keys, int sms) {
+  const int G = a.H / a.Hkv, heads = G < 4 ? G : 4;
+  const float kd = (float)keys * a.D;
+  if (few_blocks(a, sms)) return 4.6f + 1.6f * ceilf(kd / 8192.f);
+  const float blocks = (float)a.N * a.Hkv * ((G + heads - 1) / heads);
+  const float latency = 4.6f + kd / 2048.f;
+  const float work = 5.f + blocks * (0.0052f + 1.52e-6f * kd * (0.35f + 0.1625f * heads));
+  return latency > work ? latency : work;
+}
+
+inline float line_attn_us(const TreeArgs& a, int64_t keys) {
+  const int64_t rows = (int64_t)a.N * (a.H / a.Hkv) / a.R;  // of a request and kv head
+  const float items = (float)a.R * a.Hkv * (1 + rows / 256);
+  return 12.f + items * (0.032f + 0.0095f * ceilf((float)keys / 128.f) * a.D / 128.f);
+}
+
+// How a call is done, from its means (the lengths themselves are on the device).
+//  kSmall: a block a token and kv head on CUDA cores (k_answer_small.cu).
+//  kDirect: at most an item a CTA; each CTA finds its own, nothing is planned.
+//  kLine: few rows and many keys a sequence; the keys of an item are shared
+//    among CTAs and a kv head's query heads share a row tile (k_tree_tc.cu).
+//  kSorted: the rest.
+// Measured (us, H = 32, Hkv = 8, D = 128; direct or sorted / line), for sequences
+// of nq queries behind 1 to n keys:
+//   1 x   1, n 1000: 10.8 / 12.8    4 x  1, n 1000: 19.0 / 14.2   16 x  1, n 8000: 99 / 54
+//   1 x   1, n 8000: 20.2 / 13.7    4 x 32, n 1000: 18.6 / 18.3   16 x 32, n    1: 17.6 / 15.0
+//   4 x 128, n 8000: 82.5 / 57.5    4 x 64, n 1000: 18.5 / 25.1   16 x 64, n 1000: 29.6 / 42.9
+// and without keys in front (small / direct, line or sorted):
+//   1 x 16:  5.3 /  9.4    8 x  4:  5.3 / 10.8    64 x  4: 15 / 28
+//   1 x 64:  9.2 /  9.4    8 x 16:  9.6 / 10.8    64 x 16: 49 / 31
+enum Way : int { kSmall, kDirect, kLine, kSorted };
+
+inline Way prompt_way(const TreeArgs& a, int sms) {
+  if (a.Nk == 0) return kSorted;
+  const int G = a.H / a.Hkv;
+  const int64_t items = ((int64_t)a.N / kTcTile + a.R) * (G % 2 == 0 ? a.H / 2 : a.H);
+  const int64_t rows = (int64_t)a.N * G / a.R, keys = a.Nk / a.R;
+  Way by = items <= sms ? kDirect : kSorted;
+  const float tiles = (float)(keys / kTcTile + 1);  // of the longest rows
+  float us = by == kDirect ? 8.f + 1.5f * tiles : 14.f + items * (3.f + 1.6f * tiles) / sms;
+  if (rows <= kTcTile) {
+    if (keys > 512 || items > sms) {
+      by = kLine;
+      us = line_attn_us(a, keys);
+    }
+  } else if (by == kDirect) {
+    // Whether the CTAs without an item would help more than the sharing costs.
+    const float mean = a.causal && a.Nk == a.N ? 0.5f * tiles : tiles;
+    const float line = 20.f + 1.7f * mean * a.N * a.H / (2 * kTcTile) / sms;
+    if (line < us) {
+      by = kLine;
+      us = line;
+    }
+  }
+  // Under the causal rule a row sees about the keys in front of its sequence's
+  // queries and half of those among them.
+  const int64_t seen = a.causal ? (a.Nk > a.N ? (a.Nk - a.N / 2) / a.R : keys / 2) : keys;
+  return small_attn_us(a, seen + 1, sms) < us ? kSmall : by;
+}
+
+}  // namespace cpattn

@@ -445,11 +445,8 @@ __host__ __device__ inline bool load_req(const TreeArgs& a, int r, Req& x) {
   return ok;
 }
 
-// One block per token and kv head on CUDA cores, and what it and the tensor
-// cores' cut line take for `keys` keys a request (us, estimated).
+// One block per token and kv head on CUDA cores (k_answer_small.cu).
 cudaError_t launch_small_attn(const TreeArgs& a, int dtype, int sms, cudaStream_t stream);
-float small_attn_us(const TreeArgs& a, int64_t keys, int sms);
-float line_attn_us(const TreeArgs& a, int64_t keys);
 // The tensor cores' cut line (k_tree_tc.cu).
 cudaError_t launch_line_attn(const TreeArgs& a, int dtype, int dev, int sms, cudaStream_t stream);
 cudaError_t launch_page_tables(const TablesArgs& a, cudaStream_t stream);

@@ -17,6 +17,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "answer_way.h"
 #include "cpattn_internal.h"
 #include "tc_ptx.cuh"
 
@@ -230,13 +231,6 @@ __global__ void __launch_bounds__(kWarps * 32) small_kernel(const TreeArgs a) {
   }
 }
 
-// Few blocks: eight warps a block, two heads and four keys' loads at a time.
-// Many: four warps, four heads (fewer blocks read a key twice), two keys.
-bool few_blocks(const TreeArgs& a, int sms) {
-  const int G = a.H / a.Hkv;
-  return (int64_t)a.N * a.Hkv * ((G + 1) / 2) <= 2 * sms;
-}
-
 template <bool kBf16, int D, int kHeads, int kWarps, int U>
 void run(const TreeArgs& a, cudaStream_t stream) {
   const int G = a.H / a.Hkv;
@@ -265,30 +259,6 @@ void run_heads(const TreeArgs& a, int sms, cudaStream_t stream) {
 }
 
 }  // namespace
-
-// Measured, one token a request, H = 32, Hkv = 8, D = 128 (us, this kernel / the
-// tensor cores' cut line), by requests and keys:
-//            1 key        16          64         256        1000
-//     1    4.5 / 11.8  4.8 / 11.4  6.2 / 11.4  11 / 13    29 / 13
-//     8    5.0 / 13.8  5.7 / 13.5  7.0 / 13.5  12 / 17    34 / 21
-//    64    5.8 / 28    7.7 / 27     13 / 28    34 / 41   109 / 60
-//   256     16 / 79     23 / 77     44 / 77   121 / 119  418 / 181
-// The estimates below follow these within a fifth.
-float small_attn_us(const TreeArgs& a, int64_t keys, int sms) {
-  const int G = a.H / a.Hkv, heads = G < 4 ? G : 4;
-  const float kd = (float)keys * a.D;
-  if (few_blocks(a, sms)) return 4.6f + 1.6f * ceilf(kd / 8192.f);
-  const float blocks = (float)a.N * a.Hkv * ((G + heads - 1) / heads);
-  const float latency = 4.6f + kd / 2048.f;
-  const float work = 5.f + blocks * (0.0052f + 1.52e-6f * kd * (0.35f + 0.1625f * heads));
-  return latency > work ? latency : work;
-}
-
-float line_attn_us(const TreeArgs& a, int64_t keys) {
-  const int64_t rows = (int64_t)a.N * (a.H / a.Hkv) / a.R;  // of a request and kv head
-  const float items = (float)a.R * a.Hkv * (1 + rows / 256);
-  return 12.f + items * (0.032f + 0.0095f * ceilf((float)keys / 128.f) * a.D / 128.f);
-}
 
 cudaError_t launch_small_attn(const TreeArgs& a, int dtype, int sms, cudaStream_t stream) {
   if (dtype == CPATTN_BF16) {

@@ -16,7 +16,7 @@
 // Items are sorted by their number of key tiles (prompt_plan_kernel) and taken in
 // that order, in the cost bands of the ring forward (banded_item), by whichever
 // CTA is free; one sequence needs no sorting and is dealt in snake order; a call
-// of no more items than SMs is neither (way()).
+// of no more items than SMs is neither (prompt_way()).
 //
 // What bounds it: from some hundred tokens on the rate of the tensor cores'
 // instructions (16 SS and 16 TS of 128 x 128 x 16 per key tile and item, 1.52 us at
@@ -51,6 +51,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "answer_way.h"
 #include "cpattn_internal.h"
 #include "tc_ptx.cuh"
 
@@ -864,50 +865,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Blocks that the plan may list: a sequence's last block of `rows` may be short.
 int64_t most_blocks(int R, int Nq) { return (int64_t)Nq / kT + R; }
 
-// How a call is done, from its means (the lengths themselves are on the device).
-//  kSmall: a block a token and kv head on CUDA cores (k_answer_small.cu).
-//  kDirect: at most an item a CTA; each CTA finds its own, nothing is planned.
-//  kLine: few rows and many keys a sequence; the keys of an item are shared
-//    among CTAs and a kv head's query heads share a row tile (k_tree_tc.cu).
-//  kSorted: the rest.
-// Measured (us, H = 32, Hkv = 8, D = 128; direct or sorted / line), for sequences
-// of nq queries behind 1 to n keys:
-//   1 x   1, n 1000: 10.8 / 12.8    4 x  1, n 1000: 19.0 / 14.2   16 x  1, n 8000: 99 / 54
-//   1 x   1, n 8000: 20.2 / 13.7    4 x 32, n 1000: 18.6 / 18.3   16 x 32, n    1: 17.6 / 15.0
-//   4 x 128, n 8000: 82.5 / 57.5    4 x 64, n 1000: 18.5 / 25.1   16 x 64, n 1000: 29.6 / 42.9
-// and without keys in front (small / direct, line or sorted):
-//   1 x 16:  5.3 /  9.4    8 x  4:  5.3 / 10.8    64 x  4: 15 / 28
-//   1 x 64:  9.2 /  9.4    8 x 16:  9.6 / 10.8    64 x 16: 49 / 31
-enum Way { kSmall, kDirect, kLine, kSorted };
-
-Way way(const PromptArgs& a, const TreeArgs& t, int sms) {
-  if (a.Nk == 0) return kSorted;
-  const int G = a.H / a.Hkv;
-  const int64_t items = ((int64_t)a.Nq / kT + a.R) * (G % 2 == 0 ? a.H / 2 : a.H);
-  const int64_t rows = (int64_t)a.Nq * G / a.R, keys = a.Nk / a.R;
-  Way by = items <= sms ? kDirect : kSorted;
-  const float tiles = (float)(keys / kT + 1);  // of the longest rows
-  float us = by == kDirect ? 8.f + 1.5f * tiles : 14.f + items * (3.f + 1.6f * tiles) / sms;
-  if (rows <= kT) {
-    if (keys > 512 || items > sms) {
-      by = kLine;
-      us = line_attn_us(t, keys);
-    }
-  } else if (by == kDirect) {
-    // Whether the CTAs without an item would help more than the sharing costs.
-    const float mean = a.causal && a.Nk == a.Nq ? 0.5f * tiles : tiles;
-    const float line = 20.f + 1.7f * mean * a.Nq * a.H / (2 * kT) / sms;
-    if (line < us) {
-      by = kLine;
-      us = line;
-    }
-  }
-  // Under the causal rule a row sees about the keys in front of its sequence's
-  // queries and half of those among them.
-  const int64_t seen = a.causal ? (a.Nk > a.Nq ? (a.Nk - a.Nq / 2) / a.R : keys / 2) : keys;
-  return small_attn_us(t, seen + 1, sms) < us ? kSmall : by;
-}
-
 template <bool kBf16, int D>
 cudaError_t run(const PromptArgs& a, Way by, int dev, int sms, cudaStream_t stream) {
   const int grp = a.H / a.Hkv;
@@ -993,7 +950,7 @@ cudaError_t launch_prompt_attn(const PromptArgs& a, int dtype, cudaStream_t stre
   t.v_stride = a.v_stride;
   t.Nk = a.Nk;
   t.causal = a.causal;
-  const Way by = way(a, t, sms);
+  const Way by = prompt_way(t, sms);
   if (by == kSmall) return launch_small_attn(t, dtype, sms, stream);
   if (by == kLine) return launch_line_attn(t, dtype, dev, sms, stream);
   if (dtype == CPATTN_BF16)

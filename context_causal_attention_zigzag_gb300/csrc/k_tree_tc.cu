@@ -51,6 +51,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "answer_way.h"
 #include "cpattn_internal.h"
 #include "line_walk.h"
 #include "tc_ptx.cuh"
@@ -968,7 +969,7 @@ cudaError_t launch_line_attn(const TreeArgs& a, int dtype, int dev, int sms, cud
 
 // The keys of a request are only bounded here (the table's width): a table much
 // wider than its requests sends small calls to the tensor cores, which costs
-// what the table in k_answer_small.cu says.
+// what the table in answer_way.h says.
 cudaError_t launch_tree_attn(const TreeArgs& a, int dtype, cudaStream_t stream) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
