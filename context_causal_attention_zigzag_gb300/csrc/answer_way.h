@@ -58,32 +58,54 @@ inline float line_attn_us(const TreeArgs& a, int64_t keys) {
 //   1 x 64:  9.2 /  9.4    8 x 16:  9.6 / 10.8    64 x 16: 49 / 31
 enum Way : int { kSmall, kDirect, kLine, kSorted };
 
-inline Way prompt_way(const TreeArgs& a, int sms) {
-  if (a.Nk == 0) return kSorted;
+struct PromptWay {
+  Way by;
+  int above;  // kSmall: sequences of so many keys and more go to the cut line (0: none do)
+};
+
+// Only the means are known, and one block or CTA of kSmall and kDirect walks all keys of
+// its rows: in an uneven batch, or one padded with empty sequences, the longest
+// decides.  So both are also taken at their worst, all keys in one sequence.
+//  - kDirect, where that could cost more than the choice wins: the cut line.
+//  - kSmall, where it could take more than three times as long as the next best: sequences
+//    with several times the mean of keys are left to the cut line, a second kernel (and
+//    its merge) behind the first.
+// Measured (us, this choice / by the means alone; H = 32, Hkv = 8, D = 128):
+//   one of 400 among 63 of 1: 28 / 92          256 x 1, one behind 16384: 30 / 660
+//   one of 2000 in 512 slots: 86 / 1690        4 x 128, one behind 4000: 29 / 58
+//   38 x 1, one behind 19000, H = 8, Hkv = 1: 15 / 235
+// and what an even batch pays for it:
+//   64 x 1 behind 16: 10.5 / 5.2    64 x 8: 28 / 22    4 x 64 behind 1000: 25 / 19
+inline PromptWay prompt_way(const TreeArgs& a, int sms) {
+  if (a.Nk == 0) return {kSorted, 0};
   const int G = a.H / a.Hkv;
   const int64_t items = ((int64_t)a.N / kTcTile + a.R) * (G % 2 == 0 ? a.H / 2 : a.H);
   const int64_t rows = (int64_t)a.N * G / a.R, keys = a.Nk / a.R;
+  auto direct_us = [](int64_t n) { return 8.f + 1.5f * (float)(n / kTcTile + 1); };
   Way by = items <= sms ? kDirect : kSorted;
   const float tiles = (float)(keys / kTcTile + 1);  // of the longest rows
-  float us = by == kDirect ? 8.f + 1.5f * tiles : 14.f + items * (3.f + 1.6f * tiles) / sms;
+  float us = by == kDirect ? direct_us(keys) : 14.f + items * (3.f + 1.6f * tiles) / sms;
   if (rows <= kTcTile) {
-    if (keys > 512 || items > sms) {
+    const float line = line_attn_us(a, keys);
+    if (keys > 512 || by == kSorted || (a.R > 1 && direct_us(a.Nk) > 2.f * line)) {
       by = kLine;
-      us = line_attn_us(a, keys);
+      us = line;
     }
   } else if (by == kDirect) {
     // Whether the CTAs without an item would help more than the sharing costs.
     const float mean = a.causal && a.Nk == a.N ? 0.5f * tiles : tiles;
     const float line = 20.f + 1.7f * mean * a.N * a.H / (2 * kTcTile) / sms;
-    if (line < us) {
+    if (line < us || (a.R > 1 && us * direct_us(a.Nk) > line * line)) {
       by = kLine;
       us = line;
     }
   }
   // Under the causal rule a row sees about the keys in front of its sequence's
   // queries and half of those among them.
-  const int64_t seen = a.causal ? (a.Nk > a.N ? (a.Nk - a.N / 2) / a.R : keys / 2) : keys;
-  return small_attn_us(a, seen + 1, sms) < us ? kSmall : by;
+  const int64_t all = a.causal ? (a.Nk > a.N ? a.Nk - a.N / 2 : a.Nk / 2) : a.Nk;
+  if (small_attn_us(a, all / a.R + 1, sms) >= us) return {by, 0};
+  const bool even = small_attn_us(a, all + 1, sms) <= 3.f * us;
+  return {kSmall, even || a.R == 1 ? 0 : (int)(keys < 8 ? 32 : 4 * keys)};
 }
 
 }  // namespace cpattn

@@ -209,7 +209,7 @@ int cpattn_tree_attn(const void* q, int64_t q_stride, const void* k_cache, const
   a.err = err;
   a.cu_k = nullptr;
   a.k_stride = a.v_stride = 0;
-  a.Nk = a.causal = 0;
+  a.Nk = a.causal = a.above = 0;
   return status(launch_tree_attn(a, dtype, (cudaStream_t)stream));
 }
 

@@ -366,6 +366,9 @@ struct TreeArgs {
   const int* cu_k;
   int64_t k_stride, v_stride;
   int Nk, causal;
+  // Packed keys shared by two kernels (above > 0): sequences of so many keys and more
+  // are the cut line's, the others the CUDA cores'.
+  int above;
 };
 
 struct PromptArgs {
@@ -442,6 +445,14 @@ __host__ __device__ inline bool load_req(const TreeArgs& a, int r, Req& x) {
     ok &= packed_rows(a.cu_k, r, a.Nk, x.k0, x.total);
     x.ctx = a.causal ? x.total - x.n : x.total;
   }
+  return ok;
+}
+
+// The same for the cut line, for which another kernel's sequences are empty.
+template <bool kPaged>
+__host__ __device__ inline bool load_line_req(const TreeArgs& a, int r, Req& x) {
+  const bool ok = load_req<kPaged>(a, r, x);
+  if (!kPaged && x.total < a.above) x.n = 0;
   return ok;
 }
 

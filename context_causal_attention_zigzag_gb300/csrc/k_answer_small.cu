@@ -91,6 +91,7 @@ __global__ void __launch_bounds__(kWarps * 32) small_kernel(const TreeArgs a) {
   if (r < 0) return;  // behind the last request: left as it is
   Req x;
   load_req<kPaged>(a, r, x);
+  if (!kPaged && a.above > 0 && x.total >= a.above) return;  // the cut line's
   const int t = i - x.q0;
   const bool chain = a.tree == nullptr;
   unsigned long long bits = 0;

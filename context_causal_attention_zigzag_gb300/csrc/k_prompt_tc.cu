@@ -950,8 +950,12 @@ cudaError_t launch_prompt_attn(const PromptArgs& a, int dtype, cudaStream_t stre
   t.v_stride = a.v_stride;
   t.Nk = a.Nk;
   t.causal = a.causal;
-  const Way by = prompt_way(t, sms);
-  if (by == kSmall) return launch_small_attn(t, dtype, sms, stream);
+  const auto [by, above] = prompt_way(t, sms);
+  if (by == kSmall) {
+    t.above = above;
+    e = launch_small_attn(t, dtype, sms, stream);
+    return e != cudaSuccess || above == 0 ? e : launch_line_attn(t, dtype, dev, sms, stream);
+  }
   if (by == kLine) return launch_line_attn(t, dtype, dev, sms, stream);
   if (dtype == CPATTN_BF16)
     return a.D == 128 ? run<true, 128>(a, by, dev, sms, stream)

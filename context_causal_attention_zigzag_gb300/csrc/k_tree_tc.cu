@@ -194,11 +194,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   long long own = 0;
   bool bad = false;
   Req x;
-  for (int r = r_lo; r < r_hi; ++r) bad |= !load_req<kPaged>(a, r, x);
+  for (int r = r_lo; r < r_hi; ++r) bad |= !load_line_req<kPaged>(a, r, x);
   if (bad && blockIdx.x == 0) atomicExch(a.err, kErrBadTables);
   if (!__syncthreads_or(bad)) {
     for (int r = r_lo; r < r_hi; ++r) {
-      if (per > 1) load_req<kPaged>(a, r, x);
+      if (per > 1) load_line_req<kPaged>(a, r, x);
       own += head_cost(x, span, chain) * a.Hkv;
     }
   }
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       long long at = upto - own;
       int r = r_lo;
       while (per > 1) {
-        load_req<kPaged>(a, r, x);
+        load_line_req<kPaged>(a, r, x);
         const long long t = head_cost(x, span, chain) * a.Hkv;
         if (begin < at + t) break;
         at += t;

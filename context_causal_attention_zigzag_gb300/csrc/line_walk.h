@@ -106,7 +106,7 @@ struct Walk {
                 left = 0;
                 return false;
               }
-              load_req<kPaged>(a, p.r, p.x);
+              load_line_req<kPaged>(a, p.r, p.x);
             } while (p.x.n == 0);
             items = items_of(p.x, span);
           }

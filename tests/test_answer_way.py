@@ -22,7 +22,7 @@ using namespace cpattn;
 int main() {
   TreeArgs a = {};
   while (scanf("%d %d %d %d %d %d %d", &a.N, &a.R, &a.H, &a.Hkv, &a.D, &a.Nk, &a.causal) == 7)
-    printf("%d\n", (int)prompt_way(a, 152));
+    printf("%d %d\n", (int)prompt_way(a, 152).by, prompt_way(a, 152).above);
   return 0;
 }
 """
@@ -43,7 +43,7 @@ def way(tmp_path_factory):
     def ask(N, R, H, Hkv, D, Nk=None, causal=True):
         line = " ".join(str(int(x)) for x in (N, R, H, Hkv, D, N if Nk is None else Nk, causal))
         out = subprocess.run([str(exe)], input=line, capture_output=True, text=True, check=True).stdout.split()
-        return NAMES[int(out[0])]
+        return NAMES[int(out[0])] + (f"+{out[1]}" if out[1] != "0" else "")
     return ask
 
 
@@ -57,6 +57,14 @@ def test_planned_calls_are_sorted(way):
         assert way(N, R, H, Hkv, D) == "sorted"
 
 
+def test_tests_of_shared_batches_share_them(way):
+    from test_gpu_answer_ways import SHARE, SHARED
+    for causal in (True, False):
+        assert [way(sum(nq), len(nq), H, Hkv, D, sum(nk or nq), causal) for nq, nk, H, Hkv, D in SHARED] == \
+            [f"small+{SHARE}"] * len(SHARED)
+    assert way(463, 64, 32, 8, 128) == f"small+{SHARE}"
+
+
 def test_tests_of_the_softmax_correction_reach_every_tensor_core_kernel(way):
     cases = marks(test_gpu_answer_rescale.test_rising_scores_in_prompts, "nq,nk,H,Hkv,D")
     want = ["sorted"] * 6 + ["direct"] * 2 + ["line"] * 3
@@ -68,3 +76,32 @@ def test_tests_of_weak_weights_reach_every_tensor_core_kernel(way):
     cases = marks(test_gpu_answer_weights.test_many_weak_keys_behind_a_strong_one_in_a_prompt, "nq,nk,R,H,Hkv,D")
     assert [way(nq * R, R, H, Hkv, D, nk * R, False) for nq, nk, R, H, Hkv, D in cases] == \
         ["sorted"] * 3 + ["line"] * 2
+
+
+# sequences of nq queries and nk keys (None: nq), H, Hkv: the kernel; a number behind it:
+# sequences of so many keys and more go to the cut line
+UNEVEN = [
+    ([400] + [1] * 63, None, 32, 8, "small+32"),
+    ([400] + [0] * 63, None, 32, 8, "small+32"),
+    ([2000] + [0] * 511, None, 32, 8, "small+32"),
+    ([1] * 256, [16384] + [1] * 255, 32, 8, "small+256"),
+    ([1] * 38, [19000] + [1] * 37, 8, 1, "line"),
+    ([128] * 4, [4128] + [128] * 3, 32, 8, "line"),
+]
+EVEN = [
+    ([77], None, 32, 8, "direct"),
+    ([4] * 8, None, 32, 8, "small"),
+    ([1] * 64, None, 32, 8, "small"),
+    ([128] * 4, [500] * 4, 32, 8, "direct"),
+    ([16] * 8, None, 32, 8, "direct"),
+    ([16] * 64, None, 32, 8, "line"),
+    ([1], [1001], 32, 8, "line"),
+    ([1000] * 16, None, 32, 8, "sorted"),
+]
+
+
+@pytest.mark.parametrize("nq,nk,H,Hkv,want", UNEVEN + EVEN)
+def test_the_longest_sequence_is_kept_in_mind(way, nq, nk, H, Hkv, want):
+    """No kernel whose blocks walk a sequence alone takes a batch of which one sequence
+    could hold nearly all keys."""
+    assert way(sum(nq), len(nq), H, Hkv, 128, sum(nk or nq)) == want
