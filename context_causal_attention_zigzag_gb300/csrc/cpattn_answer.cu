@@ -54,10 +54,11 @@ bool check_cache(const void* k, const void* v, const CacheShape& c, int D) {
 
 // Rows of a packed tensor, positions of a request in the cache and requests (the
 // empty ones are passed one by one): within these an item, and the way to it, take
-// less than the kernels' bounded waits allow (2 s).  A key tile takes 1.6 us of
-// packed keys; in pages of 16 at most 3 us (64 KB at the 3.4 TB/s that 16 drafted
-// trees reach, their start and merge included).
-constexpr int kMostRows = 1 << 27;
+// less than the kernels' bounded waits allow (2 s), some of which last a whole item.
+// A key tile of packed keys takes 1.6 us at 1.9 GHz and 2.1 us at 1.5, where a GPU at
+// its power limit was seen: 2^19 of them 1.1 s.  In pages of 16 it takes 2.0 us (items
+// of 128 rows behind 131072 positions), 2.5 us at 1.5 GHz: 1.3 s.
+constexpr int kMostRows = 1 << 26;
 constexpr int kMostPositions = 1 << 26;
 constexpr int kMostRequests = 1 << 20;
 

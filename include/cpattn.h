@@ -644,7 +644,7 @@ CPATTN_API int cpattn_tree_attn(const void* q, int64_t q_stride, const void* k_c
  * j <= i + nk - nq -- the last query sees every key, so that keys of a part
  * answered earlier may stand in front -- or (causal = 0) all nk.
  *   q [Nq, H, D], k, v [Nk, Hkv, D], tokens q_stride, k_stride, v_stride apart;
- *   out [Nq, H, D]; lse [H, Nq] float32.  Nq, Nk at most 2^27, R at most 2^20,
+ *   out [Nq, H, D]; lse [H, Nq] float32.  Nq, Nk at most 2^26, R at most 2^20,
  *   (Nq / 128 + R) * H below 2^30.
  * A query that sees nothing gets out = 0 and lse = -inf.  Rows of out and lse
  * behind cu_q[R] are left as they were; what lies in rows of other sequences

@@ -142,3 +142,11 @@ def test_sizes_whose_work_could_outlast_the_bounded_waits_are_refused():
     assert call("cpattn_prompt_attn", PROMPT, R=most + 1) == E
     assert call("cpattn_prompt_attn", PROMPT, R=most, H=1024, Hkv=512, qs=1024 * 64, ks=512 * 64,
                 vs=512 * 64) == E
+
+
+def test_packed_rows_whose_items_could_outlast_the_bounded_waits_at_a_low_clock_are_refused():
+    # 2^27 keys in one item take more than 2 s at 1.5 GHz.
+    most, apart = 1 << 26, dict(out=ctypes.c_void_p(1 << 50), ws=null)
+    for size in ("Nq", "Nk"):
+        assert call("cpattn_prompt_attn", PROMPT, **{size: most + 1}, **apart) == E
+    assert call("cpattn_prompt_attn", PROMPT, Nq=most, Nk=most, **apart) == W
