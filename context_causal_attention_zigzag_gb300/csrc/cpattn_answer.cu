@@ -39,6 +39,15 @@ bool overlaps(const void* p, int64_t stride, int64_t rows, int heads, int D, con
   return a < b + n && b < a + 2 * ((rows - 1) * stride + (int64_t)heads * D);
 }
 
+// The same for a cache, from its first value to its last.
+bool overlaps(const void* p, const CacheShape& c, int Hkv, int D, const void* out, int64_t n) {
+  const __int128 a = reinterpret_cast<intptr_t>(p), b = reinterpret_cast<intptr_t>(out);
+  const __int128 values = (__int128)(c.num_pages - 1) * c.page_stride +
+                          (__int128)(c.page_size - 1) * c.token_stride +
+                          (__int128)(Hkv - 1) * c.head_stride + D;
+  return a < b + n && b < a + 2 * values;
+}
+
 bool page_size_ok(int P) {
   return P == 16 || P == 32 || P == 64 || (P >= 128 && P <= 1024 && P % 128 == 0);
 }
@@ -183,6 +192,9 @@ int cpattn_tree_attn(const void* q, int64_t q_stride, const void* k_cache, const
   if (!workspace || !aligned(workspace, 256) ||
       workspace_bytes < tree_workspace_bytes(N, H, Hkv, D))
     return CPATTN_ERR_WORKSPACE;
+  const int64_t out_bytes = 2 * (int64_t)N * H * D;
+  if (overlaps(k_cache, c, Hkv, D, out, out_bytes) || overlaps(v_cache, c, Hkv, D, out, out_bytes))
+    return CPATTN_ERR_INVALID_ARG;
   int* err = device_error_word();
   if (err == nullptr) return CPATTN_ERR_CUDA;
   TreeArgs a;

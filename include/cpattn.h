@@ -565,8 +565,8 @@ CPATTN_API int cpattn_attention_host_docs(const void* q, const void* k, const vo
  * + p % page_size.  16-byte aligned pointers, strides multiples of 8, page_size *
  * num_pages below 2^31.
  *
- * Outputs and workspace overlap no input (an out that overlaps q, k or v is
- * refused).  A call's kernels follow one another on its stream, and can be
+ * Outputs and workspace overlap no input (an out that overlaps q, k, v or lies
+ * between the first and the last value of a cache is refused).  A call's kernels follow one another on its stream, and can be
  * captured into a graph whose replays see the lengths and tables of their time;
  * make the first such call on a device before any capture.
  */

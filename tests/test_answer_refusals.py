@@ -150,3 +150,13 @@ def test_packed_rows_whose_items_could_outlast_the_bounded_waits_at_a_low_clock_
     for size in ("Nq", "Nk"):
         assert call("cpattn_prompt_attn", PROMPT, **{size: most + 1}, **apart) == E
     assert call("cpattn_prompt_attn", PROMPT, Nq=most, Nk=most, **apart) == W
+
+
+def test_an_out_within_a_cache_is_refused():
+    # 8 pages of 16 tokens, 2 heads of 64: 2 * 8 * 2048 bytes; out has 4 * 4 * 64 values.
+    cache, size, out = 0x1000000, 2 * 8 * 2048, 2 * 4 * 4 * 64
+    need = cp_attn.lib().cpattn_tree_attn_workspace_bytes(4, 4, 2, 64)
+    for which in ("kc", "vc"):
+        for at in (cache, cache + size - 16, cache + 4096, cache - out + 16):
+            args = {which: ctypes.c_void_p(cache), "out": ctypes.c_void_p(at), "wb": need}
+            assert call("cpattn_tree_attn", TREE, **args) == E, (which, at)
