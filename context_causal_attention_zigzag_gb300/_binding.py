@@ -827,8 +827,10 @@ def _answer_outputs(q, N, H, D, out, lse, dev):
         out = torch.empty((N, H, D), device=dev, dtype=q.dtype)
     if lse is None:
         lse = torch.empty((H, N), device=dev, dtype=torch.float32)
-    _on(dev, "out", out, q.dtype, N * H * D)
-    _on(dev, "lse", lse, torch.float32, H * N)
+    if out.shape != (N, H, D) or lse.shape != (H, N):
+        raise ValueError(f"out must be [{N}, {H}, {D}] and lse [{H}, {N}]")
+    _on(dev, "out", out, q.dtype)
+    _on(dev, "lse", lse, torch.float32)
     return out, lse
 
 

@@ -160,3 +160,19 @@ def test_an_out_within_a_cache_is_refused():
         for at in (cache, cache + size - 16, cache + 4096, cache - out + 16):
             args = {which: ctypes.c_void_p(cache), "out": ctypes.c_void_p(at), "wb": need}
             assert call("cpattn_tree_attn", TREE, **args) == E, (which, at)
+
+
+@pytest.mark.parametrize("out,lse", [((4, 6, 64), (4, 6)), ((24, 64), None), (None, (24,)), (None, (1, 6, 4))])
+def test_binding_refuses_outputs_of_another_shape(out, lse):
+    # lse is [H, N]: one of [N, H] would be filled in the other order.
+    class Host:
+        index = -1
+
+    H, N, D = 6, 4, 64
+    q = torch.zeros(N, H, D, dtype=torch.float16)
+    right = torch.empty(N, H, D, dtype=torch.float16), torch.empty(H, N)
+    assert all(a is b for a, b in zip(_binding._answer_outputs(q, N, H, D, *right, Host), right))
+    wrong = (right[0] if out is None else torch.empty(out, dtype=torch.float16),
+             right[1] if lse is None else torch.empty(lse))
+    with pytest.raises(ValueError):
+        _binding._answer_outputs(q, N, H, D, *wrong, Host)
