@@ -124,7 +124,8 @@ int cpattn_page_tables(const int32_t* ctx_lens, const int32_t* new_lens, int R, 
                        const int32_t* free_pages, int num_free, int32_t* block_table,
                        int table_width, int64_t table_stride, int32_t* cu_new, int64_t* slots,
                        int64_t num_slots, int32_t* used, cpattn_stream_t stream) {
-  if (R < 0 || !page_size_ok(page_size) || num_free < 0 || table_width < 0 ||
+  // The kernel steps through the requests in an int.
+  if (R < 0 || R > (1 << 30) || !page_size_ok(page_size) || num_free < 0 || table_width < 0 ||
       table_stride < table_width || num_slots < 0 || num_slots > INT32_MAX)
     return CPATTN_ERR_INVALID_ARG;
   if (!cu_new || !used || (R > 0 && (!ctx_lens || !new_lens)) || (num_free > 0 && !free_pages) ||

@@ -585,7 +585,7 @@ CPATTN_API int cpattn_attention_host_docs(const void* q, const void* k, const vo
  * Tokens whose page is missing (a bad length, a narrow table, an empty pool)
  * get slot -1, so that cpattn_cache_write skips them; tokens behind num_slots
  * are left out (also an error).  Sums of new tokens and of pages stay below
- * 2^31.
+ * 2^31, R at most 2^30.
  */
 CPATTN_API int cpattn_page_tables(const int32_t* ctx_lens, const int32_t* new_lens, int R,
                                   int page_size, const int32_t* free_pages, int num_free,

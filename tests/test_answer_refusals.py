@@ -176,3 +176,9 @@ def test_binding_refuses_outputs_of_another_shape(out, lse):
              right[1] if lse is None else torch.empty(lse))
     with pytest.raises(ValueError):
         _binding._answer_outputs(q, N, H, D, *wrong, Host)
+
+
+def test_page_tables_of_more_requests_than_its_counters_hold_are_refused():
+    # The kernel steps through the requests 1024 at a time in an int.
+    for R in ((1 << 30) + 1, (1 << 31) - 1):
+        assert call("cpattn_page_tables", TABLES, R=R) == E
