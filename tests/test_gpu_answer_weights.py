@@ -4,7 +4,8 @@ The tensor cores multiply weights rounded to the input type.  float16 has a
 smallest step of 2^-24; the largest weight of a row is 2^7 at least, so a weight
 is off by eps/2 of itself or 2^-25 / 2^7 = 2^-32 of the largest, and the sum of the
 weights is no less than the largest: m keys are off by m 2^-32 max |v|.  The other
-terms are those of test_gpu_answer.
+terms are those of test_gpu_answer; an output below 2^-14 is itself rounded to that
+step, by 2^-25.
 """
 import pytest
 import torch
@@ -21,7 +22,7 @@ def tight(q, k, v, seen, scale=None):
     if q.dtype == torch.float16:
         G, most = q.shape[1] // k.shape[1], v.double().abs().amax((0, 2))
         for h in range(q.shape[1]):
-            to[:, h] -= k.shape[0] * (2.0 ** -25 - 2.0 ** -32) * most[h // G]
+            to[:, h] += 2.0 ** -25 - k.shape[0] * (2.0 ** -25 - 2.0 ** -32) * most[h // G]
     return o, lse, to, tl
 
 
