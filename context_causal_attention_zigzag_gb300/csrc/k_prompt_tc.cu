@@ -22,8 +22,8 @@
 // instructions (16 SS and 16 TS of 128 x 128 x 16 per key tile and item, 1.52 us at
 // 1.9 GHz against 1.57-1.62 measured per tile), below that what an item costs
 // around its tiles (about 2.5 us: the last product, the epilogue, the first
-// softmax) and the start (6-8 us).  16384 tokens, H = 32, Hkv = 8, D = 128: 1.33-1.43
-// ms (1.54-1.65 PFLOP/s); 16 prompts of 100-2000: 0.223 ms (1.07 PFLOP/s).
+// softmax) and the start (6-8 us).  16384 tokens, H = 32, Hkv = 8, D = 128: 1.39-1.46
+// ms (1.51-1.59 PFLOP/s); 16 prompts of 100-2000: 0.222 ms (1.08 PFLOP/s).
 //
 // Sequences start at any row: TMA takes any first row, and a tile's rows
 // behind the sequence's end belong to others.  Their scores are replaced by

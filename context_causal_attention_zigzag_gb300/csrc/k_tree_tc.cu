@@ -32,8 +32,8 @@
 // With packed keys instead of a cache (kPaged false) it answers prompts of few
 // rows and many keys.
 // Measured (H = 32, Hkv = 8, D = 128): 64 single tokens over 100-8192 cached ones
-// 183-187 us (6.1 TB/s, 91 % of the copy rate), two trees of 6-8 tokens over
-// 100000-131072 160 us (6.1 TB/s), 16 trees of 5-31 tokens over 500-5000 in pages of
+// 183-188 us (6.0-6.2 TB/s, 90 % of the copy rate), two trees of 6-8 tokens over
+// 100000-131072 158-163 us, 16 trees of 5-31 tokens over 500-5000 in pages of
 // 16 54 us (3.4 TB/s: half of it start, first loads and merge), one token over 1000
 // 13 us.
 // Pages hold whatever was left in them behind a request's last position:
