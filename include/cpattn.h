@@ -569,6 +569,9 @@ CPATTN_API int cpattn_attention_host_docs(const void* q, const void* k, const vo
  * between the first and the last value of a cache is refused).  A call's kernels follow one another on its stream, and can be
  * captured into a graph whose replays see the lengths and tables of their time;
  * make the first such call on a device before any capture.
+ * Which kernel answers follows from the call's sizes, and the kernels round the
+ * softmax weights differently: a sequence's results do not change from run to run,
+ * but may by a rounding with the sizes of the rest of its call.
  */
 
 /*
