@@ -18,4 +18,7 @@ from ._binding import (  # noqa: F401
     ulysses_workspace_bytes, attention_ulysses_fwd_bwd, attention_host,
     attention_host_workspace_bytes, attention_host_parts, attention_host_docs,
     attention_host_docs_workspace_bytes, wait_probe, page_tables, cache_write,
-    tree_attention, tree_attention_workspace, prompt_attention, prompt_attention_workspace)
+    tree_attention, tree_attention_workspace, prompt_attention, prompt_attention_workspace,
+    ROTARY_PLAIN, ROTARY_LINEAR, ROTARY_BASE, ROTARY_PARTS, rotary_frequencies, rotary, rotary_bwd,
+    rotary_cache_write, cache_weights, cache_weights_workspace, cache_evict, cache_evict_workspace,
+    cache_evict_outputs)

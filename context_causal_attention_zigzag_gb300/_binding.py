@@ -24,14 +24,16 @@ CONTIGUOUS = 0
 ZIGZAG = 1
 F32 = 0
 BF16 = 1
-F16 = 2  # the answering calls only
+F16 = 2  # the answering, rotary and cache calls only
 GRAD_F32 = 0x10  # OR into the backward's dtype: dq, dk, dv written as float32
 ONEPASS = 0x20   # OR into the backward's dtype: one-pass tensor-core backward (dQ by reductions)
 PATH_SIMT = 0
 PATH_TCGEN05 = 1
+ROTARY_PLAIN, ROTARY_LINEAR, ROTARY_BASE, ROTARY_PARTS = range(4)
 
 # Every entry point include/cpattn.h declares, with its ctypes signature.
 _vp, _i, _i64, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+_d = ctypes.c_double
 _ip = ctypes.POINTER(ctypes.c_int)
 SIGNATURES = {
     "cpattn_zigzag_permute": (_i, [_vp, _vp, _i64, _i64, _i64, _i, _i, _vp]),
@@ -77,6 +79,17 @@ SIGNATURES = {
                          + [_vp] * 5 + [_i] * 6 + [_f, _vp, _sz, _vp]),
     "cpattn_prompt_attn_workspace_bytes": (_sz, [_i] * 4),
     "cpattn_prompt_attn": (_i, [_vp, _i64] * 3 + [_vp] * 4 + [_i] * 8 + [_f, _vp, _sz, _vp]),
+    "cpattn_rotary_frequencies": (_i, [_vp, _vp, _i, _d, _i] + [_d] * 4),
+    "cpattn_rotary": (_i, [_vp, _i64, _vp, _i64] + [_i] * 7 + [_vp, _f, _i, _vp, _i64, _i64]
+                      + [_i] * 5 + [_vp]),
+    "cpattn_rotary_cache_write": (_i, [_vp, _i64] * 4 + [_vp, _vp, _i64, _i, _i, _vp, _f, _vp, _vp,
+                                                         _i64, _i] + [_i64] * 3 + [_i] * 4 + [_vp]),
+    "cpattn_cache_weights_workspace_bytes": (_sz, [_i] * 4),
+    "cpattn_cache_weights": (_i, [_vp, _i64, _vp, _i64, _i, _i64, _i64, _i64, _vp, _i, _i64]
+                             + [_vp] * 5 + [_f] + [_i] * 6 + [_f, _vp, _sz, _vp]),
+    "cpattn_cache_evict_workspace_bytes": (_sz, [_i] * 5),
+    "cpattn_cache_evict": (_i, [_vp] * 4 + [_i64, _i, _i64, _i64, _i64, _vp, _i, _i64, _vp, _vp]
+                           + [_i] * 3 + [_vp] * 3 + [_i, _vp] + [_i] * 4 + [_vp, _sz, _vp]),
     "cpattn_tile_counts": (_i, [_i64, _i, _i, _i, _i64, _vp, _vp]),
     "cpattn_device_status": (_i, [_vp]),
     "cpattn_wait_probe": (_i, [_i64, _vp]),
@@ -906,6 +919,231 @@ def prompt_attention(q, k, v, cu_q, cu_k=None, causal=True, scale=None, out=None
             cu_q.data_ptr(), cu_k.data_ptr(), out.data_ptr(), lse.data_ptr(), R, Nq, Nk, H, Hkv, D,
             1 if causal else 0, code, _scale(scale), ws.data_ptr(), ws.numel())
     return out, lse
+
+
+# ---------------------------------------------------------------------------
+# rotary positions
+# ---------------------------------------------------------------------------
+
+_ROTARY_DTYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+
+
+def rotary_frequencies(rot, base=10000.0, scaling=ROTARY_PLAIN, factor=1.0, original=0.0, low=1.0,
+                       high=32.0, device="cuda"):
+    """(frequencies float64 [rot / 2] on `device`, magnitude) for heads of which
+    the first `rot` values are turned (cpattn_rotary_frequencies)."""
+    rot = int(rot)
+    freqs, magnitude = torch.empty(max(rot // 2, 0), dtype=torch.float64), ctypes.c_double()
+    rc = lib().cpattn_rotary_frequencies(_ptr(freqs), ctypes.byref(magnitude), rot, base, int(scaling),
+                                         factor, original, low, high)
+    _check("cpattn_rotary_frequencies", rc)
+    return freqs.to(device), magnitude.value
+
+
+def _token_rows(t, name):
+    """(B, S, H, D, token stride) of [B, S, H, D] or [N, H, D] whose tokens' heads lie
+    back to back and whose sequences follow one another."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) == 3:
+        shape, strides = (1,) + tuple(shape), (0,) + tuple(strides)
+    if len(shape) != 4:
+        raise ValueError(f"{name} must be [B, S, H, D] or [tokens, H, D]")
+    B, S, H, D = shape
+    if (strides[3] != 1 and D > 1) or (strides[2] != D and H > 1):
+        raise ValueError(f"a token's heads must lie back to back in {name} (strides {t.stride()})")
+    if S > 1:
+        row = strides[1]
+    else:  # the stride of an axis of one says nothing
+        row = strides[0] if B > 1 else H * D
+    if B > 1 and S > 0 and strides[0] != S * row:
+        raise ValueError(f"the sequences of {name} must follow one another (strides {t.stride()})")
+    return B, S, H, D, row
+
+
+def _turned_values(freqs, device):
+    _on(device, "freqs", freqs, torch.float64)
+    return 2 * freqs.numel()
+
+
+def _rotary(transposed, x, freqs, positions, interleaved, magnitude, offset, cp, layout,
+            from_sharded, to_sharded, length, out):
+    dev = _cuda_device(x)
+    code = _ROTARY_DTYPES.get(x.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {x.dtype}: float32, bfloat16 or float16")
+    B, S_in, H, D, xs = _token_rows(x, "x")
+    rot = _turned_values(freqs, dev)
+    S_out = S_in if length is None else int(length)
+    if from_sharded == to_sharded and not from_sharded and S_out != S_in:
+        raise ValueError("a sequence changes its length only on its way into or out of the ring")
+    if from_sharded and to_sharded and S_out != S_in:
+        raise ValueError("a sequence changes its length only on its way into or out of the ring")
+    # The natural side holds the real tokens.
+    S_nat, S = (S_out, S_in) if from_sharded else (S_in, S_out)
+    if out is None:
+        shape = x.shape[:-3] + (S_out, H, D)
+        out = torch.empty(shape, device=dev, dtype=x.dtype)
+    elif out.shape != x.shape[:-3] + (S_out, H, D) or out.dtype is not x.dtype \
+            or out.get_device() != dev.index:
+        raise ValueError(f"out must be {x.dtype} {tuple(x.shape[:-3]) + (S_out, H, D)} on {dev}")
+    os_ = _token_rows(out, "out")[4]
+    at, ps = None, 0
+    if positions is not None:
+        if positions.shape == (B, S_nat) and B > 1:
+            ps = S_nat
+        elif positions.numel() != S_nat or positions.dim() not in (1, 2):
+            raise ValueError(f"positions must be [{S_nat}] or [{B}, {S_nat}] (natural order)")
+        _on(dev, "positions", positions, torch.int32)
+        at = positions.data_ptr()
+    _launch("cpattn_rotary", dev, x.data_ptr(), xs, out.data_ptr(), os_, B, S_nat, S, H, D, rot,
+            1 if interleaved else 0, freqs.data_ptr(), magnitude, transposed, at, ps, offset, cp,
+            layout, 1 if from_sharded else 0, 1 if to_sharded else 0, code)
+    return out
+
+
+def rotary(x, freqs, positions=None, interleaved=False, magnitude=1.0, offset=0, cp=1,
+           layout=ZIGZAG, from_sharded=False, to_sharded=False, length=None, out=None):
+    """Turns the first 2 * len(freqs) values of each head of x [B, S, H, D] or
+    [tokens, H, D] to the tokens' positions (cpattn_rotary), bringing x into
+    (to_sharded) or out of (from_sharded) the ranks' order in the same pass.
+    positions int32 [S] or [B, S] in natural order; None: offset + the natural
+    position.  length: tokens of out where they are not x's (padding added on the
+    way in, dropped on the way out)."""
+    return _rotary(0, x, freqs, positions, interleaved, magnitude, offset, cp, layout, from_sharded,
+                   to_sharded, length, out)
+
+
+def rotary_bwd(dout, freqs, positions=None, interleaved=False, magnitude=1.0, offset=0, cp=1,
+               layout=ZIGZAG, from_sharded=False, to_sharded=False, length=None, out=None):
+    """The gradient of rotary: dout turned back.  from_sharded and to_sharded are
+    the orders of dout and of what is returned (those of rotary exchanged)."""
+    return _rotary(1, dout, freqs, positions, interleaved, magnitude, offset, cp, layout,
+                   from_sharded, to_sharded, length, out)
+
+
+def rotary_cache_write(q, k, v, freqs, positions, k_cache, v_cache, slots, interleaved=False,
+                       magnitude=1.0, out=None):
+    """A step's tokens: q [N, H, D] turned to its positions (int32 [N]), k turned and
+    v as it is written to their slots of the cache (cpattn_rotary_cache_write).
+    Returns (q turned, k_cache, v_cache); out may be q."""
+    dev = _cuda_device(q)
+    if k.shape != v.shape or k.dtype != q.dtype or v.dtype != q.dtype \
+            or k.get_device() != dev.index or v.get_device() != dev.index:
+        raise ValueError("k and v must share a shape, and q's dtype and device")
+    code, qs, ks, vs = (_answer_dtype(q), _heads_rows(q, "q"), _heads_rows(k, "k"),
+                        _heads_rows(v, "v"))
+    N, H, D = q.shape
+    Nk, Hkv, Dk = k.shape
+    if Nk != N or Dk != D:
+        raise ValueError("q, k and v must share their tokens and D")
+    cache = _cache_args(k_cache, v_cache, Hkv, D, q.dtype, dev)
+    rot = _turned_values(freqs, dev)
+    _on(dev, "positions", positions, torch.int32, N)
+    _on(dev, "slots", slots, torch.int64, N)
+    if out is None:
+        out = torch.empty((N, H, D), device=dev, dtype=q.dtype)
+    elif out.shape != q.shape or out.dtype is not q.dtype or out.get_device() != dev.index:
+        raise ValueError(f"out must be {q.dtype} {tuple(q.shape)} on {dev}")
+    _launch("cpattn_rotary_cache_write", dev, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+            out.data_ptr(), _heads_rows(out, "out"), positions.data_ptr(), slots.data_ptr(), N, rot,
+            1 if interleaved else 0, freqs.data_ptr(), magnitude, k_cache.data_ptr(),
+            v_cache.data_ptr(), *cache, H, Hkv, D, code)
+    return out, k_cache, v_cache
+
+
+# ---------------------------------------------------------------------------
+# the weight of cached positions, and eviction
+# ---------------------------------------------------------------------------
+
+def _page_values(t, name, pages, Hkv, page_size, device):
+    if t.shape != (pages, Hkv, page_size):
+        raise ValueError(f"{name} must be [{pages}, {Hkv}, {page_size}]")
+    _on(device, name, t, torch.float32)
+
+
+def cache_weights_workspace(q, k_cache, cu):
+    """Scratch for cache_weights calls with q of this shape."""
+    N, H, D = q.shape
+    return _workspace(None, q.device, lib().cpattn_cache_weights_workspace_bytes, N, H,
+                      k_cache.shape[2], D)
+
+
+def cache_weights(q, k_cache, block_table, ctx_lens, cu, lse, weights, tree=None, scale=None,
+                  decay=1.0, workspace=None):
+    """What a call of tree_attention (its q, cache, lengths, tree and scale, and
+    the lse it returned) gave to each cached position, added to weights float32
+    [pages, Hkv, page_size] (cpattn_cache_weights); returns weights."""
+    dev = _cuda_device(q)
+    code, qs = _answer_dtype(q), _heads_rows(q, "q")
+    N, H, D = q.shape
+    Hkv, R = k_cache.shape[2], cu.numel() - 1
+    cache = _cache_args(k_cache, k_cache, Hkv, D, q.dtype, dev)
+    _on(dev, "cu", cu, torch.int32)
+    _on(dev, "ctx_lens", ctx_lens, torch.int32, R)
+    width, stride = _table_args(block_table, R, dev)
+    if tree is not None:
+        _on(dev, "tree", tree, torch.int64, N)
+    if lse.shape != (H, N):
+        raise ValueError(f"lse must be [{H}, {N}]")
+    _on(dev, "lse", lse, torch.float32)
+    _page_values(weights, "weights", cache[0], Hkv, cache[1], dev)
+    ws = _workspace(workspace, dev, lib().cpattn_cache_weights_workspace_bytes, N, H, Hkv, D)
+    _launch("cpattn_cache_weights", dev, q.data_ptr(), qs, k_cache.data_ptr(), *cache,
+            block_table.data_ptr(), width, stride, ctx_lens.data_ptr(), cu.data_ptr(),
+            None if tree is None else tree.data_ptr(), lse.data_ptr(), weights.data_ptr(), decay, R,
+            N, H, Hkv, D, code, _scale(scale), ws.data_ptr(), ws.numel())
+    return weights
+
+
+def cache_evict_workspace(k_cache, block_table, most):
+    """Scratch for cache_evict calls of these shapes."""
+    R, width = block_table.shape
+    return _workspace(None, k_cache.device, lib().cpattn_cache_evict_workspace_bytes, R,
+                      k_cache.shape[2], width, k_cache.shape[1], int(most))
+
+
+def cache_evict_outputs(k_cache, block_table, ctx_lens, most):
+    """(new_lens, kept, freed, num_freed) for cache_evict calls of these shapes."""
+    dev, R = k_cache.device, ctx_lens.numel()
+    return tuple(torch.empty(shape, device=dev, dtype=torch.int32)
+                 for shape in ((R,), (R, k_cache.shape[2], int(most)), (block_table.numel(),), (1,)))
+
+
+def cache_evict(weights, k_cache, v_cache, block_table, ctx_lens, keep, most, first=0, recent=0,
+                scores=None, outputs=None, workspace=None):
+    """Brings each request's cache down to keep (int32 [R]) positions: for each kv
+    head its first, its most recent, and the heaviest by scores (float32, laid out as
+    weights; None: weights) of those between (cpattn_cache_evict).  Keys, values
+    and weights move in place.  Returns (new_lens int32 [R], kept int32 [R, Hkv, most]: where each
+    position was, freed int32: pages no longer needed, num_freed int32 [1])."""
+    dev = _cuda_device(weights)
+    code = _answer_dtype(k_cache)
+    if len(k_cache.shape) != 4:
+        raise ValueError("k_cache and v_cache must be [pages, page_size, Hkv, D] of one shape")
+    Hkv, D = k_cache.shape[2:]
+    cache = _cache_args(k_cache, v_cache, Hkv, D, k_cache.dtype, dev)
+    R, most = ctx_lens.numel(), int(most)
+    _on(dev, "ctx_lens", ctx_lens, torch.int32)
+    _on(dev, "keep", keep, torch.int32, R)
+    width, stride = _table_args(block_table, R, dev)
+    _page_values(weights, "weights", cache[0], Hkv, cache[1], dev)
+    if scores is not None:
+        _page_values(scores, "scores", cache[0], Hkv, cache[1], dev)
+    if outputs is None:
+        outputs = cache_evict_outputs(k_cache, block_table, ctx_lens, most)
+    new_lens, kept, freed, count = outputs
+    _on(dev, "new_lens", new_lens, torch.int32, R)
+    _on(dev, "kept", kept, torch.int32, R * Hkv * most)
+    _on(dev, "freed", freed, torch.int32)
+    _on(dev, "num_freed", count, torch.int32, 1)
+    ws = _workspace(workspace, dev, lib().cpattn_cache_evict_workspace_bytes, R, Hkv, width,
+                    cache[1], most)
+    _launch("cpattn_cache_evict", dev, weights.data_ptr(),
+            None if scores is None else scores.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            *cache, block_table.data_ptr(), width, stride, ctx_lens.data_ptr(), keep.data_ptr(),
+            first, recent, most, new_lens.data_ptr(), kept.data_ptr(), freed.data_ptr(),
+            freed.numel(), count.data_ptr(), R, Hkv, D, code, ws.data_ptr(), ws.numel())
+    return outputs
 
 
 # ---------------------------------------------------------------------------

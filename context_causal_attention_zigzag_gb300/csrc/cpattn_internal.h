@@ -469,6 +469,80 @@ cudaError_t launch_tree_attn(const TreeArgs& a, int dtype, cudaStream_t stream);
 size_t prompt_workspace_bytes(int R, int Nq, int H, int D);
 cudaError_t launch_prompt_attn(const PromptArgs& a, int dtype, cudaStream_t stream);
 
+// ---------------------------------------------------------------------------
+// Rotary positions, the weight of cached positions, eviction.
+// ---------------------------------------------------------------------------
+
+struct RotaryArgs {
+  const void* x;
+  void* out;
+  int64_t x_stride, out_stride;  // elements between tokens
+  int B, S_in, S_out, S_nat;     // tokens of a sequence of x, of out, and real ones
+  int H, D, rot;
+  const double* freqs;
+  float magnitude, sign;  // sign -1: transposed
+  const int* positions;   // nullptr: offset + n
+  int64_t positions_stride, offset;
+  RingShape ring;  // cp, per_rank, L and c
+  bool from_sharded, to_sharded;
+};
+cudaError_t launch_rotary(const RotaryArgs& a, int dtype, bool interleaved, cudaStream_t stream);
+
+struct RotaryWriteArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* out;
+  int64_t q_stride, k_stride, v_stride, out_stride;
+  const int* positions;
+  const int64_t* slots;
+  int64_t N;
+  int H, Hkv, D, rot;
+  const double* freqs;
+  float magnitude;
+  void* k_cache;
+  void* v_cache;
+  CacheShape cache;
+  int* err;
+};
+cudaError_t launch_rotary_write(const RotaryWriteArgs& a, int dtype, bool interleaved,
+                                cudaStream_t stream);
+
+// The weights of a call of cpattn_tree_attn: `t` holds its arguments (out unused,
+// lse the answered ones, read only).
+struct WeightsArgs {
+  TreeArgs t;
+  const float* lse;
+  float* weights;
+  float decay;
+};
+size_t weights_workspace_bytes(int N, int H, int Hkv, int D);
+cudaError_t launch_cache_weights(const WeightsArgs& a, int dtype, cudaStream_t stream);
+
+struct EvictArgs {
+  float* weights;
+  const float* scores;
+  void* k_cache;
+  void* v_cache;
+  CacheShape cache;
+  const int* table;
+  int width;
+  int64_t table_stride;
+  const int* ctx;
+  const int* keep;
+  int first, recent, most;
+  int* new_lens;
+  int* kept;
+  int* freed;
+  int num_freed_max;
+  int* num_freed;
+  int R, Hkv, D;
+  int* lists;  // [R, Hkv, 2, list_cap]: places to fill, and what fills them
+  int64_t list_cap;
+  int* err;
+};
+cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t stream);
+
 // One CTA whose bounded mbarrier wait gives up after limit_ns (raising *err).
 cudaError_t launch_wait_probe(int* err, uint64_t limit_ns, cudaStream_t stream);
 

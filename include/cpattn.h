@@ -72,8 +72,9 @@ enum cpattn_layout { CPATTN_LAYOUT_CONTIGUOUS = 0, CPATTN_LAYOUT_ZIGZAG = 1 };
 enum cpattn_dtype {
   CPATTN_F32 = 0,
   CPATTN_BF16 = 1,
-  /* float16: taken by the answering calls only (cpattn_cache_write,
-   * cpattn_tree_attn, cpattn_prompt_attn); every other call answers
+  /* float16: taken by the answering calls (cpattn_cache_write,
+   * cpattn_tree_attn, cpattn_prompt_attn, cpattn_cache_weights,
+   * cpattn_cache_evict) and the rotary calls only; every other call answers
    * CPATTN_ERR_INVALID_ARG. */
   CPATTN_F16 = 2,
   /* Flag for the backward calls (OR it into dtype): dq, dk, dv are written
@@ -662,6 +663,160 @@ CPATTN_API int cpattn_prompt_attn(const void* q, int64_t q_stride, const void* k
                                   const int32_t* cu_k, void* out, float* lse, int R, int Nq,
                                   int Nk, int H, int Hkv, int D, int causal, int dtype,
                                   float softmax_scale, void* workspace, size_t workspace_bytes,
+                                  cpattn_stream_t stream);
+
+/*
+ * Rotary positions.  The pages' models give attention its positions before the
+ * ring; these calls turn q and k (and their gradients) where the ring and the
+ * cache hold them.
+ *
+ * Of each head's D values the first `rot` are pairs, pair i being the values
+ * (i, i + rot / 2), or (2 i, 2 i + 1) with interleaved = 1; the others pass.
+ * At position p, pair (a, b) of frequency f = freqs[i] (radians a position)
+ * becomes
+ *   (m (a cos pf - b sin pf), m (a sin pf + b cos pf)),  m = magnitude,
+ * and with transposed = 1 (the gradient of that) the same with -sin.  Angles
+ * are reduced in 64-bit fixed point, so that far positions lose nothing;
+ * products and sums are float32, rounded once.
+ *
+ * cpattn_rotary_frequencies (host only) fills freqs [rot / 2] and *magnitude:
+ *   CPATTN_ROTARY_PLAIN   f_i = base^(-2 i / rot)
+ *   CPATTN_ROTARY_LINEAR  f_i / factor
+ *   CPATTN_ROTARY_BASE    the base times factor^(rot / (rot - 2))  (rot > 2)
+ *   CPATTN_ROTARY_PARTS   by turns within the length `original` that the model was
+ *     trained on, r_i = original f_i / 2 pi: f_i / factor below `low`, f_i above
+ *     `high`, and with g = (r_i - low) / (high - low) in between
+ *     (1 - g) f_i / factor + g f_i; magnitude 0.1 ln(factor) + 1
+ * (magnitude 1 otherwise).  rot even and at least 2, base > 1, factor >= 1 and,
+ * for PARTS, original > 0 and 0 <= low < high.
+ */
+enum cpattn_rotary_scaling {
+  CPATTN_ROTARY_PLAIN = 0,
+  CPATTN_ROTARY_LINEAR = 1,
+  CPATTN_ROTARY_BASE = 2,
+  CPATTN_ROTARY_PARTS = 3
+};
+CPATTN_API int cpattn_rotary_frequencies(double* freqs, double* magnitude, int rot, double base,
+                                         int scaling, double factor, double original, double low,
+                                         double high);
+
+/*
+ * Turns x, and brings it from or into the ranks' order in the same pass.  The
+ * sequence has S_nat tokens in natural order and S in sharded order
+ * (cpattn_zigzag_permute; S_nat <= S, the rest being padding as in
+ * cpattn_zigzag_permute_pad).  x [B, Sx, H, D] is in sharded order (Sx = S) if
+ * from_sharded, else in natural order (Sx = S_nat); out [B, So, H, D] likewise
+ * by to_sharded.  Padding is written as zeros.
+ *   positions: device int32, of natural token n of sequence b at
+ *   positions[b * positions_stride + n] (stride 0: one row for all), any
+ *   value; NULL: offset + n.
+ *   freqs: device float64 [rot / 2], finite.
+ *   Tokens lie x_stride / out_stride elements apart, sequences Sx / So tokens.
+ * dtype CPATTN_F32, CPATTN_BF16 or CPATTN_F16; D a multiple of 8 up to 256, rot even, 2 to
+ * D; x and out 16-byte aligned, strides multiples of 16 bytes.  out may be x
+ * itself (same stride and order), else they must not overlap.  S at most 2^30,
+ * B at most 65535.  The gradient of a call is the same call with transposed = 1
+ * and the orders exchanged.
+ */
+CPATTN_API int cpattn_rotary(const void* x, int64_t x_stride, void* out, int64_t out_stride, int B,
+                             int S_nat, int S, int H, int D, int rot, int interleaved,
+                             const double* freqs, float magnitude, int transposed,
+                             const int32_t* positions, int64_t positions_stride, int64_t offset,
+                             int cp_size, int layout, int from_sharded, int to_sharded, int dtype,
+                             cpattn_stream_t stream);
+
+/*
+ * One step's tokens on their way into the cache: out_i = q_i turned to
+ * positions[i], the key k_i turned likewise and v_i as it is written to slot
+ * slots[i] (as cpattn_cache_write: a negative slot is skipped, one outside the
+ * cache is skipped and raises the error word).  q_i is turned whatever its slot.
+ *   q [N, H, D], out [N, H, D] (out may be q itself), k, v [N, Hkv, D], tokens
+ *   q_stride, out_stride, k_stride, v_stride apart; positions int32 [N].
+ * Types, D and the cache as in the answering calls; rot, freqs, interleaved and
+ * magnitude as above.
+ */
+CPATTN_API int cpattn_rotary_cache_write(
+    const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+    int64_t v_stride, void* out, int64_t out_stride, const int32_t* positions,
+    const int64_t* slots, int64_t N, int rot, int interleaved, const double* freqs,
+    float magnitude, void* k_cache, void* v_cache, int64_t num_pages, int page_size,
+    int64_t page_stride, int64_t token_stride, int64_t head_stride, int H, int Hkv, int D,
+    int dtype, cpattn_stream_t stream);
+
+/*
+ * How much the cached positions are looked at, and a cache that does not grow.
+ * weights: device float32 [num_pages, Hkv, page_size], contiguous, one value
+ * for each position and kv head, in the cache's pages.
+ *
+ * cpattn_cache_weights adds what the new tokens of a call of cpattn_tree_attn
+ * gave to each position: with its q, cache, lengths, tree, scale and the lse
+ * that it answered,
+ *   w_j <- decay w_j + sum_i exp(scale q_i k_j - lse_i)   for j < ctx_lens[r],
+ *   w_j <-             sum_i exp(scale q_i k_j - lse_i)   for the new positions,
+ * the sum over the request's new tokens i that see j and the query heads of the
+ * kv head.  A row whose lse is -inf gives nothing.  Requests without new tokens
+ * are left as they are, and so is everything else in weights; two runs give
+ * the same bits.
+ *   q [N, H, D], tokens q_stride apart; lse [H, N]; decay finite.  The rest, and
+ *   what broken lengths and tables do, as cpattn_tree_attn.
+ * No page belongs to two requests of the call, or the old weights that it holds
+ * may count for either.
+ * workspace: device, at least cpattn_cache_weights_workspace_bytes, 256-byte
+ * aligned, scratch.
+ */
+CPATTN_API size_t cpattn_cache_weights_workspace_bytes(int N, int H, int Hkv, int D);
+CPATTN_API int cpattn_cache_weights(const void* q, int64_t q_stride, const void* k_cache,
+                                    int64_t num_pages, int page_size, int64_t page_stride,
+                                    int64_t token_stride, int64_t head_stride,
+                                    const int32_t* block_table, int table_width,
+                                    int64_t table_stride, const int32_t* ctx_lens,
+                                    const int32_t* cu_new, const uint64_t* tree, const float* lse,
+                                    float* weights, float decay, int R, int N, int H, int Hkv,
+                                    int D, int dtype, float softmax_scale, void* workspace,
+                                    size_t workspace_bytes, cpattn_stream_t stream);
+
+/*
+ * Brings each request's cache down to keep[r] positions.  A request of c =
+ * ctx_lens[r] <= keep[r] positions stays as it is.  Of any other, with f =
+ * min(first, keep), t = min(recent, keep - f) and cut = keep - t, each kv head
+ * by itself keeps its first f positions, its last t, and of those between them
+ * the cut - f of the highest scores (of equal ones the lowest position; NaN is
+ * below all others).  They move as little as possible: what stays and lies
+ * below the cut stays in place, the places below the cut that became free are
+ * filled in ascending order with what stays from behind it, in its order, and the last t
+ * follow in their order, to position keep.  Keys, values and weights move
+ * together.  Attention over the cache does not depend on the order, and the
+ * last positions are again the most recent.
+ *   scores: float32, laid out as weights (which may be passed: NULL selects
+ *   them).  Scores are not moved.
+ *   new_lens [R] int32: min(c, keep).
+ *   kept [R, Hkv, most] int32: where the position now at i was, -1 from
+ *   new_lens[r] on.  keep[r] <= most for every request that is cut, and c <=
+ *   most for the others.
+ *   freed [num_freed_max] int32: the pages that requests no longer need, in request
+ *   order, then -1; num_freed [1] int32: how many.  The tables stay as they are
+ *   (entries behind a request's last page are not read).
+ * Broken lengths, tables, a negative keep, one above `most`, or too little room
+ * in freed raise the device error word; such a request is left as it is
+ * (new_lens = c), and pages that freed has no room for are not listed.  No page belongs to
+ * two requests of the call.
+ *   first, recent >= 0; most 1 to 2^26; R at most 65535, R * Hkv * most below
+ *   2^40, Hkv at most 65535; the cache as above, dtype CPATTN_BF16 or
+ *   CPATTN_F16.
+ * workspace: device, at least cpattn_cache_evict_workspace_bytes, 256-byte
+ * aligned, scratch.
+ */
+CPATTN_API size_t cpattn_cache_evict_workspace_bytes(int R, int Hkv, int table_width,
+                                                     int page_size, int most);
+CPATTN_API int cpattn_cache_evict(float* weights, const float* scores, void* k_cache,
+                                  void* v_cache, int64_t num_pages, int page_size,
+                                  int64_t page_stride, int64_t token_stride, int64_t head_stride,
+                                  const int32_t* block_table, int table_width,
+                                  int64_t table_stride, const int32_t* ctx_lens,
+                                  const int32_t* keep, int first, int recent, int most,
+                                  int32_t* new_lens, int32_t* kept, int32_t* freed,
+                                  int num_freed_max, int32_t* num_freed, int R, int Hkv, int D,
+                                  int dtype, void* workspace, size_t workspace_bytes,
                                   cpattn_stream_t stream);
 
 /*
