@@ -173,7 +173,7 @@ int cpattn_rotary_cache_write(const void* q, int64_t q_stride, const void* k, in
 
 size_t cpattn_cache_weights_workspace_bytes(int N, int H, int Hkv, int D) {
   if (N < 0 || check_heads(H, Hkv, D, CPATTN_BF16) != CPATTN_OK) return 0;
-  return weights_workspace_bytes(N, H, Hkv, D);
+  return weights_workspace_bytes();
 }
 
 int cpattn_cache_weights(const void* q, int64_t q_stride, const void* k_cache, int64_t num_pages,
@@ -185,7 +185,7 @@ int cpattn_cache_weights(const void* q, int64_t q_stride, const void* k_cache, i
                          void* workspace, size_t workspace_bytes, cpattn_stream_t stream) {
   int rc = check_heads(H, Hkv, D, dtype);
   if (rc != CPATTN_OK) return rc;
-  if (R < 0 || R > kMostRequests || N < 0 || (int64_t)N * (H / Hkv) > (1 << 30) ||
+  if (R < 0 || R > kMostRequests || N < 0 || (int64_t)N * (H / Hkv) > (1 << 27) ||
       !scale_ok(softmax_scale) || !isfinite(decay))
     return CPATTN_ERR_INVALID_ARG;
   CacheShape c = {num_pages, page_size, page_stride, token_stride, head_stride};
@@ -204,7 +204,7 @@ int cpattn_cache_weights(const void* q, int64_t q_stride, const void* k_cache, i
       rows_meet(weights, ww, 1, ww, lse, 4 * (Bytes)H * N, 1, 4 * (Bytes)H * N))
     return CPATTN_ERR_INVALID_ARG;
   if (!workspace || !aligned(workspace, 256) ||
-      workspace_bytes < weights_workspace_bytes(N, H, Hkv, D))
+      workspace_bytes < weights_workspace_bytes())
     return CPATTN_ERR_WORKSPACE;
   int* err = device_error_word();
   if (err == nullptr) return CPATTN_ERR_CUDA;

@@ -423,6 +423,12 @@ bool encode_tiled(CUtensorMap* m, bool bf16, int rank, const void* ptr, const cu
 bool rows_map(CUtensorMap* m, const void* ptr, bool bf16, int heads, int D, int64_t stride,
               int64_t rows);
 
+// The cache, box 64 columns of up to 128 tokens of one page and head; tokens that
+// share a box of Q, and Q in such boxes (k_tree_tc.cu).
+bool cache_map(CUtensorMap* m, const void* ptr, bool bf16, const CacheShape& c, int Hkv, int D);
+int query_box(int R, int N, int G);
+bool query_map(CUtensorMap* m, const TreeArgs& a, bool bf16, int G, int D, int tokens);
+
 // What one request asks for, held to the buffers whatever its lengths say.
 struct Req {
   int q0, n;   // its rows of q
@@ -516,7 +522,10 @@ struct WeightsArgs {
   float* weights;
   float decay;
 };
-size_t weights_workspace_bytes(int N, int H, int Hkv, int D);
+size_t weights_workspace_bytes();
+// On the tensor cores (k_weights_tc.cu).
+cudaError_t launch_tc_weights(const WeightsArgs& a, int dtype, int dev, int sms,
+                              cudaStream_t stream);
 cudaError_t launch_cache_weights(const WeightsArgs& a, int dtype, cudaStream_t stream);
 
 struct EvictArgs {

@@ -839,37 +839,6 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const Tree
 // host side
 // ---------------------------------------------------------------------------
 
-// The cache as a 4-D tensor (d, head, token of the page, page), box 64 columns
-// of up to 128 tokens of one page and head.
-bool make_map(CUtensorMap* m, const void* ptr, bool bf16, const CacheShape& c, int Hkv, int D) {
-  cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)Hkv, (cuuint64_t)c.page_size,
-                        (cuuint64_t)c.num_pages};
-  cuuint64_t strides[3] = {(cuuint64_t)c.head_stride * 2, (cuuint64_t)c.token_stride * 2,
-                           (cuuint64_t)c.page_stride * 2};
-  cuuint32_t box[4] = {64, 1, (cuuint32_t)(c.page_size < kT ? c.page_size : kT), 1};
-  return encode_tiled(m, bf16, 4, ptr, dims, strides, box);
-}
-
-// Tokens of a box of Q: about what a request has on the average, so that little
-// is read for nothing, but whole swizzle groups of 8 rows and a part of a tile
-// (else a tile).
-int query_box(int R, int N, int G) {
-  const int tpt = kT / G;
-  const int64_t mean = ((int64_t)N + R - 1) / R;
-  for (int t = 1; t < tpt; t *= 2)
-    if (t >= mean && t * G % 8 == 0 && tpt % t == 0) return t;
-  return tpt;
-}
-
-// Q as a 3-D tensor (d, head, token), box 64 columns, the heads of a kv head and
-// `tokens` tokens.
-bool query_map(CUtensorMap* m, const TreeArgs& a, bool bf16, int G, int D, int tokens) {
-  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.H, (cuuint64_t)a.N};
-  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.q_stride * 2};
-  cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)tokens};
-  return encode_tiled(m, bf16, 3, a.q, dims, strides, box);
-}
-
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Two row tiles an item where the requests have more than a tile's rows (128)
@@ -890,8 +859,8 @@ cudaError_t run(const TreeArgs& a, int dev, int sms, cudaStream_t stream) {
   const int box = query_box(a.R, a.N, G);
   if (!query_map(&mq, a, kBf16, G, D, box)) return cudaErrorInvalidValue;
   if constexpr (kPaged) {
-    if (!make_map(&mk, a.k_cache, kBf16, a.cache, a.Hkv, D) ||
-        !make_map(&mv, a.v_cache, kBf16, a.cache, a.Hkv, D))
+    if (!cache_map(&mk, a.k_cache, kBf16, a.cache, a.Hkv, D) ||
+        !cache_map(&mv, a.v_cache, kBf16, a.cache, a.Hkv, D))
       return cudaErrorInvalidValue;
   } else {
     if (!rows_map(&mk, a.k_cache, kBf16, a.Hkv, D, a.k_stride, a.Nk) ||
@@ -927,6 +896,37 @@ cudaError_t run(const TreeArgs& a, int dev, int sms, cudaStream_t stream) {
 }
 
 }  // namespace
+
+// The cache as a 4-D tensor (d, head, token of the page, page), box 64 columns
+// of up to 128 tokens of one page and head.
+bool cache_map(CUtensorMap* m, const void* ptr, bool bf16, const CacheShape& c, int Hkv, int D) {
+  cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)Hkv, (cuuint64_t)c.page_size,
+                        (cuuint64_t)c.num_pages};
+  cuuint64_t strides[3] = {(cuuint64_t)c.head_stride * 2, (cuuint64_t)c.token_stride * 2,
+                           (cuuint64_t)c.page_stride * 2};
+  cuuint32_t box[4] = {64, 1, (cuuint32_t)(c.page_size < kT ? c.page_size : kT), 1};
+  return encode_tiled(m, bf16, 4, ptr, dims, strides, box);
+}
+
+// Tokens of a box of Q: about what a request has on the average, so that little
+// is read for nothing, but whole swizzle groups of 8 rows and a part of a tile
+// (else a tile).
+int query_box(int R, int N, int G) {
+  const int tpt = kT / G;
+  const int64_t mean = ((int64_t)N + R - 1) / R;
+  for (int t = 1; t < tpt; t *= 2)
+    if (t >= mean && t * G % 8 == 0 && tpt % t == 0) return t;
+  return tpt;
+}
+
+// Q as a 3-D tensor (d, head, token), box 64 columns, the heads of a kv head and
+// `tokens` tokens.
+bool query_map(CUtensorMap* m, const TreeArgs& a, bool bf16, int G, int D, int tokens) {
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.H, (cuuint64_t)a.N};
+  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.q_stride * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)tokens};
+  return encode_tiled(m, bf16, 3, a.q, dims, strides, box);
+}
 
 namespace {
 size_t places_bytes(size_t rows, int D) {

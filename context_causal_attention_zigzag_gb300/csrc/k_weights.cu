@@ -131,15 +131,16 @@ cudaError_t run(const WeightsArgs& w, int sms, cudaStream_t stream) {
 
 }  // namespace
 
-size_t weights_workspace_bytes(int, int, int, int) { return 0; }
-
 cudaError_t launch_cache_weights(const WeightsArgs& w, int dtype, cudaStream_t stream) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  return dtype == CPATTN_BF16 ? run<true>(w, sms, stream) : run<false>(w, sms, stream);
+  const int64_t rows = (int64_t)w.t.N * (w.t.H / w.t.Hkv);
+  if (rows <= 32 && (int64_t)w.t.width * w.t.cache.page_size <= 2048)
+    return dtype == CPATTN_BF16 ? run<true>(w, sms, stream) : run<false>(w, sms, stream);
+  return launch_tc_weights(w, dtype, dev, sms, stream);
 }
 
 }  // namespace cpattn
