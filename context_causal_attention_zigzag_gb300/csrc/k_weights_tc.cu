@@ -5,13 +5,14 @@
 // With the normalisers known the sum needs no running maximum and no second
 // product: S = K Q^T has a key a row, so a thread of the epilogue holds one key and
 // adds up its row, exp by exp, and nothing is exchanged.
-//  * An item is 256 keys of a kv head: two key tiles, whose products with a tile of
-//    128 rows (tokens x query heads) alternate.  A key tile is the products' left
-//    operand and stays in TMEM for all of them (a product from shared memory runs at
-//    60 % of the tensor rate, from TMEM at 86 %); only the rows stream, by TMA.
-//  * Many rows (prompts): bound by the tensor cores.  Few rows (single tokens, drafts):
-//    by HBM, which the ring of key tiles keeps loading; the rows of a request and kv
-//    head then stay in shared memory from one item to the next.
+//  * An item is 256 keys of a kv head: two key tiles, which share the tiles of 128 rows
+//    (tokens x query heads).  Both lie in shared memory; TMA loads pages and rows.
+//  * Many rows (prompts): bound by the tensor cores and the exponentials.  Three
+//    warpgroups take the steps (a tile of rows each) by turns and walk both key tiles'
+//    rows of products; at the item's end their sums meet in shared memory.
+//  * Few rows (single tokens, drafts): bound by HBM, which the ring of key tiles keeps
+//    loading.  A warpgroup takes a key tile, and the rows of a request and kv head stay in
+//    shared memory from one item to the next.
 //  * The work is cut without regard to requests and items: all products of all items
 //    stand in one line and CTA c of N takes the c-th N-th of it.  An item that a cut
 //    divides leaves float32 sums, joined in order by weights_merge_kernel, so that
@@ -22,10 +23,9 @@
 // rows of S of their own, which nobody stores.  Columns of tokens behind its last one,
 // or that do not see a key, are passed over by selection.
 //
-// CTA = 384 threads: warp 0 loads K, warp 2 Q, warp 3 the normalisers (and notes down the pieces), warp 1 owns
-// TMEM and issues the products, warps 4-7 and 8-11 take a key tile each: they move it from
-// shared memory to TMEM and read the products' rows.  TMEM: S0 [0,128) S1 [128,256), then
-// two places for each key tile [256,512).
+// Threads: warp 0 loads K and Q, warps 1 and 2 issue the products of a key tile each,
+// warp 3 writes down the pieces and the normalisers, warps 4-11 or 4-15 are the
+// warpgroups, a key a thread.  TMEM: two places of 128 columns for each key tile's products.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -45,23 +45,8 @@ using namespace wline;
 
 constexpr int kT = kTcTile;
 constexpr int kBoxBytes = kT * 64 * 2;
-constexpr int kThreads = 384;
 constexpr int kMaxCtas = 160;  // sums are laid out for so many
 constexpr float kLog2e = 1.4426950408889634f;
-// Registers per thread of the control warps and of the warpgroups, which hold a row of
-// products (setmaxnreg); the launch gives 384 threads x 168.
-constexpr int kRegCtl = 128, kRegSum = 184;
-static_assert(128 * kRegCtl + 256 * kRegSum <= kThreads * 168, "register split");
-
-template <int N>
-__device__ __forceinline__ void reg_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void reg_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 // What the warpgroups need to know of a piece; warp 3 writes it down, so that their
 // registers are left to the products.
 struct __align__(16) Note {
@@ -70,48 +55,56 @@ struct __align__(16) Note {
   int s0, s1, begins[2];
   int more, last, fresh, whole;  // more: another piece follows
   int end_cta;                   // that holds the item's last step
-  int pad[3];
+  int in_page[2];                // where a key tile begins within its page
+  int pad;
+  int page[16];                  // of each 128 / page_size-th of the tiles (a tile each from 128 on)
 };
 constexpr int kNotes = 4;
 
-// kDeep: deeper rings of keys (few rows a request), else of rows.  Each key tile of the
-// pair has a ring of its own: the warpgroup that takes it then sees every phase of its
-// barriers (of a shared ring's it would miss those of the other's tiles, and take one
+// kDeep: few rows a request, deeper rings of keys, else of rows.  Each key tile of the
+// pair has a ring of its own: the warpgroups that take it then see every phase of its
+// barriers (of a shared ring's they would miss those of the other's tiles, and take one
 // for the next but one).
 template <int D, bool kDeep>
 struct Cfg {
+  static constexpr int kGroups = kDeep ? 2 : 3;  // warpgroups
+  static constexpr int kHands = 128 * kGroups;   // their threads
+  static constexpr int kThreads = 128 + kHands;
   static constexpr int kHalves = D / 64;
   static constexpr int kTileBytes = kHalves * kBoxBytes;
-  static constexpr int kDepth = (D == 128 ? 1 : 2) * (kDeep ? 2 : 1);  // of a key tile's ring
+  static constexpr int kDepth = D == 128 || !kDeep ? 2 : 4;  // of a key tile's ring
   static constexpr int kKeys = 2 * kDepth;
-  static constexpr int kRows = (D == 128 ? 1 : 2) * (kDeep ? 2 : 4);
+  static constexpr int kRows = D == 128 ? 2 : (kDeep ? 4 : 8);
+  // Of normalisers: more than the warpgroups that take the steps by turns, so that none waits
+  // for a place of which it has not seen the phase before.
+  static constexpr int kNorms = kRows < 4 ? 4 : kRows;
   static constexpr int kOffK = 0;
   static constexpr int kOffQ = kKeys * kTileBytes;
   static constexpr int kOffL = kOffQ + kRows * kTileBytes;  // also the prologue's sums
-  static constexpr int kOffBar = kOffL + kRows * kT * 4;
+  static constexpr int kOffX = kOffL + kNorms * kT * 4;  // sums, by turns
+  static constexpr int kOffBar = kOffX + (kDeep ? 0 : 2 * kGroups * kPair * 4);
   static constexpr int kBarKFull = 0;
   static constexpr int kBarKEmpty = kBarKFull + kKeys;
   static constexpr int kBarQFull = kBarKEmpty + kKeys;
   static constexpr int kBarQEmpty = kBarQFull + kRows;
   static constexpr int kBarLFull = kBarQEmpty + kRows;
-  static constexpr int kBarLEmpty = kBarLFull + kRows;
-  static constexpr int kBarS = kBarLEmpty + kRows;    // [2] products of a tile are there
-  static constexpr int kBarSFree = kBarS + 2;         // [2] and have been read
-  static constexpr int kBarA = kBarSFree + 2;         // [2][2] a key tile is in its place
-  static constexpr int kBarPFull = kBarA + 4;      // a piece's notes
+  static constexpr int kBarLEmpty = kBarLFull + kNorms;
+  static constexpr int kBarS = kBarLEmpty + kNorms;      // [2][2][3] products are there, for a reader
+  static constexpr int kBarSFree = kBarS + 12;          // [2][2] and have been read
+  static constexpr int kBarPFull = kBarSFree + 4;       // a piece's notes
   static constexpr int kBarPEmpty = kBarPFull + kNotes;
-  static constexpr int kBarDrain = kBarPEmpty + kNotes;
-  static constexpr int kNumBars = kBarDrain + 1;
+  static constexpr int kBarXFull = kBarPEmpty + kNotes;  // [2] the warpgroups' sums
+  static constexpr int kBarXEmpty = kBarXFull + 2;
+  static constexpr int kBarDrain = kBarXEmpty + 2;
+  static constexpr int kNumBars = kBarDrain + 2;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kOffNotes = (kOffMisc + 16 + 15) / 16 * 16;
   static constexpr int kSmemBytes = kOffNotes + kNotes * (int)sizeof(Note);
   static_assert(kSmemBytes <= 232448, "shared memory");
 };
 
-__host__ __device__ constexpr uint32_t col_s(int i) { return 128u * (uint32_t)i; }
-__host__ __device__ constexpr uint32_t col_a(int i, int which) {
-  return 256u + 128u * (uint32_t)i + 64u * (uint32_t)which;
-}
+// TMEM: two places of products for each key tile.
+__device__ constexpr uint32_t col_s(int place) { return 128u * (uint32_t)place; }
 
 // The sums of items that were cut: per CTA two places (0: of an item begun by an
 // earlier CTA, 1: of one that goes on in the next), and a record of the item begun
@@ -126,10 +119,11 @@ struct Sums {
 };
 
 template <bool kBf16, int D, bool kDeep>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D, kDeep>::kThreads, 1)
     weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const WeightsArgs args, const Sums out, const int q_box) {
   using C = Cfg<D, kDeep>;
+  constexpr int kThreads = C::kThreads;
   const TreeArgs& a = args.t;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = opaque(smem_u32(smem));
@@ -144,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
-  // [12] of the warps; then where this CTA begins: in_req, r and the request.
+  // [20] of the warps; then where this CTA begins: in_req, r and the request.
   long long* sums = reinterpret_cast<long long*>(smem + C::kOffL);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -156,25 +150,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kKeys; ++s) {
       mbar_init(bar(C::kBarKFull + s), 1);
-      mbar_init(bar(C::kBarKEmpty + s), 128);
+      mbar_init(bar(C::kBarKEmpty + s), 1);
     }
     for (int s = 0; s < C::kRows; ++s) {
       mbar_init(bar(C::kBarQFull + s), 1);
-      mbar_init(bar(C::kBarQEmpty + s), 1);
-      mbar_init(bar(C::kBarLFull + s), 32);
-      mbar_init(bar(C::kBarLEmpty + s), 256);
+      mbar_init(bar(C::kBarQEmpty + s), 2);
     }
+    for (int s = 0; s < C::kNorms; ++s) {
+      mbar_init(bar(C::kBarLFull + s), 32);
+      mbar_init(bar(C::kBarLEmpty + s), kDeep ? 256 : 128);
+    }
+    for (int i = 0; i < 12; ++i) mbar_init(bar(C::kBarS + i), 1);
+    for (int i = 0; i < 4; ++i) mbar_init(bar(C::kBarSFree + i), 128);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(C::kBarS + i), 1);
-      mbar_init(bar(C::kBarSFree + i), 128);
-      mbar_init(bar(C::kBarA + 2 * i), 128);
-      mbar_init(bar(C::kBarA + 2 * i + 1), 128);
+      mbar_init(bar(C::kBarXFull + i), C::kHands);
+      mbar_init(bar(C::kBarXEmpty + i), 256);
     }
     for (int i = 0; i < kNotes; ++i) {
       mbar_init(bar(C::kBarPFull + i), 32);
-      mbar_init(bar(C::kBarPEmpty + i), 256);
+      mbar_init(bar(C::kBarPEmpty + i), C::kHands);
     }
     mbar_init(bar(C::kBarDrain), 1);
+    mbar_init(bar(C::kBarDrain + 1), 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -233,16 +230,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         at += t;
         ++r;
       }
-      sums[13] = begin - at;
-      sums[14] = r;
-      *reinterpret_cast<Req*>(sums + 16) = x;
+      sums[20] = begin - at;
+      sums[21] = r;
+      *reinterpret_cast<Req*>(sums + 22) = x;
     }
   }
   if (threadIdx.x == 0) out.cuts[cta].last = -1;
   __syncthreads();
   const uint32_t tmem = *tmem_slot;
   Walk walk;
-  walk.init(a, tpt, (int)sums[14], *reinterpret_cast<const Req*>(sums + 16), sums[13], begin, count);
+  walk.init(a, tpt, (int)sums[21], *reinterpret_cast<const Req*>(sums + 22), sums[20], begin, count);
   __syncthreads();  // the sums' place is used again
   Piece& p = walk.p;
 
@@ -250,13 +247,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     return __all_sync(0xffffffffu, mbar_wait_short(bar_addr, parity, wc));
   };
 
-  if (warp < 4) {
-  reg_dec<kRegCtl>();
   if (warp == 0) {
-    // -------------------------------------------------------------------- K
+    // -------------------------------------------------------------- K and Q
     // Lane l holds the page number of copy l of the pair (the next pair's are fetched
     // ahead); lane c * halves + half issues copy c of a tile, columns 64 * half.
-    if (lane == 0) tma_prefetch_desc(&tm_k);
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_q);
+    }
+    const int box_bytes = q_box * G * 128;
+    uint32_t rows = 0;
     const int P = a.cache.page_size;
     const int box = P < kT ? P : kT;  // rows of a copy
     const int ppt = kT / box;         // copies of a tile and 64 columns
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t seq[2] = {0, 0};
     bool ok = true;
     int ahead = walk.more ? page_of(walk.ahead) : -1;
-    while (ok && walk.next(a, tpt)) {
+    while (ok && walk.next(a, tpt, kDeep)) {
       const int now = ahead;
       if (walk.more) ahead = page_of(walk.ahead);
 #pragma unroll
@@ -291,71 +291,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_4d(base + C::kOffK + sl * C::kTileBytes + half * kBoxBytes + c * box * 128, &tm_k,
                       bar(C::kBarKFull + sl), half * 64, p.g, k0 % P, id);
       }
-    }
-    if (!ok) {
-      // Let the copies already issued land before the CTA exits.
-      for (int i = 0; i < 2; ++i)
-        for (uint32_t n = seq[i] > (uint32_t)C::kDepth ? seq[i] - C::kDepth : 0; n < seq[i]; ++n)
-          mbar_drain(bar(C::kBarKFull + i * C::kDepth + n % C::kDepth), (n / C::kDepth) & 1);
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------------ MMA
-    const bool leader = elect_one();
-    const uint64_t d_q = sdesc_sw128(base + C::kOffQ, 16, 1024);
-    uint32_t rows = 0, staged[2] = {0, 0}, used[2] = {0, 0};
-    bool ok = true;
-    while (ok && walk.next(a, tpt)) {
-      const int from[2] = {p.begins(0, tpt, chain), p.begins(1, tpt, chain)};
-      for (int s = p.s0; ok && s < p.s1; ++s) {
-        if (p.fresh) {
-          ok = wwait(bar(C::kBarQFull + rows % C::kRows), (rows / C::kRows) & 1);
-          if (!ok) break;
-          ++rows;
-        }
-        const uint32_t slot = (rows - 1) % C::kRows;
-        const int live = min(tpt, p.x.n - (p.q0t + s) * tpt) * G;
-        const uint32_t idesc = idesc_f16(kBf16, 128, 128, false, false) -
-                               ((uint32_t)((kT - (live + 31) / 32 * 32) >> 3) << 17);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (s < from[i]) continue;
-          if (s == from[i]) {
-            ok = ok && wwait(bar(C::kBarA + 2 * i + (staged[i] & 1)), (staged[i] >> 1) & 1);
-            ++staged[i];
-          }
-          ok = ok && wwait(bar(C::kBarSFree + i), (used[i] & 1) ^ 1);
-          if (!ok) break;
-          ++used[i];
-          tc_fence_after();
-          if (leader) {
-            const uint64_t b0 = sdesc_advance(d_q, slot * C::kTileBytes);
-            const uint32_t at = tmem + col_a(i, (staged[i] - 1) & 1);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              mma_ts(tmem + col_s(i), at + kk * 8,
-                     sdesc_advance(b0, (kk >> 2) * kBoxBytes + (kk & 3) * 32), idesc, kk > 0);
-            mma_commit(bar(C::kBarS + i));
-          }
-        }
-        if (ok && leader && (p.last || s + 1 < p.s1)) mma_commit(bar(C::kBarQEmpty + slot));
-      }
-    }
-    if (!ok) {
-      // Let every product already issued retire before TMEM is released.
-      if (leader) mma_commit(bar(C::kBarDrain));
-      mbar_drain(bar(C::kBarDrain), 0);
-    }
-  } else if (warp == 2) {
-    // -------------------------------------------------------------------- Q
-    // Boxes of q_box tokens and 64 columns, one a lane.  A box may reach into another
-    // request's rows; their columns are passed over.
-    if (lane == 0) tma_prefetch_desc(&tm_q);
-    const int box_bytes = q_box * G * 128;
-    uint32_t rows = 0;
-    bool ok = true;
-    while (ok && walk.next(a, tpt)) {
-      if (!p.fresh) continue;
-      for (int s = p.s0; s < p.s1; ++s) {
+      // The rows: boxes of q_box tokens and 64 columns, one a lane.  A box may reach into
+      // another request's rows; their columns are passed over.
+      for (int s = p.s0; ok && p.fresh && s < p.s1; ++s) {
         const int sl = rows % C::kRows;
         ok = wwait(bar(C::kBarQEmpty + sl), ((rows / C::kRows) & 1) ^ 1);
         if (!ok) break;
@@ -373,8 +311,68 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (!ok) {
+      // Let the copies already issued land before the CTA exits.
+      for (int i = 0; i < 2; ++i)
+        for (uint32_t n = seq[i] > (uint32_t)C::kDepth ? seq[i] - C::kDepth : 0; n < seq[i]; ++n)
+          mbar_drain(bar(C::kBarKFull + i * C::kDepth + n % C::kDepth), (n / C::kDepth) & 1);
       for (uint32_t n = rows > (uint32_t)C::kRows ? rows - C::kRows : 0; n < rows; ++n)
         mbar_drain(bar(C::kBarQFull + n % C::kRows), (n / C::kRows) & 1);
+    }
+  } else if (warp < 3) {
+    // ------------------------------------------------------------------ MMA
+    // A warp issues the products of a key tile.  (One warp for both took longer to issue
+    // them, two waits and eight instructions each, than the tensor cores to compute.)
+    const bool leader = elect_one();
+    const int i = warp - 1;
+    const uint64_t d_q = sdesc_sw128(base + C::kOffQ, 16, 1024);
+    const uint64_t d_k = sdesc_sw128(base + C::kOffK, 16, 1024);
+    uint32_t rows = 0, keys = 0, used = 0;
+    int group = C::kGroups - 1;  // rows stream: that takes this step
+    bool ok = true;
+    while (ok && walk.next(a, tpt, kDeep)) {
+      const int from = p.begins(i, tpt, chain), s1 = p.s1;
+      for (int s = p.s0; s < s1; ++s) {
+        rows += p.fresh;
+        group = group == C::kGroups - 1 ? 0 : group + 1;
+        const uint32_t slot = (rows - 1) % C::kRows;
+        ok = wwait(bar(C::kBarQFull + slot), ((rows - 1) / C::kRows) & 1);
+        if (ok && s >= from) {
+          if (s == from) {
+            ok = wwait(bar(C::kBarKFull + i * C::kDepth + keys % C::kDepth), (keys / C::kDepth) & 1);
+            ++keys;
+          }
+          const int sl = i * C::kDepth + (keys - 1) % C::kDepth, at = 2 * i + (used & 1);
+          ok = ok && wwait(bar(C::kBarSFree + at), (used >> 1 & 1) ^ 1);
+          ++used;
+          if (ok) {
+            tc_fence_after();
+            // All 128 columns, or the live ones to a multiple of 32.
+            const int live = min(tpt, p.x.n - (p.q0t + s) * tpt) * G;
+            const uint32_t idesc = idesc_f16(kBf16, 128, 128, false, false) -
+                                   ((uint32_t)((kT - (live + 31) / 32 * 32) >> 3) << 17);
+            if (leader) {
+              const uint64_t a0 = sdesc_advance(d_k, sl * C::kTileBytes);
+              const uint64_t b0 = sdesc_advance(d_q, slot * C::kTileBytes);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = (kk >> 2) * kBoxBytes + (kk & 3) * 32;
+                mma_ss(tmem + col_s(at), sdesc_advance(a0, off), sdesc_advance(b0, off), idesc, kk > 0);
+              }
+              // A barrier for each place and reader: so a reader sees all its phases, and none
+              // ends before the one before it has been seen.
+              mma_commit(bar(C::kBarS + 3 * at + (kDeep ? 0 : group)));
+              if (s + 1 == s1) mma_commit(bar(C::kBarKEmpty + sl));
+            }
+          }
+        }
+        if (!ok) break;
+        if (leader && (p.last || s + 1 < s1)) mma_commit(bar(C::kBarQEmpty + slot));
+      }
+    }
+    if (!ok) {
+      // Let every product already issued retire before TMEM is released.
+      if (leader) mma_commit(bar(C::kBarDrain + i));
+      mbar_drain(bar(C::kBarDrain + i), 0);
     }
   } else if (warp == 3) {
     // ---------------------------------------------------- notes and normalisers
@@ -393,17 +391,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       int q0, n, g, q0t, s, s1;
       bool fresh;
     } at = {}, then = {};  // the piece whose normalisers go out, and the next
+    // Lane l holds the page number of the l-th part of the pair, the next pair's ahead.
+    const int P = a.cache.page_size, box = P < kT ? P : kT, parts_of_pair = 2 * (kT / box);
+    auto page_of = [&](const Piece& u) {
+      const int pos = u.m * kPair + lane * box;
+      return lane < parts_of_pair && pos < u.x.total
+                 ? a.table[(int64_t)u.r * a.table_stride + pos / P]
+                 : -1;
+    };
+    int pages_ahead = walk.more ? page_of(walk.ahead) : -1;
     uint32_t noted = 0, rows = 0;
     bool ok = true, more = true;
     // Writes down the next piece, and keeps it in `then`.
     auto note = [&]() {
-      more = walk.next(a, tpt);
+      more = walk.next(a, tpt, kDeep);
       if (!more) return true;
+      const int page = pages_ahead;
+      if (walk.more) pages_ahead = page_of(walk.ahead);
       const int sl = noted % kNotes;
       if (!wwait(bar(C::kBarPEmpty + sl), ((noted / kNotes) & 1) ^ 1)) return false;
       ++noted;
+      Note& c = *reinterpret_cast<Note*>(smem + C::kOffNotes + sl * sizeof(Note));
+      if (lane < 16) c.page[lane] = page >= 0 && page < a.cache.num_pages ? page : -1;
       if (lane == 0) {
-        Note c;
         c.q0 = p.x.q0;
         c.n = p.x.n;
         c.ctx = p.x.ctx;
@@ -420,8 +430,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         c.last = p.last;
         c.fresh = p.fresh;
         c.whole = p.whole();
+        c.in_page[0] = p.m * kPair % P;
+        c.in_page[1] = (p.m * kPair + kT) % P;
         c.end_cta = c.whole || p.s0 > 0 ? -1 : cuts.of(p.item_at + kItemCost + p.steps - 1);
-        *reinterpret_cast<Note*>(smem + C::kOffNotes + sl * sizeof(Note)) = c;
       }
       mbar_arrive(bar(C::kBarPFull + sl));
       then = {p.x.q0, p.x.n, p.g, p.q0t, p.s0, p.s1, p.fresh};
@@ -459,8 +470,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           fetch(at);
         else if (more)
           fetch(then);
-        const int sl = rows % C::kRows;
-        ok = wwait(bar(C::kBarLEmpty + sl), ((rows / C::kRows) & 1) ^ 1);
+        const int sl = rows % C::kNorms;
+        ok = wwait(bar(C::kBarLEmpty + sl), ((rows / C::kNorms) & 1) ^ 1);
         if (!ok) break;
         ++rows;
         reinterpret_cast<float4*>(smem + C::kOffL + sl * kT * 4)[lane] = l;
@@ -468,177 +479,200 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       some = more;
     }
-  }
   } else {
-    reg_inc<kRegSum>();
     // -------------------------------------------------------------- the sums
-    const int ti = (warp - 4) >> 2;
+    // Deep: a warpgroup a key tile.  Else the warpgroups take the steps by turns, both key
+    // tiles of each, and add up their sums at the piece's end.
+    const int group = (warp - 4) >> 2;
     const int row = (warp & 3) * 32 + lane;  // TMEM lane, key of the tile
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const float sl2 = a.scale_log2;
-    const int P = a.cache.page_size, npages = (int)a.cache.num_pages;
-    uint32_t staged = 0, used = 0, rows = 0;
+    const int P = a.cache.page_size;
+    uint32_t rows = 0, used = 0, made1 = 0;  // made1: all products of key tile 1
+    uint32_t phases = 0;                     // of this warpgroup's barriers of the places
+    int behind = group;  // steps until this warpgroup's next
     bool ok = true;
     auto note_of = [&](uint32_t k) -> const Note& {
       return *reinterpret_cast<const Note*>(smem + C::kOffNotes + (k % kNotes) * sizeof(Note));
     };
-    // Moves this warpgroup's key tile of a piece from its ring to its place in TMEM.
-    auto stage = [&](const Note& u) {
-      if (u.begins[ti] == u.s1) return true;
-      const int sl = ti * C::kDepth + staged % C::kDepth;
-      if (!wwait(bar(C::kBarKFull + sl), (staged / C::kDepth) & 1)) return false;
-      const uint8_t* from = smem + C::kOffK + sl * C::kTileBytes + row * 128;
-      const uint32_t to = tl + col_a(ti, staged & 1);
-#pragma unroll
-      for (int half = 0; half < C::kHalves; ++half) {
+    // The weight that this thread stores (of key tile `group`), and what it holds so far.
+    auto weight_of = [&](const Note& u, float& old) -> float* {
+      if (group > 1) return nullptr;
+      const int pos = u.m * kPair + group * kT + row;
+      const int page = u.page[P < kT ? (group * kT + row) / P : group];
+      if (pos >= u.total || page < 0) return nullptr;
+      float* to = args.weights + ((int64_t)page * a.Hkv + u.g) * P +
+                  (P < kT ? row & (P - 1) : u.in_page[group] + row);
+      if (u.whole && pos < u.ctx) old = *to;
+      return to;
+    };
+    float t0, t1, t2, t3;
+    auto add = [&](float y0, float y1, float y2, float y3) {
+      t0 += y0;
+      t1 += y1;
+      t2 += y2;
+      t3 += y3;
+    };
+    // A key's row of products with the tile of rows at tok0, of which all (whole) or those
+    // that see the key count; frees the products' place.
+    auto row_sum = [&](uint32_t at, int free_bar, const float* nl, bool whole, int ahead_by, int tok0,
+                       int n, int q0) {
+      t0 = t1 = t2 = t3 = 0.f;
+      const int ntok = min(tpt, n - tok0), live = ntok * G;
+      const int first = chain && ahead_by > tok0 ? min(ahead_by - tok0, tpt) * G : 0;
+#pragma unroll 1
+      for (int c = 0; c < live; c += 32) {
         uint32_t r[32];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const uint4 v =
-              *reinterpret_cast<const uint4*>(from + half * kBoxBytes + ((c ^ (row & 7)) * 16));
-          r[4 * c] = v.x;
-          r[4 * c + 1] = v.y;
-          r[4 * c + 2] = v.z;
-          r[4 * c + 3] = v.w;
+        tmem_ld32(at + c, r);
+        const int hi = live - c, lo = first - c;
+        tmem_wait_ld_regs(r);
+        if (hi <= 32) {
+          tc_fence_before();
+          mbar_arrive(bar(free_bar));
         }
-        tmem_st32(to + half * 32, r);
+        float y[32];
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          const float4 l = *reinterpret_cast<const float4*>(nl + c + j);
+          y[j] = ex2(fmaf(__uint_as_float(r[j]), sl2, l.x));
+          y[j + 1] = ex2(fmaf(__uint_as_float(r[j + 1]), sl2, l.y));
+          y[j + 2] = ex2(fmaf(__uint_as_float(r[j + 2]), sl2, l.z));
+          y[j + 3] = ex2(fmaf(__uint_as_float(r[j + 3]), sl2, l.w));
+        }
+        if (!whole) {
+          // Which of the columns see this key: of the live ones those of the key's own token
+          // and later ones, or those whose word names it.
+          uint32_t seen = hi >= 32 ? 0xffffffffu : (1u << hi) - 1;
+          if (lo > 0) seen = lo >= 32 ? 0u : seen >> lo << lo;
+          if (!chain && ahead_by >= 0) {
+            uint32_t named = 0;
+            for (int t = c / G; t < ntok && t * G < c + 32; ++t) {
+              const unsigned long long word = a.tree[q0 + tok0 + t];
+              if (ahead_by < n && ahead_by < 64 && (word >> ahead_by & 1)) {
+                const int b = max(t * G - c, 0), e = min(t * G + G - c, 32);
+                named |= (e - b >= 32 ? 0xffffffffu : (1u << (e - b)) - 1) << b;
+              }
+            }
+            seen &= named;
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) y[j] = seen >> j & 1 ? y[j] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) add(y[j], y[j + 1], y[j + 2], y[j + 3]);
       }
-      mbar_arrive(bar(C::kBarKEmpty + sl));
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(bar(C::kBarA + 2 * ti + (staged & 1)));
-      ++staged;
-      return true;
+      return (t0 + t1) + (t2 + t3);
     };
-    auto page_of = [&](const Note& u) {
-      const int pos = u.m * kPair + ti * kT + row;
-      return pos < u.total ? a.table[(int64_t)u.r * a.table_stride + pos / P] : -1;
+    // total + x, with what the rounding leaves out in `lost`.
+    auto plus = [](float& total, float& lost, float x) {
+      const float term = x - lost, sum = total + term;
+      lost = fabsf(sum) < INFINITY ? __fadd_rn(__fadd_rn(sum, -total), -term) : 0.f;
+      total = sum;
     };
-    int page_ahead = -1;
     bool more = walk.more;
+    float old_ahead = 0.f;
+    float* to_ahead = nullptr;
     if (more) {
       ok = wwait(bar(C::kBarPFull), 0);
-      if (ok) {
-        page_ahead = page_of(note_of(0));
-        ok = stage(note_of(0));
-      }
+      if (ok) to_ahead = weight_of(note_of(0), old_ahead);
     }
     for (uint32_t k = 0; ok && more; ++k) {
       const Note& u = note_of(k);
-      const int page = page_ahead;
+      float* const to = to_ahead;
+      const float old = old_ahead;
       more = u.more;
       if (more) {
         ok = wwait(bar(C::kBarPFull + (k + 1) % kNotes), ((k + 1) / kNotes) & 1);
         if (!ok) break;
-        page_ahead = page_of(note_of(k + 1));
+        to_ahead = weight_of(note_of(k + 1), old_ahead);
       }
-      const int s1 = u.s1, from = u.begins[ti];
-      const bool fresh = u.fresh, last = u.last, whole = u.whole;
-      const int pos = u.m * kPair + ti * kT + row, ahead_by = pos - u.ctx;
-      float* to = nullptr;
-      if (pos < u.total && page >= 0 && page < npages)
-        to = args.weights + ((int64_t)page * a.Hkv + u.g) * P + pos % P;
-      float old = 0.f;
-      if (to && whole && ahead_by < 0) old = *to;
-      if (from == s1 && more) ok = stage(note_of(k + 1));
-      float total = 0.f, lost = 0.f;  // lost: what total's roundings left out
-      int tok0 = (u.q0t + u.s0) * tpt;
-#pragma unroll 1
-      for (int s = u.s0; ok && s < s1; ++s, tok0 += tpt) {
-        rows += fresh;
-        const uint32_t slot = (rows - 1) % C::kRows;
-        if (s < from) {
-          // Another key tile's step: its normalisers pass by.
-          ok = wwait(bar(C::kBarLFull + slot), ((rows - 1) / C::kRows) & 1);
+      const int s0 = u.s0, s1 = u.s1, n = u.n, q0 = u.q0, ctx = u.ctx, q0t = u.q0t;
+      const int from0 = u.begins[0], from1 = u.begins[1];
+      const int ahead_by = u.m * kPair + row - ctx;  // >= 0: the new token of key tile 0's position
+      const int edge = u.m * kPair + kT - 1 - ctx;   // of its last key
+      float total0 = 0.f, lost0 = 0.f, total1 = 0.f, lost1 = 0.f;
+      auto whole_at = [&](int edge, int tok0) {
+        return n - tok0 >= tpt && tpt * G == kT && edge <= (chain ? tok0 : -1);
+      };
+      if constexpr (kDeep) {
+        const bool last = u.last;
+        for (int s = s0; s < s1; ++s) {
+          rows += u.fresh;
+          const uint32_t slot = (rows - 1) % C::kNorms;
+          ok = wwait(bar(C::kBarLFull + slot), ((rows - 1) / C::kNorms) & 1);
           if (!ok) break;
-        } else {
-          // The next tile goes to its place while this one's last product runs.
-          if (s + 1 == s1 && more) ok = stage(note_of(k + 1));
-          ok = ok && wwait(bar(C::kBarLFull + slot), ((rows - 1) / C::kRows) & 1) &&
-               wwait(bar(C::kBarS + ti), used & 1);
-          if (!ok) break;
-          ++used;
-          tc_fence_after();
-          const int ntok = min(tpt, u.n - tok0), live = ntok * G;
-          const float* nl = reinterpret_cast<const float*>(smem + C::kOffL + slot * kT * 4);
-          uint32_t r[128];
-          tmem_ld32(tl + col_s(ti) + 0, r + 0);
-          tmem_ld32(tl + col_s(ti) + 32, r + 32);
-          tmem_ld32(tl + col_s(ti) + 64, r + 64);
-          tmem_ld32(tl + col_s(ti) + 96, r + 96);
-          tmem_wait_ld_regs(r);
-          reg_fence32(r + 32);
-          reg_fence32(r + 64);
-          reg_fence32(r + 96);
-          tc_fence_before();
-          mbar_arrive(bar(C::kBarSFree + ti));
-          float t0 = 0.f, t1 = 0.f, t2 = 0.f, t3 = 0.f;
-          // The tile's last key against the tile's first token.
-          const int edge = ahead_by - row + kT - 1;
-          if (live == kT && (chain ? edge <= tok0 : edge < 0)) {
-#pragma unroll
-            for (int j = 0; j < kT; j += 4) {
-              const float4 l = *reinterpret_cast<const float4*>(nl + j);
-              t0 += ex2(fmaf(__uint_as_float(r[j]), sl2, l.x));
-              t1 += ex2(fmaf(__uint_as_float(r[j + 1]), sl2, l.y));
-              t2 += ex2(fmaf(__uint_as_float(r[j + 2]), sl2, l.z));
-              t3 += ex2(fmaf(__uint_as_float(r[j + 3]), sl2, l.w));
-            }
-          } else {
-            // The columns that see this key, as a bit mask: of the live ones those of
-            // the key's own token and later ones, or those whose word names it.
-            typedef unsigned __int128 u128;
-            u128 v = live >= kT ? ~(u128)0 : (((u128)1 << live) - 1);
-            if (chain) {
-              const int first = ahead_by > tok0 ? min(ahead_by - tok0, tpt) * G : 0;
-              v = first >= kT ? 0 : v >> first << first;
-            } else if (ahead_by >= 0) {
-              v = 0;
-              for (int t = 0; t < ntok; ++t) {
-                const unsigned long long word = a.tree[u.q0 + tok0 + t];
-                const u128 cols = G >= kT ? ~(u128)0 : (((u128)1 << G) - 1);
-                if (ahead_by < u.n && ahead_by < 64 && (word >> ahead_by & 1)) v |= cols << (t * G);
-              }
-            }
-            const uint32_t vis[4] = {(uint32_t)v, (uint32_t)(v >> 32), (uint32_t)(v >> 64),
-                                     (uint32_t)(v >> 96)};
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              if (c * 32 >= live) break;
-#pragma unroll
-              for (int j = c * 32; j < c * 32 + 32; j += 4) {
-                const float4 l = *reinterpret_cast<const float4*>(nl + j);
-                const float y0 = ex2(fmaf(__uint_as_float(r[j]), sl2, l.x));
-                const float y1 = ex2(fmaf(__uint_as_float(r[j + 1]), sl2, l.y));
-                const float y2 = ex2(fmaf(__uint_as_float(r[j + 2]), sl2, l.z));
-                const float y3 = ex2(fmaf(__uint_as_float(r[j + 3]), sl2, l.w));
-                t0 += vis[c] >> (j & 31) & 1 ? y0 : 0.f;
-                t1 += vis[c] >> ((j & 31) + 1) & 1 ? y1 : 0.f;
-                t2 += vis[c] >> ((j & 31) + 2) & 1 ? y2 : 0.f;
-                t3 += vis[c] >> ((j & 31) + 3) & 1 ? y3 : 0.f;
-              }
-            }
+          if (s >= (group == 0 ? from0 : from1)) {
+            const int at = 2 * group + (used & 1), tok0 = (q0t + s) * tpt;
+            ok = wwait(bar(C::kBarS + 3 * at), used >> 1 & 1);
+            if (!ok) break;
+            ++used;
+            tc_fence_after();
+            plus(total0, lost0,
+                 row_sum(tl + col_s(at), C::kBarSFree + at,
+                         reinterpret_cast<const float*>(smem + C::kOffL + slot * kT * 4),
+                         whole_at(edge + group * kT, tok0), ahead_by + group * kT, tok0, n, q0));
           }
-          const float term = ((t0 + t1) + (t2 + t3)) - lost;
-          const float sum = total + term;
-          lost = fabsf(sum) < INFINITY ? __fadd_rn(__fadd_rn(sum, -total), -term) : 0.f;
-          total = sum;
+          if (last || s + 1 < s1) mbar_arrive(bar(C::kBarLEmpty + slot));
         }
-        if (last || s + 1 < s1) mbar_arrive(bar(C::kBarLEmpty + slot));
+      } else {
+        // Step s0 + behind is this warpgroup's, then each kGroups-th.
+        int s = s0 + behind;
+        for (; s < s1; s += C::kGroups) {
+          const uint32_t step = rows + (s - s0), slot = step % C::kNorms;
+          const int tok0 = (q0t + s) * tpt;
+          const float* nl = reinterpret_cast<const float*>(smem + C::kOffL + slot * kT * 4);
+          ok = wwait(bar(C::kBarLFull + slot), (step / C::kNorms) & 1);
+#pragma unroll 1
+          for (int i = 0; ok && i < (s >= from1 ? 2 : 1); ++i) {
+            const int at = 2 * i + ((i == 0 ? step : made1 + (uint32_t)(s - from1)) & 1);
+            ok = wwait(bar(C::kBarS + 3 * at + group), phases >> at & 1);
+            if (!ok) break;
+            phases ^= 1u << at;
+            tc_fence_after();
+            const float x = row_sum(tl + col_s(at), C::kBarSFree + at, nl, whole_at(edge + i * kT, tok0),
+                                    ahead_by + i * kT, tok0, n, q0);
+            plus(i == 0 ? total0 : total1, i == 0 ? lost0 : lost1, x);
+          }
+          if (!ok) break;
+          mbar_arrive(bar(C::kBarLEmpty + slot));
+        }
+        behind = s - s1;
+        made1 += s1 - from1;
+        rows += s1 - s0;
       }
       if (!ok) break;
-      if (whole) {
-        if (to) *to = ahead_by < 0 ? fmaf(args.decay, old, total) : total;
-      } else {
-        const int which = u.s0 == 0 ? 1 : 0;
-        out.sums[((int64_t)cta * 2 + which) * kPair + ti * kT + row] = total;
-        if (which == 1 && ti == 0 && row == 0) {
-          Cut c;
-          c.last = u.end_cta;
-          c.r = u.r;
-          c.g = u.g;
-          c.m = u.m;
-          out.cuts[cta] = c;
+      float total = total0;
+      if constexpr (!kDeep) {
+        // Two places by turns: the sums of the piece before the last have been read.
+        float* x = reinterpret_cast<float*>(smem + C::kOffX) + (k & 1) * C::kGroups * kPair + row;
+        ok = wwait(bar(C::kBarXEmpty + (k & 1)), (k >> 1 & 1) ^ 1);
+        if (!ok) break;
+        x[group * kPair] = total0;
+        x[group * kPair + kT] = total1;
+        mbar_arrive(bar(C::kBarXFull + (k & 1)));
+        if (group < 2) {
+          ok = wwait(bar(C::kBarXFull + (k & 1)), k >> 1 & 1);
+          if (!ok) break;
+          total = 0.f;
+#pragma unroll
+          for (int w = 0; w < C::kGroups; ++w) total += x[w * kPair + group * kT];
+          mbar_arrive(bar(C::kBarXEmpty + (k & 1)));
+        }
+      }
+      if (group < 2) {
+        if (u.whole) {
+          if (to) *to = ahead_by + group * kT < 0 ? fmaf(args.decay, old, total) : total;
+        } else {
+          const int which = u.s0 == 0 ? 1 : 0;
+          out.sums[((int64_t)cta * 2 + which) * kPair + group * kT + row] = total;
+          if (which == 1 && group == 0 && row == 0) {
+            Cut c;
+            c.last = u.end_cta;
+            c.r = u.r;
+            c.g = u.g;
+            c.m = u.m;
+            out.cuts[cta] = c;
+          }
         }
       }
       mbar_arrive(bar(C::kBarPEmpty + k % kNotes));
@@ -701,7 +735,7 @@ cudaError_t run(const WeightsArgs& w, int dev, int sms, cudaStream_t stream) {
   out.cuts = reinterpret_cast<Cut*>(ws);
   out.sums = reinterpret_cast<float*>(ws + align256(kMaxCtas * sizeof(Cut)));
   const int grid = sms < kMaxCtas ? sms : kMaxCtas;
-  weights_kernel<kBf16, D, kDeep><<<grid, kThreads, smem, stream>>>(mq, mk, w, out, box);
+  weights_kernel<kBf16, D, kDeep><<<grid, Cfg<D, kDeep>::kThreads, smem, stream>>>(mq, mk, w, out, box);
   e = cudaGetLastError();
   // No request has more than one tile of rows: no item has two steps, none is cut.
   if (e != cudaSuccess || a.N <= kT / G) return e;

@@ -186,13 +186,14 @@ struct Walk {
       }
     }
   }
-  __host__ __device__ inline bool next(const TreeArgs& a, int tpt) {
+  // keep: a tile of tokens that is its request's only one serves the next piece too.
+  __host__ __device__ inline bool next(const TreeArgs& a, int tpt, bool keep) {
     if (!more) return false;
     const bool fresh = p.last;
     p = ahead;
     p.fresh = fresh;
     advance(a, tpt);
-    p.last = !(more && ahead.r == p.r && ahead.g == p.g && tiles_of(p.x, tpt) == 1);
+    p.last = !(keep && more && ahead.r == p.r && ahead.g == p.g && tiles_of(p.x, tpt) == 1);
     return true;
   }
 };

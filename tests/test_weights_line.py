@@ -49,7 +49,7 @@ int one(std::mt19937& rng) {
   a.width = 1000;
   a.cache.page_size = 16;
   a.tree = pick(0, 2) ? nullptr : &word;
-  const bool chain = a.tree == nullptr;
+  const bool chain = a.tree == nullptr, keep = pick(0, 1);
   std::vector<Req> req(R);
   std::vector<long long> before(R + 1, 0);
   std::map<std::tuple<int, int, int>, std::pair<int, int>> items;  // first tile and steps
@@ -86,7 +86,7 @@ int one(std::mt19937& rng) {
     w.init(a, tpt, r, req[r], begin - before[r], begin, count);
     bool first = true, open = false, kept = false;
     int pr = -1, pg = -1, pt = -1;
-    while (w.next(a, tpt)) {
+    while (w.next(a, tpt, keep)) {
       const Piece& p = w.p;
       const std::tuple<int, int, int> item{p.r, p.g, p.m};
       CHECK(!open);  // a piece that goes on is the CTA's last
@@ -98,6 +98,7 @@ int one(std::mt19937& rng) {
       CHECK(p.fresh == !kept);
       if (kept) CHECK(p.r == pr && p.g == pg && p.q0t == pt && p.s1 - p.s0 == 1 && p.q0t == 0);
       kept = !p.last;
+      CHECK(keep || !kept);
       if (kept) CHECK(w.more);
       pr = p.r, pg = p.g, pt = p.q0t + p.s1 - 1;
       for (int i = 0; i < 2; ++i) {
@@ -154,7 +155,7 @@ def test_pieces_cover_every_step_once(tmp_path):
 
 PIECES = [(1, 0, 0, True), (1, 0, 0, False), (1, 0, 1, True), (2, 0, 0, False), (4, 0, 2, False), (5, 0, 5, False),
           (3, 0, 1, False), (2, 0, 2, False)]
-RINGS = [dict(depth=1, rows=4), dict(depth=2, rows=2), dict(depth=2, rows=8), dict(depth=4, rows=4)]
+RINGS = [dict(), dict(rows=8), dict(deep=True), dict(depth=4, rows=4, deep=True)]
 
 
 def draws(n, seed):
@@ -164,15 +165,15 @@ def draws(n, seed):
 
 @pytest.mark.parametrize("ring", RINGS)
 def test_protocol_holds_under_random_schedules(ring):
-    for seed, work in enumerate(draws(300, 5)):
+    for seed, work in enumerate(draws(1500, 5)):
         weights_kernel.run(work, seed, **ring)
 
 
-@pytest.mark.parametrize("mutation", [1, 2, 3, 4, 5, 6, 7, 8, 9])
-def test_planted_protocol_mistake_is_caught(mutation):
+@pytest.mark.parametrize("deep,mutation", [(False, m) for m in (1, 2, 3, 6, 7, 8, 9, 10, 11, 12, 13)] + [(True, m) for m in (1, 2, 3, 4, 5, 6, 7, 8, 9, 11)])
+def test_planted_protocol_mistake_is_caught(deep, mutation):
     for seed, work in enumerate(draws(2000, 7)):
         try:
-            weights_kernel.run(work, seed, mutation=mutation, depth=1, rows=2)
+            weights_kernel.run(work, seed, mutation=mutation, depth=1 + seed % 2, deep=deep)
         except AssertionError:
             return
     pytest.fail(f"mutation {mutation} survived 2000 schedules")
