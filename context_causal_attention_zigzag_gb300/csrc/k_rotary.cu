@@ -16,14 +16,21 @@
 //
 // Both calls are bound by HBM: each value is read and written once, in 16-byte
 // vectors where rot allows it.  A thread holds the same vectors of each head (both
-// partners of their pairs), so its sines and cosines serve all heads of a token.
+// partners of their pairs), so its sines and cosines serve several heads of a token.
+// Measured: 131072 tokens of 32 heads of 128 into the ring's order in bfloat16 316 us
+// (6.8 TB/s, the copy rate), 2 x 16384 in float32 out of it 163 us (6.6 TB/s); 32001
+// tokens of 32 + 8 + 8 heads into the cache 126 us (6.2 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+#include <string.h>
+
+#include <type_traits>
 
 #include "cpattn.h"
 #include "cpattn_internal.h"
+#include "tc_ptx.cuh"
 
 namespace cpattn {
 namespace {
@@ -36,6 +43,12 @@ int sm_count() {
 }
 
 constexpr int kThreads = 256;
+// Blocks an SM (registers allow what is in flight): 131072 tokens of 32 heads of 128 in
+// bfloat16 take 437 us with 2, 316 with 3, 551 with 4 (which spills).
+constexpr int kResident = 3;
+// Threads an SM from which on a thread takes more heads (and fewer sines).
+constexpr int kEnough = 2048;
+constexpr int kMostPairs = 128;  // of a head (D at most 256)
 
 // kVec values as they lie in memory.
 template <int kBytes>
@@ -57,30 +70,43 @@ struct Raw<2> {
   typedef uint16_t type;
 };
 
+// Two 16-bit values as they lie in a word.
 template <typename T>
-__device__ __forceinline__ float to_float(T x) {
-  return static_cast<float>(x);
+__device__ __forceinline__ float2 unpack(uint32_t w);
+template <>
+__device__ __forceinline__ float2 unpack<__nv_bfloat16>(uint32_t w) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+}
+template <>
+__device__ __forceinline__ float2 unpack<__half>(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 template <typename T>
-__device__ __forceinline__ T from_float(float x);
-template <>
-__device__ __forceinline__ float from_float<float>(float x) {
-  return x;
-}
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) {
-  return __float2bfloat16_rn(x);
-}
-template <>
-__device__ __forceinline__ __half from_float<__half>(float x) {
-  return __float2half_rn(x);
+__device__ __forceinline__ uint32_t pack(float x, float y) {
+  return tc::pack16<std::is_same<T, __nv_bfloat16>::value>(x, y);
 }
 
+// kVec values as 32-bit words.
 template <typename T, int kVec>
-union Values {
-  typename Raw<sizeof(T) * kVec>::type raw;
-  T v[kVec];
-  __device__ __forceinline__ Values() {}
+struct Values {
+  static constexpr int kBytes = sizeof(T) * kVec, kWords = kBytes < 4 ? 1 : kBytes / 4;
+  typedef typename Raw<kBytes>::type Raw_;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void read(const T* p) {
+    const Raw_ r = *reinterpret_cast<const Raw_*>(p);
+    if constexpr (kBytes == 2)
+      w[0] = r;
+    else
+      memcpy(w, &r, kBytes);
+  }
+  __device__ __forceinline__ void write(T* p) const {
+    Raw_ r;
+    if constexpr (kBytes == 2)
+      r = (uint16_t)w[0];
+    else
+      memcpy(&r, w, kBytes);
+    *reinterpret_cast<Raw_*>(p) = r;
+  }
 };
 
 // Fraction of a turn a position, in units of 2^-64.
@@ -115,8 +141,8 @@ template <typename T, int kVec, bool kInterleaved>
 struct Turn {
   static constexpr int kPairs = kInterleaved ? kVec / 2 : kVec;
   static constexpr int kVecs = kInterleaved ? 1 : 2;
-  unsigned long long f[kPairs];
   float c[kPairs], s[kPairs];
+  const unsigned long long* f;  // of its first pair, in shared memory
   int at, half;
   bool turns_;
 
@@ -124,15 +150,16 @@ struct Turn {
   __host__ __device__ static int turning(int rot) { return rot / (kVec * kVecs); }
   __host__ __device__ static int units(int D, int rot) { return turning(rot) + (D - rot) / kVec; }
 
-  __device__ __forceinline__ void init(int unit, int rot, const double* freqs) {
+  // table: rot / 2 values, filled by the block.
+  __device__ __forceinline__ void init(int unit, int rot, const double* freqs,
+                                       unsigned long long* table) {
+    for (int i = threadIdx.x; i < rot / 2; i += kThreads) table[i] = turns(freqs[i]);
+    __syncthreads();
     const int n = turning(rot);
     turns_ = unit < n;
     half = rot / 2;
     at = turns_ ? unit * kVec : rot + (unit - n) * kVec;
-    if (turns_) {
-#pragma unroll
-      for (int i = 0; i < kPairs; ++i) f[i] = turns(freqs[unit * kPairs + i]);
-    }
+    f = table + unit * kPairs;
   }
   __device__ __forceinline__ void angles(long long position, float magnitude, float sign) {
     if (!turns_) return;
@@ -144,24 +171,64 @@ struct Turn {
     }
   }
   __device__ __forceinline__ void load(const T* x, Values<T, kVec> (&v)[kVecs]) const {
-    v[0].raw = *reinterpret_cast<const decltype(v[0].raw)*>(x + at);
-    if (kVecs == 2 && turns_)
-      v[kVecs - 1].raw = *reinterpret_cast<const decltype(v[0].raw)*>(x + at + half);
+    v[0].read(x + at);
+    if (kVecs == 2 && turns_) v[kVecs - 1].read(x + at + half);
+  }
+  __device__ __forceinline__ void pair(int i, float& x, float& y) const {
+    const float u = x;
+    x = u * c[i] - y * s[i];
+    y = u * s[i] + y * c[i];
   }
   __device__ __forceinline__ void turn(Values<T, kVec> (&v)[kVecs]) const {
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < kPairs; ++i) {
-      T& a = kInterleaved ? v[0].v[2 * i] : v[0].v[i];
-      T& b = kInterleaved ? v[0].v[2 * i + 1] : v[kVecs - 1].v[i];
-      const float x = to_float(a), y = to_float(b);
-      a = from_float<T>(x * c[i] - y * s[i]);
-      b = from_float<T>(x * s[i] + y * c[i]);
+      for (int i = 0; i < kPairs; ++i) {
+        uint32_t& a = kInterleaved ? v[0].w[2 * i] : v[0].w[i];
+        uint32_t& b = kInterleaved ? v[0].w[2 * i + 1] : v[kVecs - 1].w[i];
+        float x = __uint_as_float(a), y = __uint_as_float(b);
+        pair(i, x, y);
+        a = __float_as_uint(x);
+        b = __float_as_uint(y);
+      }
+    } else if constexpr (kInterleaved) {
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        float2 x = unpack<T>(v[0].w[i]);
+        pair(i, x.x, x.y);
+        v[0].w[i] = pack<T>(x.x, x.y);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < Values<T, kVec>::kWords; ++i) {
+        float2 x = unpack<T>(v[0].w[i]), y = unpack<T>(v[kVecs - 1].w[i]);
+        pair(kVec > 1 ? 2 * i : 0, x.x, y.x);
+        if (kVec > 1) pair(kVec > 1 ? 2 * i + 1 : 0, x.y, y.y);
+        v[0].w[i] = pack<T>(x.x, x.y);
+        v[kVecs - 1].w[i] = pack<T>(y.x, y.y);
+      }
+    }
+  }
+  // n heads from `from` to `to`, turned or as they are; all loads of four before their stores.
+  template <typename Step>
+  __device__ __forceinline__ void move(const T* from, Step from_step, T* to, Step to_step, int n,
+                                       bool turned) const {
+    constexpr int U = 4;
+    for (int h = 0; h < n; h += U) {
+      Values<T, kVec> v[U][kVecs];
+#pragma unroll
+      for (int j = 0; j < U; ++j)
+        if (h + j < n) load(from + (h + j) * from_step, v[j]);
+#pragma unroll
+      for (int j = 0; j < U; ++j)
+        if (h + j < n) {
+          if (turned) turn(v[j]);
+          store(to + (h + j) * to_step, v[j]);
+        }
     }
   }
   __device__ __forceinline__ void store(T* x, const Values<T, kVec> (&v)[kVecs]) const {
-    *reinterpret_cast<decltype(v[0].raw)*>(x + at) = v[0].raw;
-    if (kVecs == 2 && turns_)
-      *reinterpret_cast<decltype(v[0].raw)*>(x + at + half) = v[kVecs - 1].raw;
+    v[0].write(x + at);
+    if (kVecs == 2 && turns_) v[kVecs - 1].write(x + at + half);
   }
 };
 
@@ -171,18 +238,18 @@ struct Turn {
 // out's tokens.  In place nothing is copied (units of a head: `units`).
 // ---------------------------------------------------------------------------
 template <typename T, int kVec, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, int units, int groups,
+__global__ void __launch_bounds__(kThreads, kResident) rotary_kernel(const RotaryArgs a, int units, int groups,
                                                           int per_group) {
   typedef Turn<T, kVec, kInterleaved> Unit;
-  constexpr int U = 4;
   // The unit and the group are the same in each step: the stride is a multiple of
   // units * groups threads.
   const int per_token = units * groups;
   const int tokens = kThreads / per_token;  // of a step of the block
   const int lane = threadIdx.x % per_token;
-  if ((int)threadIdx.x >= tokens * per_token) return;
+  __shared__ unsigned long long table[kMostPairs];
   Unit u;
-  u.init(lane % units, a.rot, a.freqs);
+  u.init(lane % units, a.rot, a.freqs, table);
+  if ((int)threadIdx.x >= tokens * per_token) return;
   const int h0 = lane / units * per_group, h1 = min(a.H, h0 + per_group);
   const long long total = (long long)a.B * a.S_out;
   for (long long i = (long long)blockIdx.x * tokens + threadIdx.x / per_token; i < total;
@@ -191,11 +258,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, in
     const int n = a.to_sharded ? natural_pos(a.ring, p) : p;
     T* out = static_cast<T*>(a.out) + i * a.out_stride;
     if (n >= a.S_nat) {  // padding
-      Values<T, kVec> zero[Unit::kVecs];
-#pragma unroll
-      for (int j = 0; j < kVec; ++j)
-#pragma unroll
-        for (int e = 0; e < Unit::kVecs; ++e) zero[e].v[j] = from_float<T>(0.f);
+      Values<T, kVec> zero[Unit::kVecs] = {};
       for (int h = h0; h < h1; ++h) u.store(out + h * a.D, zero);
       continue;
     }
@@ -203,18 +266,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, in
     const T* x = static_cast<const T*>(a.x) + from * a.x_stride;
     u.angles(a.positions ? a.positions[b * a.positions_stride + n] : a.offset + n, a.magnitude,
              a.sign);
-    for (int h = h0; h < h1; h += U) {
-      Values<T, kVec> v[U][Unit::kVecs];
-#pragma unroll
-      for (int j = 0; j < U; ++j)
-        if (h + j < h1) u.load(x + (h + j) * a.D, v[j]);
-#pragma unroll
-      for (int j = 0; j < U; ++j)
-        if (h + j < h1) {
-          if (u.turns_) u.turn(v[j]);
-          u.store(out + (h + j) * a.D, v[j]);
-        }
-    }
+    u.move(x + h0 * a.D, a.D, out + h0 * a.D, a.D, h1 - h0, u.turns_);
   }
 }
 
@@ -225,7 +277,7 @@ cudaError_t run(const RotaryArgs& a, cudaStream_t stream) {
   const int units = in_place ? Unit::turning(a.rot) : Unit::units(a.D, a.rot);
   // All heads a thread where that leaves threads enough for the SMs.
   const long long total = (long long)a.B * a.S_out;
-  const long long full = (long long)sm_count() * 1024;
+  const long long full = (long long)sm_count() * kEnough;
   int per_group = a.H;
   while (per_group > 1 &&
          total * units * ((a.H + per_group - 1) / per_group) < full &&
@@ -242,67 +294,69 @@ cudaError_t run(const RotaryArgs& a, cudaStream_t stream) {
 }
 
 // ---------------------------------------------------------------------------
-// A step's tokens: "heads" 0 .. H - 1 are q's, then k's, then v's.
+// A step's tokens.  A thread holds the same vectors of `per_group` heads of q, of k or
+// of v: consecutive threads take the units, then the groups, then the next tokens.
 // ---------------------------------------------------------------------------
+constexpr int kWriteThreads = 384;  // three groups of the narrowest units (127) at least
+// Heads a thread has in flight: 32001 tokens of 32 + 8 + 8 heads of 128 take 175 us with 1,
+// 126 with 2, 152 with 4 (which spills); with two blocks an SM that step through the tokens.
+// 142 with sixteen times as many (each makes the table of frequencies).
+constexpr int kMostHeads = 2;
+
 template <typename T, int kVec, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) rotary_write_kernel(const RotaryWriteArgs a, int units,
-                                                                int groups, int per_group) {
+__global__ void __launch_bounds__(kWriteThreads, 2)
+    rotary_write_kernel(const RotaryWriteArgs a, int units, int q_groups, int groups, int per_group) {
   typedef Turn<T, kVec, kInterleaved> Unit;
-  constexpr int U = 4;
   const int per_token = units * groups;
-  const int tokens = kThreads / per_token;
+  const int tokens = kWriteThreads / per_token;
   const int lane = threadIdx.x % per_token;
-  if ((int)threadIdx.x >= tokens * per_token) return;
+  __shared__ unsigned long long table[kMostPairs];
   Unit u;
-  u.init(lane % units, a.rot, a.freqs);
-  const int all = a.H + 2 * a.Hkv;
-  const int h0 = lane / units * per_group, h1 = min(all, h0 + per_group);
+  u.init(lane % units, a.rot, a.freqs, table);
+  if ((int)threadIdx.x >= tokens * per_token) return;
+  int group = lane / units, kind = 0;  // 0: q, 1: k, 2: v
+  if (group >= q_groups) {
+    const int kv_groups = (groups - q_groups) / 2;
+    group -= q_groups;
+    kind = group < kv_groups ? 1 : 2;
+    if (kind == 2) group -= kv_groups;
+  }
+  const int heads = kind == 0 ? a.H : a.Hkv, h0 = group * per_group, n = min(per_group, heads - h0);
+  const T* x = static_cast<const T*>(kind == 0 ? a.q : (kind == 1 ? a.k : a.v)) + h0 * a.D;
+  const int64_t x_stride = kind == 0 ? a.q_stride : (kind == 1 ? a.k_stride : a.v_stride);
+  const int64_t step = kind == 0 ? a.D : a.cache.head_stride;
+  T* to = static_cast<T*>(kind == 0 ? a.out : (kind == 1 ? a.k_cache : a.v_cache)) + h0 * step;
+  // In place nothing is copied.
+  const bool turned = u.turns_ && kind < 2, idle = kind == 0 && !u.turns_ && a.q == a.out;
   const long long places = a.cache.num_pages * a.cache.page_size;
   for (long long i = (long long)blockIdx.x * tokens + threadIdx.x / per_token; i < a.N;
        i += (long long)gridDim.x * tokens) {
-    long long slot = a.slots[i];
-    if (slot >= places) {
-      if (lane == 0) atomicExch(a.err, kErrBadTables);
-      slot = -1;
+    if (idle) continue;
+    const T* from = x + i * x_stride;
+    const long long slot = kind != 0 ? a.slots[i] : 0;
+    if (turned) u.angles(a.positions[i], a.magnitude, 1.f);
+    T* row = to + i * a.out_stride;
+    if (kind != 0) {
+      if (slot >= places && kind == 1 && h0 == 0 && lane % units == 0)
+        atomicExch(a.err, kErrBadTables);
+      if (slot < 0 || slot >= places) continue;
+      const int page = (int)slot / a.cache.page_size;
+      row = to + page * a.cache.page_stride +
+            ((int)slot - page * a.cache.page_size) * a.cache.token_stride;
     }
-    const int page = slot < 0 ? 0 : (int)slot / a.cache.page_size;
-    const int64_t row = page * a.cache.page_stride +
-                        (slot < 0 ? 0 : (int)slot - page * a.cache.page_size) * a.cache.token_stride;
-    const T* q = static_cast<const T*>(a.q) + i * a.q_stride;
-    const T* k = static_cast<const T*>(a.k) + i * a.k_stride;
-    const T* v = static_cast<const T*>(a.v) + i * a.v_stride;
-    T* out = static_cast<T*>(a.out) + i * a.out_stride;
-    T* kc = static_cast<T*>(a.k_cache) + row;
-    T* vc = static_cast<T*>(a.v_cache) + row;
-    u.angles(a.positions[i], a.magnitude, 1.f);
-    const bool in_place = a.q == a.out;
-    for (int h = h0; h < h1; h += U) {
-      Values<T, kVec> w[U][Unit::kVecs];
-      T* to[U];
+    for (int h = 0; h < n; h += kMostHeads) {
+      Values<T, kVec> v[kMostHeads][Unit::kVecs];
 #pragma unroll
-      for (int j = 0; j < U; ++j) {
-        to[j] = nullptr;
-        int g = h + j;
-        if (g >= h1) continue;
-        const T* from;
-        if (g < a.H) {
-          from = q + g * a.D;
-          if (u.turns_ || !in_place) to[j] = out + g * a.D;
-        } else {
-          g -= a.H;
-          const bool key = g < a.Hkv;
-          if (!key) g -= a.Hkv;
-          from = (key ? k : v) + g * a.D;
-          if (slot >= 0) to[j] = (key ? kc : vc) + g * a.cache.head_stride;
+      for (int j = 0; j < kMostHeads; ++j)
+        if (h + j < n) u.load(from + (h + j) * a.D, v[j]);
+#pragma unroll
+      for (int j = 0; j < kMostHeads; ++j) {
+        if (h + j < n) {
+          if (turned) u.turn(v[j]);
+          u.store(row, v[j]);
         }
-        if (to[j]) u.load(from, w[j]);
+        row += step;
       }
-#pragma unroll
-      for (int j = 0; j < U; ++j)
-        if (to[j]) {
-          if (u.turns_ && h + j < a.H + a.Hkv) u.turn(w[j]);
-          u.store(to[j], w[j]);
-        }
     }
   }
 }
@@ -310,20 +364,25 @@ __global__ void __launch_bounds__(kThreads) rotary_write_kernel(const RotaryWrit
 template <typename T, int kVec, bool kInterleaved>
 cudaError_t run(const RotaryWriteArgs& a, cudaStream_t stream) {
   typedef Turn<T, kVec, kInterleaved> Unit;
-  const int units = Unit::units(a.D, a.rot), all = a.H + 2 * a.Hkv;
-  const long long full = (long long)sm_count() * 1024;
-  int per_group = all;
-  while (per_group > 1 &&
-         a.N * units * ((all + per_group - 1) / per_group) < full &&
-         units * ((all + (per_group + 1) / 2 - 1) / ((per_group + 1) / 2)) <= kThreads)
-    per_group = (per_group + 1) / 2;
-  const int groups = (all + per_group - 1) / per_group;
-  const int tokens = kThreads / (units * groups);
+  const int units = Unit::units(a.D, a.rot);
+  // Few heads a thread where there are few tokens; more where a token needs more threads
+  // than a block has.
+  const long long full = (long long)sm_count() * kEnough;
+  int per_group = 1, q_groups, groups;
+  while (true) {
+    q_groups = (a.H + per_group - 1) / per_group;
+    groups = q_groups + 2 * ((a.Hkv + per_group - 1) / per_group);
+    if (units * groups <= kWriteThreads &&
+        (per_group >= kMostHeads || a.N * units * groups <= full))
+      break;
+    per_group *= 2;
+  }
+  const int tokens = kWriteThreads / (units * groups);
   long long grid = (a.N + tokens - 1) / tokens;
-  const long long cap = (long long)sm_count() * 16;
+  const long long cap = (long long)sm_count() * 2;
   if (grid > cap) grid = cap;
-  rotary_write_kernel<T, kVec, kInterleaved><<<(unsigned)grid, kThreads, 0, stream>>>(
-      a, units, groups, per_group);
+  rotary_write_kernel<T, kVec, kInterleaved><<<(unsigned)grid, kWriteThreads, 0, stream>>>(
+      a, units, q_groups, groups, per_group);
   return cudaGetLastError();
 }
 
