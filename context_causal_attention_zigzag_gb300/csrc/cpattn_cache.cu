@@ -239,7 +239,7 @@ int cpattn_cache_weights(const void* q, int64_t q_stride, const void* k_cache, i
 namespace {
 // Shapes that the workspace can be asked for.
 bool evict_shape_ok(int R, int Hkv, int width, int P, int most) {
-  return R >= 0 && R <= 65535 && Hkv >= 1 && Hkv <= 65535 && (int64_t)R * Hkv <= (1 << 27) &&
+  return R >= 0 && R <= 65535 && Hkv >= 1 && Hkv <= 65535 && (int64_t)R * Hkv <= (1 << 24) &&
          width >= 0 && page_size_ok(P) && width <= kMostPositions / P && most >= 1 &&
          most <= kMostPositions && (int64_t)R * Hkv * most < ((int64_t)1 << 40);
 }
@@ -253,7 +253,8 @@ int64_t evict_list(int width, int P, int most) {
 size_t cpattn_cache_evict_workspace_bytes(int R, int Hkv, int table_width, int page_size,
                                           int most) {
   if (!evict_shape_ok(R, Hkv, table_width, page_size, most)) return 0;
-  return (size_t)R * Hkv * 2 * evict_list(table_width, page_size, most) * sizeof(int);
+  const size_t items = (size_t)R * Hkv;
+  return (items + items * 2 * evict_list(table_width, page_size, most)) * sizeof(int);
 }
 
 int cpattn_cache_evict(float* weights, const float* scores, void* k_cache, void* v_cache,
@@ -313,7 +314,9 @@ int cpattn_cache_evict(float* weights, const float* scores, void* k_cache, void*
   a.R = R;
   a.Hkv = Hkv;
   a.D = D;
-  a.lists = static_cast<int*>(workspace);
+  a.fills = static_cast<int*>(workspace);
+  a.lists = a.fills + (int64_t)R * Hkv;
+  a.item0 = 0;
   a.list_cap = evict_list(table_width, page_size, most);
   a.err = err;
   return status(launch_cache_evict(a, (cudaStream_t)stream));

@@ -546,8 +546,10 @@ struct EvictArgs {
   int num_freed_max;
   int* num_freed;
   int R, Hkv, D;
-  int* lists;  // [R, Hkv, 2, list_cap]: places to fill, and what fills them
+  int* fills;  // [R, Hkv]: how many places are filled, -1 where nothing moves
+  int* lists;  // [R, Hkv, 2, list_cap]: those places, and what fills them
   int64_t list_cap;
+  int item0;   // first of the (request, head) of a launch
   int* err;
 };
 cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t stream);

@@ -1,28 +1,30 @@
 // Eviction: each request and kv head keeps the heaviest positions of its cache,
-// which move as little as possible.
+// which move as little as possible.  With f, t, cut and keep of the call, M = c - t - f
+// positions lie between the first and the last ones and m = cut - f of them stay.
 //
-// A cluster of CTAs takes one kv head of one request.  With f, t, cut and keep of
-// the call, M = c - t - f positions lie between the first and the last ones and m
-// = cut - f of them stay:
+// evict_select_kernel, a CTA (long tables: a cluster of them) for each head of a request:
 //  1. Each CTA takes a run of those positions, and turns their scores into
 //     integers of the same order in shared memory (read again where a run is too
 //     long for it).
 //  2. The m-th largest is found digit by digit (11, 11 and 10 bits): each CTA
-//     counts the digits of its run that begin as the ones found so far, and all of
-//     them add up the cluster's counts through distributed shared memory and take
-//     the digit in which the m-th lies.  Counts are integers: nothing depends on
-//     the order of additions.
+//     counts the digits of its run that begin as the ones found so far; the first
+//     one adds the counts up (through distributed shared memory) and finds the digit in
+//     which the m-th lies.  Counts are integers: no order of additions matters.
 //  3. What is above it stays, and of its equals as many as are left, from the
 //     lowest position on.  Counts of a thread's positions, summed over the CTA and
 //     the cluster, number the places below the cut that become free and the
 //     positions behind it that stay; both go into lists, so that the n-th place is
 //     filled by the n-th position.
-//  4. The pairs of the lists are copied, a warp a pair (key and value at once);
-//     sources lie behind the cut and destinations before it, so no order matters.
-//  5. The last t move to the cut, a wave at a time: all CTAs read the wave into
-//     registers, meet, and write it.
-// Bound by HBM for long caches (scores once, moved rows once in and out); for short
-// ones by its chain of meetings.
+// evict_fill_kernel copies the pairs of the lists: a lane looks up a pair's pages and moves
+// its weight, then the warp copies the pairs' rows, key and value at once.  Sources lie
+// behind the cut and destinations before it, so no order matters.
+// evict_shift_kernel moves the last t to the cut, over what the fills have read by then:
+// a CTA takes 64 bytes of each row, a wave of rows at a time, read whole before any is
+// written (the last ones may move within themselves).  It also lists the pages that
+// became free.
+//
+// Bound by HBM for many positions (scores once, moved rows once in and out), by the
+// chain of its steps for few.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <limits.h>
@@ -30,13 +32,14 @@
 
 #include "cpattn.h"
 #include "cpattn_internal.h"
+#include "tc_ptx.cuh"
 
 namespace cg = cooperative_groups;
 
 namespace cpattn {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kRun = 16384;  // scores of a CTA's run in shared memory
@@ -44,8 +47,9 @@ constexpr int kMaxCluster = 8;
 
 struct Shared {
   uint32_t run[kRun];
-  int count[2][kBins];  // of the digits, by turns
-  int meet[4];          // this CTA's counts, read by the others
+  int count[kBins];  // of the digits
+  int total[kBins];  // the cluster's, in its first CTA
+  int meet[4];       // this CTA's counts, read by the others
   int warp[2][kWarps];
   int pick[2];
 };
@@ -111,17 +115,24 @@ __device__ __forceinline__ void block_sums(int& x, int& y, int (*part)[kWarps], 
   y = by + v - y;
 }
 
-__global__ void __launch_bounds__(kThreads) evict_kernel(const EvictArgs a) {
+__global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs a) {
   extern __shared__ __align__(16) uint8_t raw[];
   Shared& s = *reinterpret_cast<Shared*>(raw);
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int item = blockIdx.x / C, r = item / a.Hkv, g = item % a.Hkv;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x;
   const int P = a.cache.page_size;
   const int* table = a.table + (int64_t)r * a.table_stride;
   int* kept = a.kept + ((int64_t)r * a.Hkv + g) * a.most;
   const int everyone = C * kThreads, me = rank * kThreads + tid;
+  auto together = [&]() {
+    if (C > 1)
+      cluster.sync();
+    else
+      __syncthreads();
+  };
+  tc::launch_dependents();
 
   Plan p;
   bool good = plan_of(a, r, p);
@@ -140,26 +151,29 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictArgs a) {
   }
   if (g == 0 && rank == 0 && tid == 0) a.new_lens[r] = good ? p.keep : a.ctx[r];
   if (p.keep == p.c) {
+    if (rank == 0 && tid == 0) a.fills[item] = -1;  // nothing moves
     for (int i = me; i < a.most; i += everyone) kept[i] = i < p.c ? i : -1;
     return;
   }
   for (int i = me; i < a.most; i += everyone)
     if (i < p.f || i >= p.cut) kept[i] = i < p.f ? i : (i < p.keep ? i + (p.c - p.keep) : -1);
 
-  // The run of positions [lo, hi) of this CTA.
+  // The run of positions [lo, lo + n) of this CTA.
   const int M = p.c - p.t - p.f, m = p.cut - p.f;
   const int per = (M + C - 1) / C;
-  const int lo = p.f + min(M, rank * per), hi = p.f + min(M, (rank + 1) * per), n = hi - lo;
+  const int lo = p.f + min(M, rank * per), n = p.f + min(M, (rank + 1) * per) - lo;
   const bool held = per <= kRun;
   auto score = [&](int pos) {
     const int page = table[pos / P];
     return ordered(a.scores[((int64_t)page * a.Hkv + g) * P + pos % P]);
   };
   auto key_of = [&](int i) { return held ? s.run[i] : score(lo + i); };
-  if (held)
+  if (held) {
+#pragma unroll 4
     for (int i = tid; i < n; i += kThreads) s.run[i] = score(lo + i);
-  for (int i = tid; i < 2 * kBins; i += kThreads) (&s.count[0][0])[i] = 0;
-  __syncthreads();
+  }
+  for (int i = tid; i < kBins; i += kThreads) s.count[i] = s.total[i] = 0;
+  together();
 
   // The m-th largest, `found` being its leading bits and `left` its rank among those that
   // begin alike.
@@ -169,59 +183,67 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictArgs a) {
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       const int bits = pass < 2 ? 11 : 10;
-      int* count = s.count[pass & 1];
-      if (pass == 2) {  // read by all two meetings ago
-        for (int i = tid; i < kBins; i += kThreads) count[i] = 0;
-        __syncthreads();
-      }
       const int above = shift;
       shift -= bits;
       for (int i = tid; i < n; i += kThreads) {
         const uint32_t k = key_of(i);
         if (pass == 0 || k >> above == found)
-          atomicAdd(&count[k >> shift & ((1u << bits) - 1)], 1);
-      }
-      cluster.sync();
-      // Four bins a thread from the highest down: thread 0 holds the last ones.
-      int mine[kBins / kThreads], sum = 0, none = 0;
-#pragma unroll
-      for (int j = 0; j < kBins / kThreads; ++j) {
-        const int b = kBins - 1 - (tid * (kBins / kThreads) + j);
-        mine[j] = 0;
-        for (int c = 0; c < C; ++c) mine[j] += cluster.map_shared_rank(count, c)[b];
-        sum += mine[j];
-      }
-      int before = sum, t0, t1;
-      block_sums(before, none, s.warp, t0, t1);
-      if (before < left && left <= before + sum) {
-        int x = before;
-#pragma unroll
-        for (int j = 0; j < kBins / kThreads; ++j) {
-          if (x < left && left <= x + mine[j]) {
-            s.pick[0] = kBins - 1 - (tid * (kBins / kThreads) + j);
-            s.pick[1] = left - x;
-          }
-          x += mine[j];
-        }
+          atomicAdd(&s.count[k >> shift & ((1u << bits) - 1)], 1);
       }
       __syncthreads();
+      int* sums = s.count;
+      if (C > 1) {
+        int* first = cluster.map_shared_rank(s.total, 0);
+        for (int i = tid; i < kBins; i += kThreads)
+          if (s.count[i] > 0) atomicAdd(&first[i], s.count[i]);
+        cluster.sync();
+        sums = s.total;
+      }
+      if (rank == 0) {
+        // Two bins a thread from the highest down.
+        const int b = kBins - 1 - 2 * tid, hi = sums[b], lo2 = sums[b - 1];
+        int before = hi + lo2, none = 0, t0, t1;
+        block_sums(before, none, s.warp, t0, t1);
+        int digit = -1, rest = 0;
+        if (before < left && left <= before + hi) {
+          digit = b;
+          rest = left - before;
+        } else if (before + hi < left && left <= before + hi + lo2) {
+          digit = b - 1;
+          rest = left - before - hi;
+        }
+        if (digit >= 0)
+          for (int c = 0; c < C; ++c) {
+            int* pick = C > 1 ? cluster.map_shared_rank(s.pick, c) : s.pick;
+            pick[0] = digit;
+            pick[1] = rest;
+          }
+        __syncthreads();
+        if (C > 1)
+          for (int i = tid; i < kBins; i += kThreads) s.total[i] = 0;
+      }
+      if (C > 1) cluster.sync();
+      for (int i = tid; i < kBins; i += kThreads) s.count[i] = 0;
       found = found << bits | (uint32_t)s.pick[0];
       left = s.pick[1];
-      __syncthreads();
+      together();  // before the next digit is picked
     }
   }
   // Of the equals of `found` the first `left` stay.  Which are in this run: by the runs before.
+  // A thread takes positions one after another, an odd number of them (in different banks).
   int equal = 0, none = 0, mine_equal, t1;
-  const int chunk = (n + kThreads - 1) / kThreads;  // positions a thread, one after another
+  const int chunk = ((n + kThreads - 1) / kThreads) | 1;
   const int i0 = min(n, tid * chunk), i1 = min(n, i0 + chunk);
   if (m > 0)
     for (int i = i0; i < i1; ++i) equal += key_of(i) == found;
   int rank_equal = equal;
   block_sums(rank_equal, none, s.warp, mine_equal, t1);
-  if (tid == 0) s.meet[0] = mine_equal;
-  cluster.sync();
   int quota = left;
-  for (int c = 0; c < rank; ++c) quota -= *cluster.map_shared_rank(&s.meet[0], c);
+  if (C > 1) {
+    if (tid == 0) s.meet[0] = mine_equal;
+    cluster.sync();
+    for (int c = 0; c < rank; ++c) quota -= *cluster.map_shared_rank(&s.meet[0], c);
+  }
   auto stays = [&](int i, int& nth) {
     const uint32_t k = key_of(i);
     if (k != found) return k > found;
@@ -239,21 +261,25 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictArgs a) {
   int all_holes, all_late;
   int hole0 = holes, late0 = late;
   block_sums(hole0, late0, s.warp, all_holes, all_late);
-  if (tid == 0) {
-    s.meet[1] = all_holes;
-    s.meet[2] = all_late;
-  }
-  cluster.sync();
-  int fills = 0;
-  for (int c = 0; c < C; ++c) {
-    const int h = cluster.map_shared_rank(s.meet, c)[1], l = cluster.map_shared_rank(s.meet, c)[2];
-    if (c < rank) {
-      hole0 += h;
-      late0 += l;
+  int fills = all_holes;
+  if (C > 1) {
+    if (tid == 0) {
+      s.meet[1] = all_holes;
+      s.meet[2] = all_late;
     }
-    fills += h;
+    cluster.sync();
+    fills = 0;
+    for (int c = 0; c < C; ++c) {
+      const int h = cluster.map_shared_rank(s.meet, c)[1], l = cluster.map_shared_rank(s.meet, c)[2];
+      if (c < rank) {
+        hole0 += h;
+        late0 += l;
+      }
+      fills += h;
+    }
   }
-  int* to = a.lists + 2 * ((int64_t)r * a.Hkv + g) * a.list_cap;
+  if (rank == 0 && tid == 0) a.fills[item] = fills;
+  int* to = a.lists + 2 * (int64_t)item * a.list_cap;
   int* from = to + a.list_cap;
   nth = rank_equal;
   for (int i = i0; i < i1; ++i) {
@@ -268,88 +294,78 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictArgs a) {
       from[late0++] = pos;
     }
   }
-  __threadfence();
-  cluster.sync();
-
-  // Copies.  A lane takes 16 bytes of the key (the first lanes of a row) or value.
-  const int vecs = a.D / 8, rows = 32 / (2 * vecs);  // of a warp at a time
-  const int which = lane % (2 * vecs) / vecs, col = lane % vecs * 8, sub = lane / (2 * vecs);
-  uint16_t* base = static_cast<uint16_t*>(which ? a.v_cache : a.k_cache) +
-                   g * a.cache.head_stride + col;
-  auto at = [&](int pos) {
-    return base + table[pos / P] * a.cache.page_stride + pos % P * a.cache.token_stride;
-  };
-  auto weight = [&](int pos) {
-    return a.weights + ((int64_t)table[pos / P] * a.Hkv + g) * P + pos % P;
-  };
-  const bool first = lane % (2 * vecs) == 0;
-  constexpr int U = 4;
-  const int step = C * kWarps * rows, begin = (rank * kWarps + warp) * rows + sub;
-  for (int h0 = begin; h0 < fills; h0 += step * U) {
-    uint4 v[U];
-    float x[U];
-    int dst[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * step;
-      if (h < fills) {
-        const int src = __ldcg(from + h);
-        dst[u] = __ldcg(to + h);
-        v[u] = *reinterpret_cast<const uint4*>(at(src));
-        if (first) {
-          x[u] = *weight(src);
-          kept[dst[u]] = src;
-        }
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (h0 + u * step < fills) {
-        *reinterpret_cast<uint4*>(at(dst[u])) = v[u];
-        if (first) *weight(dst[u]) = x[u];
-      }
-  }
-  // The last ones: no wave is written before all of it, and what the copies above
-  // read from its places, has been read.
-  const int shift_by = p.c - p.keep;
-  for (int w0 = p.cut; w0 < p.keep; w0 += step * U) {
-    uint4 v[U];
-    float x[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int pos = w0 + begin + u * step;
-      if (pos < p.keep) {
-        v[u] = *reinterpret_cast<const uint4*>(at(pos + shift_by));
-        if (first) x[u] = *weight(pos + shift_by);
-      }
-    }
-    cluster.sync();
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int pos = w0 + begin + u * step;
-      if (pos < p.keep) {
-        *reinterpret_cast<uint4*>(at(pos)) = v[u];
-        if (first) *weight(pos) = x[u];
-      }
-    }
-  }
-  cluster.sync();  // no CTA leaves while another reads its shared memory
+  if (C > 1) cluster.sync();  // no CTA leaves while another reads its shared memory
 }
 
 // ---------------------------------------------------------------------------
-// The pages that became free, in request order.  Each block sums the requests
-// and fills its share of the list.
+// Blocks (part, item): a warp takes 32 pairs of the item's lists at a time.
 // ---------------------------------------------------------------------------
-constexpr int kFreedThreads = 512;
+constexpr int kFillWarps = 4;
 
-__global__ void __launch_bounds__(kFreedThreads) freed_kernel(const EvictArgs a) {
-  __shared__ int part[2][kFreedThreads / 32];
-  __shared__ int pre[kFreedThreads], have[kFreedThreads], gone[kFreedThreads];
+template <int D>
+__global__ void __launch_bounds__(kFillWarps * 32) evict_fill_kernel(const EvictArgs a) {
+  constexpr int kLanes = D / 4;          // of a pair of rows, 16 bytes each
+  constexpr int kRows = 32 / kLanes;     // of a warp at a time
+  constexpr int U = 8 / kRows;           // turns whose loads are in flight
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int item = a.item0 + blockIdx.y, r = item / a.Hkv, g = item % a.Hkv;
+  const int P = a.cache.page_size;
+  const int* table = a.table + (int64_t)r * a.table_stride;
+  const int sub = lane / kLanes, l = lane % kLanes;
+  // The first half of a pair's lanes copies the key, the second the value.
+  uint16_t* base = static_cast<uint16_t*>(l < kLanes / 2 ? a.k_cache : a.v_cache) +
+                   g * a.cache.head_stride + l % (kLanes / 2) * 8;
+  tc::launch_dependents();
+  tc::wait_prior_grid();
+  const int fills = a.fills[item];
+  const int* to = a.lists + 2 * (int64_t)item * a.list_cap;
+  const int* from = to + a.list_cap;
+  for (int h0 = (blockIdx.x * kFillWarps + warp) * 32; h0 < fills;
+       h0 += gridDim.x * kFillWarps * 32) {
+    const int n = min(32, fills - h0);
+    int64_t src = 0, dst = 0;
+    if (lane < n) {
+      const int x = from[h0 + lane], y = to[h0 + lane];
+      const int px = table[x / P], py = table[y / P];
+      a.kept[(int64_t)item * a.most + y] = x;
+      a.weights[((int64_t)py * a.Hkv + g) * P + y % P] =
+          a.weights[((int64_t)px * a.Hkv + g) * P + x % P];
+      src = px * a.cache.page_stride + x % P * a.cache.token_stride;
+      dst = py * a.cache.page_stride + y % P * a.cache.token_stride;
+    }
+    for (int j0 = 0; j0 < n; j0 += U * kRows) {
+      uint4 v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int j = j0 + u * kRows + sub;
+        const int64_t at = __shfl_sync(0xffffffffu, src, j & 31);
+        if (j < n) v[u] = *reinterpret_cast<const uint4*>(base + at);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int j = j0 + u * kRows + sub;
+        const int64_t at = __shfl_sync(0xffffffffu, dst, j & 31);
+        if (j < n) *reinterpret_cast<uint4*>(base + at) = v[u];
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Blocks (slice, item): 64 bytes of each of the last rows (slice 0 their weights, too).
+// The blocks behind those list the pages that became free, in request order: each sums
+// the requests and fills its share of the list.
+// ---------------------------------------------------------------------------
+constexpr int kShiftThreads = 512;
+
+__device__ __forceinline__ void list_freed(const EvictArgs& a, int block, int blocks) {
+  __shared__ int part[kShiftThreads / 32];
+  __shared__ int pre[kShiftThreads], have[kShiftThreads];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, P = a.cache.page_size;
   long long done = 0;  // pages of the requests before
-  const long long stride = (long long)gridDim.x * kFreedThreads;
-  const long long mine = (long long)blockIdx.x * kFreedThreads + tid;
-  for (int r0 = 0; r0 < a.R; r0 += kFreedThreads) {
+  const long long stride = (long long)blocks * kShiftThreads;
+  const long long mine = (long long)block * kShiftThreads + tid;
+  for (int r0 = 0; r0 < a.R; r0 += kShiftThreads) {
     const int r = r0 + tid;
     int first = 0, n = 0;
     if (r < a.R) {
@@ -363,22 +379,21 @@ __global__ void __launch_bounds__(kFreedThreads) freed_kernel(const EvictArgs a)
       const int u = __shfl_up_sync(0xffffffffu, sum, d);
       if (lane >= d) sum += u;
     }
-    if (lane == 31) part[0][warp] = sum;
+    if (lane == 31) part[warp] = sum;
     __syncthreads();
     int before = 0, total = 0;
-    for (int w = 0; w < kFreedThreads / 32; ++w) {
+    for (int w = 0; w < kShiftThreads / 32; ++w) {
       if (w == warp) before = total;
-      total += part[0][w];
+      total += part[w];
     }
     pre[tid] = before + sum - n;
     have[tid] = first;
-    gone[tid] = n;
     __syncthreads();
     const long long end = done + total < a.num_freed_max ? done + total : a.num_freed_max;
     for (long long x = mine < done ? mine + (done - mine + stride - 1) / stride * stride : mine;
          x < end; x += stride) {
       const int y = (int)(x - done);
-      int l = 0, h = kFreedThreads;  // the last request that begins at y or before
+      int l = 0, h = kShiftThreads;  // the last request that begins at y or before
       while (h - l > 1) {
         const int mid = (l + h) / 2;
         if (pre[mid] <= y)
@@ -400,6 +415,71 @@ __global__ void __launch_bounds__(kFreedThreads) freed_kernel(const EvictArgs a)
   }
 }
 
+__global__ void __launch_bounds__(kShiftThreads)
+    evict_shift_kernel(const EvictArgs a, int slices, int freed_blocks) {
+  tc::wait_prior_grid();
+  const int64_t shifts = (int64_t)a.R * a.Hkv * slices;
+  if (blockIdx.x >= shifts) {
+    list_freed(a, (int)(blockIdx.x - shifts), freed_blocks);
+    return;
+  }
+  const int item = blockIdx.x / slices, slice = blockIdx.x % slices;
+  const int r = item / a.Hkv, g = item % a.Hkv, P = a.cache.page_size;
+  if (a.fills[item] < 0) return;
+  Plan p;
+  plan_of(a, r, p);
+  const int by = p.c - p.keep;
+  const int* table = a.table + (int64_t)r * a.table_stride;
+  const int half = slices / 2, tid = threadIdx.x;
+  uint16_t* base = static_cast<uint16_t*>(slice < half ? a.k_cache : a.v_cache) +
+                   g * a.cache.head_stride + slice % half * 32 + tid % 4 * 8;
+  auto at = [&](int pos) {
+    return base + table[pos / P] * a.cache.page_stride + pos % P * a.cache.token_stride;
+  };
+  auto weight = [&](int pos) {
+    return a.weights + ((int64_t)table[pos / P] * a.Hkv + g) * P + pos % P;
+  };
+  const bool weighs = slice == 0 && tid % 4 == 0;
+  constexpr int U = 4, kRows = kShiftThreads / 4;
+  for (int w0 = p.cut; w0 < p.keep; w0 += U * kRows) {
+    uint4 v[U];
+    float x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int pos = w0 + u * kRows + tid / 4;
+      if (pos < p.keep) {
+        v[u] = *reinterpret_cast<const uint4*>(at(pos + by));
+        if (weighs) x[u] = *weight(pos + by);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int pos = w0 + u * kRows + tid / 4;
+      if (pos < p.keep) {
+        *reinterpret_cast<uint4*>(at(pos)) = v[u];
+        if (weighs) *weight(pos) = x[u];
+      }
+    }
+  }
+}
+
+// A launch that may begin while the one before it ends.
+template <typename... Args>
+cudaError_t launch_behind(void (*kernel)(Args...), dim3 grid, int threads, cudaStream_t stream,
+                          Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 }  // namespace
 
 cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t stream) {
@@ -409,29 +489,49 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t stream) {
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   static DeviceOnce allowed;
-  e = allowed.shared_memory(reinterpret_cast<const void*>(evict_kernel), dev, sizeof(Shared));
+  e = allowed.shared_memory(reinterpret_cast<const void*>(evict_select_kernel), dev, sizeof(Shared));
   if (e != cudaSuccess) return e;
   const int64_t items = (int64_t)a.R * a.Hkv;
-  int C = kMaxCluster;
-  while (C > 1 && items * C > 2 * sms) C /= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(items * C));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = sizeof(Shared);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = C;
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, evict_kernel, a);
-  if (e != cudaSuccess) return e;
-  const int64_t want = (a.num_freed_max + kFreedThreads - 1) / kFreedThreads;
-  const int grid = (int)(want < 1 ? 1 : (want < sms ? want : sms));
-  freed_kernel<<<grid, kFreedThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  const int slices = a.D * 4 / 64;
+  const int freed_blocks = a.num_freed_max / (8 * kShiftThreads) < sms
+                               ? a.num_freed_max / (8 * kShiftThreads) + 1
+                               : sms;
+  if (items > 0) {
+    // A CTA whose shared memory holds the scores that a request can have, or a cluster.
+    const int64_t longest = (int64_t)a.width * a.cache.page_size;
+    int C = 1;
+    while (C < kMaxCluster && C * (int64_t)kRun < longest) C *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(items * C));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = sizeof(Shared);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = C;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a);
+    if (e != cudaSuccess) return e;
+    // Warps for all the pairs that there can be, as far as the SMs can hold them.
+    const int64_t pairs = (a.list_cap + kFillWarps * 32 - 1) / (kFillWarps * 32);
+    int64_t parts = (int64_t)sms * 16 / items + 1;
+    if (parts > pairs) parts = pairs > 0 ? pairs : 1;
+    // (65535 blocks in y at most.)
+    for (int64_t i0 = 0; i0 < items; i0 += 65535) {
+      EvictArgs b = a;
+      const int64_t n = items - i0 < 65535 ? items - i0 : 65535;
+      b.item0 = (int)i0;
+      const dim3 grid((unsigned)parts, (unsigned)n);
+      e = a.D == 128 ? launch_behind(evict_fill_kernel<128>, grid, kFillWarps * 32, stream, b)
+                     : launch_behind(evict_fill_kernel<64>, grid, kFillWarps * 32, stream, b);
+      if (e != cudaSuccess) return e;
+    }
+  }
+  return launch_behind(evict_shift_kernel, dim3((unsigned)(items * slices + freed_blocks)),
+                       kShiftThreads, stream, a, slices, freed_blocks);
 }
 
 }  // namespace cpattn

@@ -801,9 +801,9 @@ CPATTN_API int cpattn_cache_weights(const void* q, int64_t q_stride, const void*
  * in freed raise the device error word; such a request is left as it is
  * (new_lens = c), and pages that freed has no room for are not listed.  No page belongs to
  * two requests of the call.
- *   first, recent >= 0; most 1 to 2^26; R at most 65535, R * Hkv * most below
- *   2^40, Hkv at most 65535; the cache as above, dtype CPATTN_BF16 or
- *   CPATTN_F16.
+ *   first, recent >= 0; most 1 to 2^26; R and Hkv at most 65535, R * Hkv at
+ *   most 2^24, R * Hkv * most below 2^40; the cache as above, dtype CPATTN_BF16
+ *   or CPATTN_F16.
  * workspace: device, at least cpattn_cache_evict_workspace_bytes, 256-byte
  * aligned, scratch.
  */
