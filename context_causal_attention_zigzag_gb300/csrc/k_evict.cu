@@ -50,8 +50,8 @@ struct Shared {
   int count[kBins];  // of the digits
   int total[kBins];  // the cluster's, in its first CTA
   int meet[4];       // this CTA's counts, read by the others
-  int warp[2][kWarps];
-  int pick[2];
+  int warp[6][kWarps];
+  int pick[3];
 };
 
 // Integers in the order of the scores: NaN lowest, -0 as 0.
@@ -81,38 +81,23 @@ __device__ __forceinline__ bool plan_of(const EvictArgs& a, int r, Plan& p) {
   return true;
 }
 
-// Exclusive sums of two values over the block; the block's in tot.
-__device__ __forceinline__ void block_sums(int& x, int& y, int (*part)[kWarps], int& tot_x,
-                                           int& tot_y) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int u = x, v = y;
+__device__ __forceinline__ int warp_sums(int x) {  // inclusive
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int p = __shfl_up_sync(0xffffffffu, u, d), q = __shfl_up_sync(0xffffffffu, v, d);
-    if (lane >= d) {
-      u += p;
-      v += q;
-    }
+    const int u = __shfl_up_sync(0xffffffffu, x, d);
+    if ((threadIdx.x & 31) >= d) x += u;
   }
-  __syncthreads();  // the sums before are read
-  if (lane == 31) {
-    part[0][warp] = u;
-    part[1][warp] = v;
-  }
+  return x;
+}
+
+// The sum of the warps' values before this warp's; the block's in tot.  `part` is used once.
+__device__ __forceinline__ int warps_before(int x, int* part, int& tot) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (lane == 0) part[warp] = x;
   __syncthreads();
-  tot_x = tot_y = 0;
-  int bx = 0, by = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w == warp) {
-      bx = tot_x;
-      by = tot_y;
-    }
-    tot_x += part[0][w];
-    tot_y += part[1][w];
-  }
-  x = bx + u - x;
-  y = by + v - y;
+  const int mine = part[lane], upto = warp_sums(mine);
+  tot = __shfl_sync(0xffffffffu, upto, 31);
+  return __shfl_sync(0xffffffffu, upto - mine, warp);
 }
 
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs a) {
@@ -155,8 +140,9 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
     for (int i = me; i < a.most; i += everyone) kept[i] = i < p.c ? i : -1;
     return;
   }
+  // (The fills put in what comes from elsewhere.)
   for (int i = me; i < a.most; i += everyone)
-    if (i < p.f || i >= p.cut) kept[i] = i < p.f ? i : (i < p.keep ? i + (p.c - p.keep) : -1);
+    kept[i] = i < p.cut ? i : (i < p.keep ? i + (p.c - p.keep) : -1);
 
   // The run of positions [lo, lo + n) of this CTA.
   const int M = p.c - p.t - p.f, m = p.cut - p.f;
@@ -202,21 +188,26 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
       if (rank == 0) {
         // Two bins a thread from the highest down.
         const int b = kBins - 1 - 2 * tid, hi = sums[b], lo2 = sums[b - 1];
-        int before = hi + lo2, none = 0, t0, t1;
-        block_sums(before, none, s.warp, t0, t1);
-        int digit = -1, rest = 0;
+        const int upto = warp_sums(hi + lo2);
+        int all;
+        const int before = upto - hi - lo2 +
+                           warps_before(__shfl_sync(0xffffffffu, upto, 31), s.warp[pass], all);
+        int digit = -1, rest = 0, alike = 0;
         if (before < left && left <= before + hi) {
           digit = b;
           rest = left - before;
+          alike = hi;
         } else if (before + hi < left && left <= before + hi + lo2) {
           digit = b - 1;
           rest = left - before - hi;
+          alike = lo2;
         }
         if (digit >= 0)
           for (int c = 0; c < C; ++c) {
             int* pick = C > 1 ? cluster.map_shared_rank(s.pick, c) : s.pick;
             pick[0] = digit;
             pick[1] = rest;
+            pick[2] = rest == alike;
           }
         __syncthreads();
         if (C > 1)
@@ -226,41 +217,52 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
       for (int i = tid; i < kBins; i += kThreads) s.count[i] = 0;
       found = found << bits | (uint32_t)s.pick[0];
       left = s.pick[1];
+      const bool enough = s.pick[2];
       together();  // before the next digit is picked
+      if (enough) break;  // all that begin alike stay
     }
   }
-  // Of the equals of `found` the first `left` stay.  Which are in this run: by the runs before.
-  // A thread takes positions one after another, an odd number of them (in different banks).
-  int equal = 0, none = 0, mine_equal, t1;
-  const int chunk = ((n + kThreads - 1) / kThreads) | 1;
-  const int i0 = min(n, tid * chunk), i1 = min(n, i0 + chunk);
-  if (m > 0)
-    for (int i = i0; i < i1; ++i) equal += key_of(i) == found;
-  int rank_equal = equal;
-  block_sums(rank_equal, none, s.warp, mine_equal, t1);
-  int quota = left;
+  // Of those whose leading bits equal `found` the first `left` stay: which of them are in this
+  // run, by the runs before.  A warp takes a row of positions, 32 at a time.
+  const int lane = tid & 31, warp = tid >> 5;
+  const unsigned below = (1u << lane) - 1;
+  const int chunk = (n + kThreads - 1) / kThreads * 32;
+  const int i0 = min(n, warp * chunk), i1 = min(n, i0 + chunk);
+  auto lead_of = [&](int i) { return shift < 32 ? key_of(i) >> shift : 0u; };
+  int equal = 0;
+  for (int i = i0; i < i1; i += 32)
+    equal += __popc(__ballot_sync(0xffffffffu, m > 0 && i + lane < i1 && lead_of(i + lane) == found));
+  int mine_equal, quota = left;
+  const int equal0 = warps_before(equal, s.warp[3], mine_equal);
   if (C > 1) {
     if (tid == 0) s.meet[0] = mine_equal;
     cluster.sync();
     for (int c = 0; c < rank; ++c) quota -= *cluster.map_shared_rank(&s.meet[0], c);
   }
-  auto stays = [&](int i, int& nth) {
-    const uint32_t k = key_of(i);
-    if (k != found) return k > found;
-    return nth++ < quota;
+  // Whether the warp's 32 positions from i on stay, as bits.
+  auto stays = [&](int i, int& seen) {
+    const bool on = m > 0 && i + lane < i1;
+    const uint32_t k = on ? lead_of(i + lane) : 0;
+    const unsigned same = __ballot_sync(0xffffffffu, on && k == found);
+    const bool stay = on && (k > found || (k == found && seen + __popc(same & below) < quota));
+    seen += __popc(same);
+    return __ballot_sync(0xffffffffu, stay);
+  };
+  // Positions from i on that lie below the cut, as bits.
+  auto early_of = [&](int i) {
+    const int e = min(p.cut, lo + i1) - (lo + i);
+    return e >= 32 ? 0xffffffffu : (e <= 0 ? 0u : (1u << e) - 1);
   };
   // Places that become free below the cut, and positions that stay behind it.
-  int holes = 0, late = 0, nth = rank_equal;
-  for (int i = i0; i < i1; ++i) {
-    const bool stay = m > 0 && stays(i, nth);
-    if (lo + i < p.cut)
-      holes += !stay;
-    else
-      late += stay;
+  int holes = 0, late = 0, seen = equal0;
+  for (int i = i0; i < i1; i += 32) {
+    const unsigned stay = stays(i, seen), early = early_of(i);
+    holes += __popc(early & ~stay);
+    late += __popc(stay & ~early);
   }
   int all_holes, all_late;
-  int hole0 = holes, late0 = late;
-  block_sums(hole0, late0, s.warp, all_holes, all_late);
+  int hole0 = warps_before(holes, s.warp[4], all_holes);
+  int late0 = warps_before(late, s.warp[5], all_late);
   int fills = all_holes;
   if (C > 1) {
     if (tid == 0) {
@@ -281,18 +283,14 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
   if (rank == 0 && tid == 0) a.fills[item] = fills;
   int* to = a.lists + 2 * (int64_t)item * a.list_cap;
   int* from = to + a.list_cap;
-  nth = rank_equal;
-  for (int i = i0; i < i1; ++i) {
-    const int pos = lo + i;
-    const bool stay = m > 0 && stays(i, nth);
-    if (pos < p.cut) {
-      if (stay)
-        kept[pos] = pos;
-      else
-        to[hole0++] = pos;
-    } else if (stay) {
-      from[late0++] = pos;
-    }
+  seen = equal0;
+  for (int i = i0; i < i1; i += 32) {
+    const unsigned stay = stays(i, seen), early = early_of(i);
+    const unsigned free_ = early & ~stay, go = stay & ~early;
+    if (free_ >> lane & 1) to[hole0 + __popc(free_ & below)] = lo + i + lane;
+    if (go >> lane & 1) from[late0 + __popc(go & below)] = lo + i + lane;
+    hole0 += __popc(free_);
+    late0 += __popc(go);
   }
   if (C > 1) cluster.sync();  // no CTA leaves while another reads its shared memory
 }
