@@ -118,6 +118,37 @@ struct Sums {
   float* sums;  // [kMaxCtas][2][kPair]
 };
 
+// Two float32 values in a register pair: an instruction for both.
+typedef unsigned long long Two;
+__device__ __forceinline__ Two two(float x, float y) {
+  Two p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+  return p;
+}
+__device__ __forceinline__ Two two(uint32_t x, uint32_t y) {
+  return two(__uint_as_float(x), __uint_as_float(y));
+}
+__device__ __forceinline__ float2 apart(Two p) {
+  float2 x;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x.x), "=f"(x.y) : "l"(p));
+  return x;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  Two d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+  Two d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ void exps(float& x, float& y, Two p) {
+  const float2 f = apart(p);
+  x = ex2(f.x);
+  y = ex2(f.y);
+}
+
 template <bool kBf16, int D, bool kDeep>
 __global__ void __launch_bounds__(Cfg<D, kDeep>::kThreads, 1)
     weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -486,7 +517,6 @@ __global__ void __launch_bounds__(Cfg<D, kDeep>::kThreads, 1)
     const int group = (warp - 4) >> 2;
     const int row = (warp & 3) * 32 + lane;  // TMEM lane, key of the tile
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const float sl2 = a.scale_log2;
     const int P = a.cache.page_size;
     uint32_t rows = 0, used = 0, made1 = 0;  // made1: all products of key tile 1
     uint32_t phases = 0;                     // of this warpgroup's barriers of the places
@@ -506,62 +536,64 @@ __global__ void __launch_bounds__(Cfg<D, kDeep>::kThreads, 1)
       if (u.whole && pos < u.ctx) old = *to;
       return to;
     };
-    float t0, t1, t2, t3;
-    auto add = [&](float y0, float y1, float y2, float y3) {
-      t0 += y0;
-      t1 += y1;
-      t2 += y2;
-      t3 += y3;
+    const Two sl2 = two(a.scale_log2, a.scale_log2);
+    Two t0, t1;
+    // Adds up 32 columns from c on of a key's row of products with the tile of rows at tok0, of
+    // which all (whole) or those that see the key count.
+    auto columns = [&](const uint32_t* r, const float* nl, int c, bool whole, int ahead_by, int tok0,
+                       int ntok, int n, int q0) {
+      float y[32];
+#pragma unroll
+      for (int j = 0; j < 32; j += 4) {
+        const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(nl + c + j);
+        exps(y[j], y[j + 1], fma2(two(r[j], r[j + 1]), sl2, l.x));
+        exps(y[j + 2], y[j + 3], fma2(two(r[j + 2], r[j + 3]), sl2, l.y));
+      }
+      if (!whole) {
+        // Which of the columns see this key: of the live ones those of the key's own token
+        // and later ones, or those whose word names it.
+        const int hi = ntok * G - c;
+        uint32_t seen = hi >= 32 ? 0xffffffffu : (1u << hi) - 1;
+        const int lo = (chain && ahead_by > tok0 ? min(ahead_by - tok0, tpt) * G : 0) - c;
+        if (lo > 0) seen = lo >= 32 ? 0u : seen >> lo << lo;
+        if (!chain && ahead_by >= 0) {
+          uint32_t named = 0;
+          for (int t = c / G; t < ntok && t * G < c + 32; ++t) {
+            const unsigned long long word = a.tree[q0 + tok0 + t];
+            if (ahead_by < n && ahead_by < 64 && (word >> ahead_by & 1)) {
+              const int b = max(t * G - c, 0), e = min(t * G + G - c, 32);
+              named |= (e - b >= 32 ? 0xffffffffu : (1u << (e - b)) - 1) << b;
+            }
+          }
+          seen &= named;
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j) y[j] = seen >> j & 1 ? y[j] : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < 32; j += 4) {
+        t0 = add2(t0, two(y[j], y[j + 1]));
+        t1 = add2(t1, two(y[j + 2], y[j + 3]));
+      }
     };
-    // A key's row of products with the tile of rows at tok0, of which all (whole) or those
-    // that see the key count; frees the products' place.
+    // The whole row; frees the products' place.
     auto row_sum = [&](uint32_t at, int free_bar, const float* nl, bool whole, int ahead_by, int tok0,
                        int n, int q0) {
-      t0 = t1 = t2 = t3 = 0.f;
+      t0 = t1 = two(0.f, 0.f);
       const int ntok = min(tpt, n - tok0), live = ntok * G;
-      const int first = chain && ahead_by > tok0 ? min(ahead_by - tok0, tpt) * G : 0;
 #pragma unroll 1
       for (int c = 0; c < live; c += 32) {
         uint32_t r[32];
         tmem_ld32(at + c, r);
-        const int hi = live - c, lo = first - c;
         tmem_wait_ld_regs(r);
-        if (hi <= 32) {
+        if (c + 32 >= live) {
           tc_fence_before();
           mbar_arrive(bar(free_bar));
         }
-        float y[32];
-#pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const float4 l = *reinterpret_cast<const float4*>(nl + c + j);
-          y[j] = ex2(fmaf(__uint_as_float(r[j]), sl2, l.x));
-          y[j + 1] = ex2(fmaf(__uint_as_float(r[j + 1]), sl2, l.y));
-          y[j + 2] = ex2(fmaf(__uint_as_float(r[j + 2]), sl2, l.z));
-          y[j + 3] = ex2(fmaf(__uint_as_float(r[j + 3]), sl2, l.w));
-        }
-        if (!whole) {
-          // Which of the columns see this key: of the live ones those of the key's own token
-          // and later ones, or those whose word names it.
-          uint32_t seen = hi >= 32 ? 0xffffffffu : (1u << hi) - 1;
-          if (lo > 0) seen = lo >= 32 ? 0u : seen >> lo << lo;
-          if (!chain && ahead_by >= 0) {
-            uint32_t named = 0;
-            for (int t = c / G; t < ntok && t * G < c + 32; ++t) {
-              const unsigned long long word = a.tree[q0 + tok0 + t];
-              if (ahead_by < n && ahead_by < 64 && (word >> ahead_by & 1)) {
-                const int b = max(t * G - c, 0), e = min(t * G + G - c, 32);
-                named |= (e - b >= 32 ? 0xffffffffu : (1u << (e - b)) - 1) << b;
-              }
-            }
-            seen &= named;
-          }
-#pragma unroll
-          for (int j = 0; j < 32; ++j) y[j] = seen >> j & 1 ? y[j] : 0.f;
-        }
-#pragma unroll
-        for (int j = 0; j < 32; j += 4) add(y[j], y[j + 1], y[j + 2], y[j + 3]);
+        columns(r, nl, c, whole, ahead_by, tok0, ntok, n, q0);
       }
-      return (t0 + t1) + (t2 + t3);
+      const float2 x0 = apart(t0), x1 = apart(t1);
+      return (x0.x + x0.y) + (x1.x + x1.y);
     };
     // total + x, with what the rounding leaves out in `lost`.
     auto plus = [](float& total, float& lost, float x) {
