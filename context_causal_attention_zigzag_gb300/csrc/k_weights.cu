@@ -129,6 +129,25 @@ cudaError_t run(const WeightsArgs& w, int sms, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+// Whether the CUDA cores are faster, from a call's sizes (the lengths themselves are on the
+// device; a table much wider than its requests makes both estimates too high).  Measured (us,
+// CUDA cores / tensor cores; H = 32, Hkv = 8, D = 128), by requests x tokens and keys a request:
+//              16          64         256        1000        4000
+//    1 x 1  5.0 / 6.8   5.1 / 6.8   5.6 / 8.1  5.8 / 8.3   7.3 / 8.9
+//    8 x 1  5.2 / 7.9   5.3 / 7.9   7.3 / 8.7   14 / 12     34 / 22
+//   64 x 1  9.1 / 15     11 / 16     25 / 24    70 / 40    273 / 119
+//    1 x 8   19 / 6.9    19 / 7.1    19 / 8.2   20 / 8.3    24 / 8.8
+// Many rows are left to the tensor cores however they are spread: a thread here walks all those
+// of its request.
+bool small_weights(const TreeArgs& a) {
+  const int64_t rows = (int64_t)a.N * (a.H / a.Hkv), keys = (int64_t)a.width * a.cache.page_size;
+  if (rows > 32) return false;
+  const float mean = (float)rows / a.R, heads = (float)a.R * a.Hkv;
+  const float latency = 4.2f + 0.46f * mean;
+  const float work = 5.f + heads * ((keys + 127) / 128) * (0.009f + 0.0018f * mean);
+  return (latency > work ? latency : work) < 7.5f + 0.0148f * heads * ((keys + 255) / 256);
+}
+
 }  // namespace
 
 cudaError_t launch_cache_weights(const WeightsArgs& w, int dtype, cudaStream_t stream) {
@@ -137,8 +156,7 @@ cudaError_t launch_cache_weights(const WeightsArgs& w, int dtype, cudaStream_t s
   if (e != cudaSuccess) return e;
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const int64_t rows = (int64_t)w.t.N * (w.t.H / w.t.Hkv);
-  if (rows <= 32 && (int64_t)w.t.width * w.t.cache.page_size <= 2048)
+  if (small_weights(w.t))
     return dtype == CPATTN_BF16 ? run<true>(w, sms, stream) : run<false>(w, sms, stream);
   return launch_tc_weights(w, dtype, dev, sms, stream);
 }
