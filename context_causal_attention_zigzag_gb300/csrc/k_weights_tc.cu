@@ -274,6 +274,11 @@ __global__ void __launch_bounds__(Cfg<D, kDeep>::kThreads, 1)
   __syncthreads();  // the sums' place is used again
   Piece& p = walk.p;
 
+  // Pages of up to a tile are powers of two.
+  const int P = a.cache.page_size, P_log = P <= kT ? 31 - __clz(P) : 0;
+  auto page_index = [&](int pos) { return P <= kT ? pos >> P_log : pos / P; };
+  auto in_page = [&](int tile_pos) { return P <= kT ? 0 : tile_pos % P; };  // of a tile's begin
+
   auto wwait = [&](uint32_t bar_addr, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait_short(bar_addr, parity, wc));
   };
@@ -288,13 +293,12 @@ __global__ void __launch_bounds__(Cfg<D, kDeep>::kThreads, 1)
     }
     const int box_bytes = q_box * G * 128;
     uint32_t rows = 0;
-    const int P = a.cache.page_size;
     const int box = P < kT ? P : kT;  // rows of a copy
     const int ppt = kT / box;         // copies of a tile and 64 columns
     const int npages = (int)a.cache.num_pages;
     auto page_of = [&](const Piece& u) {
       const int at = u.m * kPair + lane * box;
-      return lane < 2 * ppt && at < u.x.total ? a.table[(int64_t)u.r * a.table_stride + at / P] : -1;
+      return lane < 2 * ppt && at < u.x.total ? a.table[(int64_t)u.r * a.table_stride + page_index(at)] : -1;
     };
     const int c = lane / C::kHalves, half = lane % C::kHalves;
     uint32_t seq[2] = {0, 0};
@@ -320,7 +324,7 @@ __global__ void __launch_bounds__(Cfg<D, kDeep>::kThreads, 1)
         __syncwarp();
         if (good)
           tma_load_4d(base + C::kOffK + sl * C::kTileBytes + half * kBoxBytes + c * box * 128, &tm_k,
-                      bar(C::kBarKFull + sl), half * 64, p.g, k0 % P, id);
+                      bar(C::kBarKFull + sl), half * 64, p.g, in_page(k0), id);
       }
       // The rows: boxes of q_box tokens and 64 columns, one a lane.  A box may reach into
       // another request's rows; their columns are passed over.
@@ -423,11 +427,11 @@ __global__ void __launch_bounds__(Cfg<D, kDeep>::kThreads, 1)
       bool fresh;
     } at = {}, then = {};  // the piece whose normalisers go out, and the next
     // Lane l holds the page number of the l-th part of the pair, the next pair's ahead.
-    const int P = a.cache.page_size, box = P < kT ? P : kT, parts_of_pair = 2 * (kT / box);
+    const int box = P < kT ? P : kT, parts_of_pair = 2 * (kT / box);
     auto page_of = [&](const Piece& u) {
       const int pos = u.m * kPair + lane * box;
       return lane < parts_of_pair && pos < u.x.total
-                 ? a.table[(int64_t)u.r * a.table_stride + pos / P]
+                 ? a.table[(int64_t)u.r * a.table_stride + page_index(pos)]
                  : -1;
     };
     int pages_ahead = walk.more ? page_of(walk.ahead) : -1;
@@ -461,8 +465,8 @@ __global__ void __launch_bounds__(Cfg<D, kDeep>::kThreads, 1)
         c.last = p.last;
         c.fresh = p.fresh;
         c.whole = p.whole();
-        c.in_page[0] = p.m * kPair % P;
-        c.in_page[1] = (p.m * kPair + kT) % P;
+        c.in_page[0] = in_page(p.m * kPair);
+        c.in_page[1] = in_page(p.m * kPair + kT);
         c.end_cta = c.whole || p.s0 > 0 ? -1 : cuts.of(p.item_at + kItemCost + p.steps - 1);
       }
       mbar_arrive(bar(C::kBarPFull + sl));
@@ -517,7 +521,6 @@ __global__ void __launch_bounds__(Cfg<D, kDeep>::kThreads, 1)
     const int group = (warp - 4) >> 2;
     const int row = (warp & 3) * 32 + lane;  // TMEM lane, key of the tile
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const int P = a.cache.page_size;
     uint32_t rows = 0, used = 0, made1 = 0;  // made1: all products of key tile 1
     uint32_t phases = 0;                     // of this warpgroup's barriers of the places
     int behind = group;  // steps until this warpgroup's next
@@ -529,7 +532,7 @@ __global__ void __launch_bounds__(Cfg<D, kDeep>::kThreads, 1)
     auto weight_of = [&](const Note& u, float& old) -> float* {
       if (group > 1) return nullptr;
       const int pos = u.m * kPair + group * kT + row;
-      const int page = u.page[P < kT ? (group * kT + row) / P : group];
+      const int page = u.page[P < kT ? (group * kT + row) >> P_log : group];
       if (pos >= u.total || page < 0) return nullptr;
       float* to = args.weights + ((int64_t)page * a.Hkv + u.g) * P +
                   (P < kT ? row & (P - 1) : u.in_page[group] + row);

@@ -102,6 +102,7 @@ struct Piece {
 struct Walk {
   Piece p, ahead;
   bool more;       // ahead is a piece
+  int tiles, items;  // of ahead's request (a division for each piece would hold up its warp)
   long long left;  // of the CTA's part
   int off;         // where it goes on within the item; -1: at the next item
 
@@ -112,9 +113,13 @@ struct Walk {
     } while (ahead.x.n == 0);
     return true;
   }
+  __host__ __device__ inline void request(int tpt) {
+    tiles = tiles_of(ahead.x, tpt);
+    items = items_of(ahead.x);
+  }
   __host__ __device__ inline void item(int tpt, bool chain) {
-    ahead.q0t = first_tile(ahead.x, tpt, chain, ahead.m * kPair);
-    ahead.steps = tiles_of(ahead.x, tpt) - ahead.q0t;
+    ahead.q0t = tiles > 1 ? first_tile(ahead.x, tpt, chain, ahead.m * kPair) : 0;
+    ahead.steps = tiles - ahead.q0t;
   }
   // The part of n units begins in request r (x), `in_req` behind the request's begin,
   // at `at` on the line.
@@ -127,7 +132,7 @@ struct Walk {
     p = Piece();
     ahead = Piece();
     p.last = true;
-    off = 0;
+    off = tiles = items = 0;
     if (left <= 0) return;
     ahead.r = r;
     ahead.x = x;
@@ -152,6 +157,7 @@ struct Walk {
     ahead.m = lo;
     off = (int)(rest - cost_upto(x, tpt, chain, lo));
     ahead.item_at = at - off;
+    request(tpt);
     item(tpt, chain);
     advance(a, tpt);
   }
@@ -162,7 +168,7 @@ struct Walk {
       if (off < 0) {
         off = 0;
         ahead.item_at += kItemCost + ahead.steps;
-        if (++ahead.m == items_of(ahead.x)) {
+        if (++ahead.m == items) {
           ahead.m = 0;
           if (++ahead.g == a.Hkv) {
             ahead.g = 0;
@@ -170,6 +176,7 @@ struct Walk {
               left = 0;
               return;
             }
+            request(tpt);
           }
         }
         item(tpt, chain);
@@ -189,11 +196,11 @@ struct Walk {
   // keep: a tile of tokens that is its request's only one serves the next piece too.
   __host__ __device__ inline bool next(const TreeArgs& a, int tpt, bool keep) {
     if (!more) return false;
-    const bool fresh = p.last;
+    const bool fresh = p.last, only = tiles == 1;
     p = ahead;
     p.fresh = fresh;
     advance(a, tpt);
-    p.last = !(keep && more && ahead.r == p.r && ahead.g == p.g && tiles_of(p.x, tpt) == 1);
+    p.last = !(keep && more && ahead.r == p.r && ahead.g == p.g && only);
     return true;
   }
 };
