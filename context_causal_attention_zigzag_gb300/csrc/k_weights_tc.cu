@@ -23,9 +23,9 @@
 // rows of S of their own, which nobody stores.  Columns of tokens behind its last one,
 // or that do not see a key, are passed over by selection.
 //
-// Threads: warp 0 loads K and Q, warps 1 and 2 issue the products of a key tile each,
-// warp 3 writes down the pieces and the normalisers, warps 4-11 or 4-15 are the
-// warpgroups, a key a thread.  TMEM: two places of 128 columns for each key tile's products.
+// Threads: warp 0 (where keys stream, 4 too) loads K and Q, warps 1 and 2 issue the
+// products of a key tile each, warp 3 writes down the pieces and the normalisers, the last
+// 8 or 12 warps are the warpgroups, a key a thread.  TMEM: two places of 128 columns for each key tile's products.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -69,7 +69,8 @@ template <int D, bool kDeep>
 struct Cfg {
   static constexpr int kGroups = kDeep ? 2 : 3;  // warpgroups
   static constexpr int kHands = 128 * kGroups;   // their threads
-  static constexpr int kThreads = 128 + kHands;
+  static constexpr int kCtl = kDeep ? 8 : 4;  // warps before them
+  static constexpr int kThreads = 32 * kCtl + kHands;
   static constexpr int kHalves = D / 64;
   static constexpr int kTileBytes = kHalves * kBoxBytes;
   static constexpr int kDepth = kDeep ? (D == 128 ? 3 : 6) : 2;  // of a key tile's ring
@@ -283,8 +284,10 @@ __global__ void __launch_bounds__(Cfg<D, kDeep>::kThreads, 1)
     return __all_sync(0xffffffffu, mbar_wait_short(bar_addr, parity, wc));
   };
 
-  if (warp == 0) {
+  if (warp == 0 || (kDeep && warp == 4)) {
     // -------------------------------------------------------------- K and Q
+    // Deep: warp 0 loads the first key tile and Q, warp 4 the second (one for both took
+    // longer to walk and to issue than HBM to bring them).
     // Lane l holds the page number of copy l of the pair (the next pair's are fetched
     // ahead); lane c * halves + half issues copy c of a tile, columns 64 * half.
     if (lane == 0) {
@@ -309,7 +312,7 @@ __global__ void __launch_bounds__(Cfg<D, kDeep>::kThreads, 1)
       if (walk.more) ahead = page_of(walk.ahead);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        if (!ok || p.begins(i, tpt, chain) == p.s1) continue;
+        if (!ok || (kDeep && i != warp / 4) || p.begins(i, tpt, chain) == p.s1) continue;
         const int k0 = p.m * kPair + i * kT;
         const int id = __shfl_sync(0xffffffffu, now, (i * ppt + (c < ppt ? c : 0)) & 31);
         const bool mine = c < ppt && k0 + c * box < p.x.total;
@@ -328,7 +331,7 @@ __global__ void __launch_bounds__(Cfg<D, kDeep>::kThreads, 1)
       }
       // The rows: boxes of q_box tokens and 64 columns, one a lane.  A box may reach into
       // another request's rows; their columns are passed over.
-      for (int s = p.s0; ok && p.fresh && s < p.s1; ++s) {
+      for (int s = p.s0; ok && warp == 0 && p.fresh && s < p.s1; ++s) {
         const int sl = rows % C::kRows;
         ok = wwait(bar(C::kBarQEmpty + sl), ((rows / C::kRows) & 1) ^ 1);
         if (!ok) break;
@@ -514,11 +517,11 @@ __global__ void __launch_bounds__(Cfg<D, kDeep>::kThreads, 1)
       }
       some = more;
     }
-  } else {
+  } else if (warp >= C::kCtl) {
     // -------------------------------------------------------------- the sums
     // Deep: a warpgroup a key tile.  Else the warpgroups take the steps by turns, both key
     // tiles of each, and add up their sums at the piece's end.
-    const int group = (warp - 4) >> 2;
+    const int group = (warp - C::kCtl) >> 2;
     const int row = (warp & 3) * 32 + lane;  // TMEM lane, key of the tile
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     uint32_t rows = 0, used = 0, made1 = 0;  // made1: all products of key tile 1

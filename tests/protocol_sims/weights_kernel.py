@@ -2,7 +2,7 @@
 
 A piece has `steps` tiles of rows and two key tiles, key tile i being needed from
 step begins[i] on (begins[i] == steps: not at all).  One warp loads the needed key
-tiles into a ring for each i, and the tiles of rows; one their normalisers into a ring
+tiles into a ring for each i, and the tiles of rows (deep: a warp for each i); one their normalisers into a ring
 of the same length and, a piece ahead, what the warpgroups need to know of each piece
 into a ring of four.  A warp for each key tile issues its products, which take two places
 by turns; the last of a piece frees the key tile, those of a step by both warps the rows.
@@ -72,17 +72,17 @@ def run(pieces, seed, mutation=0, depth=2, rows=2, deep=False):
         e.bar(f"XFull{i}", groups)
         e.bar(f"XEmpty{i}", 2)
 
-    def load():
+    def load(tiles, with_rows):
         n, q = [0, 0], 0
         for k, (steps, begins, fresh, _) in enumerate(work):
-            for i in range(2):
+            for i in tiles:
                 if begins[i] < steps:
                     s, phase = place_of(i, n[i])
                     yield ("wait", f"KEmpty{s}", phase ^ 1)
                     e.bars[f"KFull{s}"].arrive(1, 1)
                     e.load(f"k{s}", ("K", k, i), f"KFull{s}")
                     n[i] += 1
-            for _ in range(steps if fresh else 0):
+            for _ in range(steps if fresh and with_rows else 0):
                 yield ("wait", f"QEmpty{q % rows}", ((q // rows) & 1) ^ 1)
                 e.bars[f"QFull{q % rows}"].arrive(1, 1)
                 e.load(f"q{q % rows}", ("Q", q), f"QFull{q % rows}")
@@ -193,7 +193,8 @@ def run(pieces, seed, mutation=0, depth=2, rows=2, deep=False):
             if mutation != 9:
                 e.bars[f"PEmpty{k % 4}"].arrive()
 
-    e.roles = {"load": load(), "l": normalisers(), "mma0": mma(0), "mma1": mma(1)}
+    loads = {"load0": load([0], True), "load1": load([1], False)} if deep else {"load": load([0, 1], True)}
+    e.roles = {**loads, "l": normalisers(), "mma0": mma(0), "mma1": mma(1)}
     for group in range(groups):
         e.roles[f"sum{group}"] = sums(group)
     e.run()
