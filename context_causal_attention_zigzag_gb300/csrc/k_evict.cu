@@ -44,6 +44,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kRun = 16384;  // scores of a CTA's run in shared memory
 constexpr int kMaxCluster = 8;
+constexpr int kAllLongest = 2048;
 
 struct Shared {
   uint32_t run[kRun];
@@ -100,13 +101,187 @@ __device__ __forceinline__ int warps_before(int x, int* part, int& tot) {
   return __shfl_sync(0xffffffffu, upto - mine, warp);
 }
 
+// Runs `chunk`, chunk + chunks, .. of `pairs` (at most 32) of the item's lists, by this warp: a
+// lane looks up a pair's pages and moves its weight, the warp copies the rows.
+template <int D>
+__device__ __forceinline__ void fill_places(const EvictArgs& a, int item, int fills, int pairs,
+                                            int chunk, int chunks) {
+  constexpr int kLanes = D / 4;       // of a pair of rows, 16 bytes each
+  constexpr int kRows = 32 / kLanes;  // of a warp at a time
+  constexpr int U = 8 / kRows;        // turns whose loads are in flight
+  const int lane = threadIdx.x & 31, r = item / a.Hkv, g = item % a.Hkv, P = a.cache.page_size;
+  const int* table = a.table + (int64_t)r * a.table_stride;
+  const int sub = lane / kLanes, l = lane % kLanes;
+  // The first half of a pair's lanes copies the key, the second the value.
+  uint16_t* base = static_cast<uint16_t*>(l < kLanes / 2 ? a.k_cache : a.v_cache) +
+                   g * a.cache.head_stride + l % (kLanes / 2) * 8;
+  const int* to = a.lists + 2 * (int64_t)item * a.list_cap;
+  const int* from = to + a.list_cap;
+  for (int h0 = chunk * pairs; h0 < fills; h0 += chunks * pairs) {
+    const int n = min(pairs, fills - h0);
+    int64_t src = 0, dst = 0;
+    if (lane < n) {
+      const int x = from[h0 + lane], y = to[h0 + lane];
+      const int px = table[x / P], py = table[y / P];
+      a.kept[(int64_t)item * a.most + y] = x;
+      a.weights[((int64_t)py * a.Hkv + g) * P + y % P] =
+          a.weights[((int64_t)px * a.Hkv + g) * P + x % P];
+      src = px * a.cache.page_stride + x % P * a.cache.token_stride;
+      dst = py * a.cache.page_stride + y % P * a.cache.token_stride;
+    }
+    for (int j0 = 0; j0 < n; j0 += U * kRows) {
+      uint4 v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int j = j0 + u * kRows + sub;
+        const int64_t at = __shfl_sync(0xffffffffu, src, j & 31);
+        if (j < n) v[u] = *reinterpret_cast<const uint4*>(base + at);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int j = j0 + u * kRows + sub;
+        const int64_t at = __shfl_sync(0xffffffffu, dst, j & 31);
+        if (j < n) *reinterpret_cast<uint4*>(base + at) = v[u];
+      }
+    }
+  }
+}
+
+// Vectors [vec0, vec0 + vecs) of 16 bytes of the last rows (key and value side by side; vecs a
+// power of two) to the cut, a wave of rows at a time; vector 0 brings their weights.
+template <int kCta>
+__device__ __forceinline__ void shift_rows(const EvictArgs& a, int item, const Plan& p, int vec0,
+                                           int vecs) {
+  constexpr int U = 4;
+  const int r = item / a.Hkv, g = item % a.Hkv, P = a.cache.page_size;
+  const int* table = a.table + (int64_t)r * a.table_stride;
+  const int by = p.c - p.keep, tid = threadIdx.x, rows = kCta / vecs;
+  const int vec = vec0 + tid % vecs, half = a.D / 8;
+  uint16_t* base = static_cast<uint16_t*>(vec < half ? a.k_cache : a.v_cache) +
+                   g * a.cache.head_stride + vec % half * 8;
+  auto at = [&](int pos) {
+    return base + table[pos / P] * a.cache.page_stride + pos % P * a.cache.token_stride;
+  };
+  auto weight = [&](int pos) {
+    return a.weights + ((int64_t)table[pos / P] * a.Hkv + g) * P + pos % P;
+  };
+  for (int w0 = p.cut; w0 < p.keep; w0 += U * rows) {
+    uint4 v[U];
+    float x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int pos = w0 + u * rows + tid / vecs;
+      if (pos < p.keep) {
+        v[u] = *reinterpret_cast<const uint4*>(at(pos + by));
+        if (vec == 0) x[u] = *weight(pos + by);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int pos = w0 + u * rows + tid / vecs;
+      if (pos < p.keep) {
+        *reinterpret_cast<uint4*>(at(pos)) = v[u];
+        if (vec == 0) *weight(pos) = x[u];
+      }
+    }
+  }
+}
+
+// Whether a request's pages can be used, where its positions are brought down.
+__device__ __forceinline__ bool pages_ok(const EvictArgs& a, int r, const Plan& p) {
+  const int* table = a.table + (int64_t)r * a.table_stride;
+  const int n = (p.c + a.cache.page_size - 1) / a.cache.page_size;
+  bool ok = true;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) ok &= table[i] >= 0 && table[i] < a.cache.num_pages;
+  return ok;
+}
+
+// The pages that became free, in request order: each of `blocks` blocks sums the requests and
+// fills its share of the list.  new_lens: nullptr where they are not written yet.
+constexpr int kShiftThreads = 512;
+
+template <int kCta>
+__device__ __forceinline__ void list_freed(const EvictArgs& a, int block, int blocks,
+                                           const int* new_lens) {
+  __shared__ int part[kCta / 32];
+  __shared__ int pre[kCta], have[kCta];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, P = a.cache.page_size;
+  long long done = 0;  // pages of the requests before
+  const long long stride = (long long)blocks * kCta;
+  const long long mine = (long long)block * kCta + tid;
+  for (int r0 = 0; r0 < a.R; r0 += kCta) {
+    const int r = r0 + tid;
+    int first = 0, n = 0;
+    if (r < a.R) {
+      const int c = a.ctx[r];
+      int k = c;
+      if (new_lens != nullptr) {
+        k = new_lens[r];
+      } else {
+        Plan p;
+        if (plan_of(a, r, p) && p.keep < p.c && pages_ok(a, r, p)) k = p.keep;
+      }
+      first = (k + P - 1) / P;
+      n = k < c ? (c + P - 1) / P - first : 0;
+    }
+    int sum = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, sum, d);
+      if (lane >= d) sum += u;
+    }
+    if (lane == 31) part[warp] = sum;
+    __syncthreads();
+    int before = 0, total = 0;
+    for (int w = 0; w < kCta / 32; ++w) {
+      if (w == warp) before = total;
+      total += part[w];
+    }
+    pre[tid] = before + sum - n;
+    have[tid] = first;
+    __syncthreads();
+    const long long end = done + total < a.num_freed_max ? done + total : a.num_freed_max;
+    for (long long x = mine < done ? mine + (done - mine + stride - 1) / stride * stride : mine;
+         x < end; x += stride) {
+      const int y = (int)(x - done);
+      int l = 0, h = kCta;  // the last request that begins at y or before
+      while (h - l > 1) {
+        const int mid = (l + h) / 2;
+        if (pre[mid] <= y)
+          l = mid;
+        else
+          h = mid;
+      }
+      a.freed[x] = a.table[(int64_t)(r0 + l) * a.table_stride + have[l] + (y - pre[l])];
+    }
+    done += total;
+    __syncthreads();
+  }
+  for (long long x = mine < done ? mine + (done - mine + stride - 1) / stride * stride : mine;
+       x < a.num_freed_max; x += stride)
+    a.freed[x] = -1;
+  if (mine == 0) {
+    *a.num_freed = (int)(done < a.num_freed_max ? done : a.num_freed_max);
+    if (done > a.num_freed_max) atomicExch(a.err, kErrBadTables);
+  }
+}
+
+// kAll: a CTA does all for its head; blocks behind those of the heads list the freed pages.
+template <bool kAll>
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs a) {
   extern __shared__ __align__(16) uint8_t raw[];
   Shared& s = *reinterpret_cast<Shared*>(raw);
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-  const int item = blockIdx.x / C, r = item / a.Hkv, g = item % a.Hkv;
   const int tid = threadIdx.x;
+  tc::launch_dependents();
+  if (kAll && blockIdx.x == (unsigned)(a.R * a.Hkv)) {
+    list_freed<kThreads>(a, 0, 1, nullptr);
+    return;
+  }
+  const int item = blockIdx.x / C, r = item / a.Hkv, g = item % a.Hkv;
   const int P = a.cache.page_size;
   const int* table = a.table + (int64_t)r * a.table_stride;
   int* kept = a.kept + ((int64_t)r * a.Hkv + g) * a.most;
@@ -117,8 +292,6 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
     else
       __syncthreads();
   };
-  tc::launch_dependents();
-
   Plan p;
   bool good = plan_of(a, r, p);
   // Every CTA of the request looks at its pages, so that all decide alike.
@@ -293,6 +466,16 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
     late0 += __popc(go);
   }
   if (C > 1) cluster.sync();  // no CTA leaves while another reads its shared memory
+  if constexpr (kAll) {
+    __syncthreads();
+    const int pairs = min(32, max(4, (fills + kWarps - 1) / kWarps));
+    if (a.D == 128)
+      fill_places<128>(a, item, fills, pairs, warp, kWarps);
+    else
+      fill_places<64>(a, item, fills, pairs, warp, kWarps);
+    __syncthreads();  // the fills have read what the shift writes over
+    shift_rows<kThreads>(a, item, p, 0, a.D / 4);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -302,164 +485,30 @@ constexpr int kFillWarps = 4;
 
 template <int D>
 __global__ void __launch_bounds__(kFillWarps * 32) evict_fill_kernel(const EvictArgs a) {
-  constexpr int kLanes = D / 4;          // of a pair of rows, 16 bytes each
-  constexpr int kRows = 32 / kLanes;     // of a warp at a time
-  constexpr int U = 8 / kRows;           // turns whose loads are in flight
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int item = a.item0 + blockIdx.y, r = item / a.Hkv, g = item % a.Hkv;
-  const int P = a.cache.page_size;
-  const int* table = a.table + (int64_t)r * a.table_stride;
-  const int sub = lane / kLanes, l = lane % kLanes;
-  // The first half of a pair's lanes copies the key, the second the value.
-  uint16_t* base = static_cast<uint16_t*>(l < kLanes / 2 ? a.k_cache : a.v_cache) +
-                   g * a.cache.head_stride + l % (kLanes / 2) * 8;
   tc::launch_dependents();
   tc::wait_prior_grid();
-  const int fills = a.fills[item];
-  const int* to = a.lists + 2 * (int64_t)item * a.list_cap;
-  const int* from = to + a.list_cap;
-  for (int h0 = (blockIdx.x * kFillWarps + warp) * 32; h0 < fills;
-       h0 += gridDim.x * kFillWarps * 32) {
-    const int n = min(32, fills - h0);
-    int64_t src = 0, dst = 0;
-    if (lane < n) {
-      const int x = from[h0 + lane], y = to[h0 + lane];
-      const int px = table[x / P], py = table[y / P];
-      a.kept[(int64_t)item * a.most + y] = x;
-      a.weights[((int64_t)py * a.Hkv + g) * P + y % P] =
-          a.weights[((int64_t)px * a.Hkv + g) * P + x % P];
-      src = px * a.cache.page_stride + x % P * a.cache.token_stride;
-      dst = py * a.cache.page_stride + y % P * a.cache.token_stride;
-    }
-    for (int j0 = 0; j0 < n; j0 += U * kRows) {
-      uint4 v[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int j = j0 + u * kRows + sub;
-        const int64_t at = __shfl_sync(0xffffffffu, src, j & 31);
-        if (j < n) v[u] = *reinterpret_cast<const uint4*>(base + at);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int j = j0 + u * kRows + sub;
-        const int64_t at = __shfl_sync(0xffffffffu, dst, j & 31);
-        if (j < n) *reinterpret_cast<uint4*>(base + at) = v[u];
-      }
-    }
-  }
+  const int item = a.item0 + blockIdx.y;
+  fill_places<D>(a, item, a.fills[item], 32, blockIdx.x * kFillWarps + (threadIdx.x >> 5),
+                     gridDim.x * kFillWarps);
 }
 
 // ---------------------------------------------------------------------------
 // Blocks (slice, item): 64 bytes of each of the last rows (slice 0 their weights, too).
-// The blocks behind those list the pages that became free, in request order: each sums
-// the requests and fills its share of the list.
+// The blocks behind those list the pages that became free.
 // ---------------------------------------------------------------------------
-constexpr int kShiftThreads = 512;
-
-__device__ __forceinline__ void list_freed(const EvictArgs& a, int block, int blocks) {
-  __shared__ int part[kShiftThreads / 32];
-  __shared__ int pre[kShiftThreads], have[kShiftThreads];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, P = a.cache.page_size;
-  long long done = 0;  // pages of the requests before
-  const long long stride = (long long)blocks * kShiftThreads;
-  const long long mine = (long long)block * kShiftThreads + tid;
-  for (int r0 = 0; r0 < a.R; r0 += kShiftThreads) {
-    const int r = r0 + tid;
-    int first = 0, n = 0;
-    if (r < a.R) {
-      const int c = a.ctx[r], k = a.new_lens[r];
-      first = (k + P - 1) / P;
-      n = k < c ? (c + P - 1) / P - first : 0;
-    }
-    int sum = n;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, sum, d);
-      if (lane >= d) sum += u;
-    }
-    if (lane == 31) part[warp] = sum;
-    __syncthreads();
-    int before = 0, total = 0;
-    for (int w = 0; w < kShiftThreads / 32; ++w) {
-      if (w == warp) before = total;
-      total += part[w];
-    }
-    pre[tid] = before + sum - n;
-    have[tid] = first;
-    __syncthreads();
-    const long long end = done + total < a.num_freed_max ? done + total : a.num_freed_max;
-    for (long long x = mine < done ? mine + (done - mine + stride - 1) / stride * stride : mine;
-         x < end; x += stride) {
-      const int y = (int)(x - done);
-      int l = 0, h = kShiftThreads;  // the last request that begins at y or before
-      while (h - l > 1) {
-        const int mid = (l + h) / 2;
-        if (pre[mid] <= y)
-          l = mid;
-        else
-          h = mid;
-      }
-      a.freed[x] = a.table[(int64_t)(r0 + l) * a.table_stride + have[l] + (y - pre[l])];
-    }
-    done += total;
-    __syncthreads();
-  }
-  for (long long x = mine < done ? mine + (done - mine + stride - 1) / stride * stride : mine;
-       x < a.num_freed_max; x += stride)
-    a.freed[x] = -1;
-  if (mine == 0) {
-    *a.num_freed = (int)(done < a.num_freed_max ? done : a.num_freed_max);
-    if (done > a.num_freed_max) atomicExch(a.err, kErrBadTables);
-  }
-}
-
 __global__ void __launch_bounds__(kShiftThreads)
     evict_shift_kernel(const EvictArgs a, int slices, int freed_blocks) {
   tc::wait_prior_grid();
   const int64_t shifts = (int64_t)a.R * a.Hkv * slices;
   if (blockIdx.x >= shifts) {
-    list_freed(a, (int)(blockIdx.x - shifts), freed_blocks);
+    list_freed<kShiftThreads>(a, (int)(blockIdx.x - shifts), freed_blocks, a.new_lens);
     return;
   }
   const int item = blockIdx.x / slices, slice = blockIdx.x % slices;
-  const int r = item / a.Hkv, g = item % a.Hkv, P = a.cache.page_size;
   if (a.fills[item] < 0) return;
   Plan p;
-  plan_of(a, r, p);
-  const int by = p.c - p.keep;
-  const int* table = a.table + (int64_t)r * a.table_stride;
-  const int half = slices / 2, tid = threadIdx.x;
-  uint16_t* base = static_cast<uint16_t*>(slice < half ? a.k_cache : a.v_cache) +
-                   g * a.cache.head_stride + slice % half * 32 + tid % 4 * 8;
-  auto at = [&](int pos) {
-    return base + table[pos / P] * a.cache.page_stride + pos % P * a.cache.token_stride;
-  };
-  auto weight = [&](int pos) {
-    return a.weights + ((int64_t)table[pos / P] * a.Hkv + g) * P + pos % P;
-  };
-  const bool weighs = slice == 0 && tid % 4 == 0;
-  constexpr int U = 4, kRows = kShiftThreads / 4;
-  for (int w0 = p.cut; w0 < p.keep; w0 += U * kRows) {
-    uint4 v[U];
-    float x[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int pos = w0 + u * kRows + tid / 4;
-      if (pos < p.keep) {
-        v[u] = *reinterpret_cast<const uint4*>(at(pos + by));
-        if (weighs) x[u] = *weight(pos + by);
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int pos = w0 + u * kRows + tid / 4;
-      if (pos < p.keep) {
-        *reinterpret_cast<uint4*>(at(pos)) = v[u];
-        if (weighs) *weight(pos) = x[u];
-      }
-    }
-  }
+  plan_of(a, item / a.Hkv, p);
+  shift_rows<kShiftThreads>(a, item, p, slice * 4, 4);
 }
 
 // A launch that may begin while the one before it ends.
@@ -487,16 +536,33 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t stream) {
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   static DeviceOnce allowed;
-  e = allowed.shared_memory(reinterpret_cast<const void*>(evict_select_kernel), dev, sizeof(Shared));
+  e = allowed.shared_memory(reinterpret_cast<const void*>(evict_select_kernel<false>), dev, sizeof(Shared));
   if (e != cudaSuccess) return e;
-  const int64_t items = (int64_t)a.R * a.Hkv;
-  const int slices = a.D * 4 / 64;
+  const int64_t items = (int64_t)a.R * a.Hkv, longest = (int64_t)a.width * a.cache.page_size;
   const int freed_blocks = a.num_freed_max / (8 * kShiftThreads) < sms
                                ? a.num_freed_max / (8 * kShiftThreads) + 1
                                : sms;
+  // A CTA a head does all where that is little or the heads fill the SMs.  Measured (us, one
+  // launch / three; 8 heads a request, keys and values of 128):
+  //    1 request, 1000 of 2000 kept:  19 / 19       1 request, 2000 of 4000: 28 / 22
+  //   16 requests, 1000 of 2000:      21 / 31      16 requests, 4000 of 8000: 66 / 84
+  if (items > 0 && longest <= kRun && (longest <= kAllLongest || 2 * items >= sms)) {
+    static DeviceOnce all_allowed;
+    e = all_allowed.shared_memory(reinterpret_cast<const void*>(evict_select_kernel<true>), dev,
+                                  sizeof(Shared));
+    if (e != cudaSuccess) return e;
+    // The block that lists the freed pages looks at the tables itself, if they are few.
+    const bool with_freed = (int64_t)a.R * a.width <= 8192 && a.width <= 128;
+    evict_select_kernel<true>
+        <<<(unsigned)(items + with_freed), kThreads, sizeof(Shared), stream>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || with_freed) return e;
+    return launch_behind(evict_shift_kernel, dim3(freed_blocks), kShiftThreads, stream, a, 0,
+                         freed_blocks);
+  }
+  const int slices = a.D * 4 / 64;
   if (items > 0) {
     // A CTA whose shared memory holds the scores that a request can have, or a cluster.
-    const int64_t longest = (int64_t)a.width * a.cache.page_size;
     int C = 1;
     while (C < kMaxCluster && C * (int64_t)kRun < longest) C *= 2;
     cudaLaunchConfig_t cfg = {};
@@ -511,7 +577,7 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t stream) {
     attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a);
+    e = cudaLaunchKernelEx(&cfg, evict_select_kernel<false>, a);
     if (e != cudaSuccess) return e;
     // Warps for all the pairs that there can be, as far as the SMs can hold them.
     const int64_t pairs = (a.list_cap + kFillWarps * 32 - 1) / (kFillWarps * 32);
