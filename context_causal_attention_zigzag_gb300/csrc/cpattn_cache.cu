@@ -292,7 +292,7 @@ int cpattn_cache_evict(float* weights, const float* scores, void* k_cache, void*
     return CPATTN_ERR_WORKSPACE;
   int* err = device_error_word();
   if (err == nullptr) return CPATTN_ERR_CUDA;
-  EvictArgs a;
+  EvictArgs a = {PageDiv(page_size)};
   a.weights = weights;
   a.scores = scores ? scores : weights;
   a.k_cache = k_cache;

@@ -313,6 +313,23 @@ struct CacheShape {
   int64_t page_stride, token_stride, head_stride;
 };
 
+// Pages and places of positions below 2^26 without a division: a page size is 2^s k with k at
+// most 8, and (p >> s) / k = (p >> s) * ceil(2^32 / k) >> 32 is exact there.
+struct PageDiv {
+  int size, s;
+  uint32_t magic;  // 0: k = 1
+  __host__ __device__ explicit PageDiv(int page_size) : size(page_size), s(0), magic(0) {
+    while (s < 7 && !(page_size >> s & 1)) ++s;
+    const uint32_t k = (uint32_t)page_size >> s;
+    if (k > 1) magic = (uint32_t)((((uint64_t)1 << 32) + k - 1) / k);
+  }
+  __host__ __device__ int page(int p) const {
+    const uint32_t q = (uint32_t)p >> s;
+    return (int)(magic ? (uint32_t)(((uint64_t)q * magic) >> 32) : q);
+  }
+  __host__ __device__ int place(int p, int page) const { return p - page * size; }
+};
+
 struct TablesArgs {
   const int* ctx;
   const int* fresh;  // new tokens of each request
@@ -529,6 +546,7 @@ cudaError_t launch_tc_weights(const WeightsArgs& a, int dtype, int dev, int sms,
 cudaError_t launch_cache_weights(const WeightsArgs& a, int dtype, cudaStream_t stream);
 
 struct EvictArgs {
+  PageDiv pages;
   float* weights;
   const float* scores;
   void* k_cache;

@@ -110,6 +110,7 @@ __device__ __forceinline__ void fill_places(const EvictArgs& a, int item, int fi
   constexpr int kRows = 32 / kLanes;  // of a warp at a time
   constexpr int U = 8 / kRows;        // turns whose loads are in flight
   const int lane = threadIdx.x & 31, r = item / a.Hkv, g = item % a.Hkv, P = a.cache.page_size;
+  const PageDiv div = a.pages;
   const int* table = a.table + (int64_t)r * a.table_stride;
   const int sub = lane / kLanes, l = lane % kLanes;
   // The first half of a pair's lanes copies the key, the second the value.
@@ -122,12 +123,13 @@ __device__ __forceinline__ void fill_places(const EvictArgs& a, int item, int fi
     int64_t src = 0, dst = 0;
     if (lane < n) {
       const int x = from[h0 + lane], y = to[h0 + lane];
-      const int px = table[x / P], py = table[y / P];
+      const int ix = div.page(x), iy = div.page(y), ox = div.place(x, ix), oy = div.place(y, iy);
+      const int px = table[ix], py = table[iy];
       a.kept[(int64_t)item * a.most + y] = x;
-      a.weights[((int64_t)py * a.Hkv + g) * P + y % P] =
-          a.weights[((int64_t)px * a.Hkv + g) * P + x % P];
-      src = px * a.cache.page_stride + x % P * a.cache.token_stride;
-      dst = py * a.cache.page_stride + y % P * a.cache.token_stride;
+      a.weights[((int64_t)py * a.Hkv + g) * P + oy] =
+          a.weights[((int64_t)px * a.Hkv + g) * P + ox];
+      src = px * a.cache.page_stride + ox * a.cache.token_stride;
+      dst = py * a.cache.page_stride + oy * a.cache.token_stride;
     }
     for (int j0 = 0; j0 < n; j0 += U * kRows) {
       uint4 v[U];
@@ -159,12 +161,7 @@ __device__ __forceinline__ void shift_rows(const EvictArgs& a, int item, const P
   const int vec = vec0 + tid % vecs, half = a.D / 8;
   uint16_t* base = static_cast<uint16_t*>(vec < half ? a.k_cache : a.v_cache) +
                    g * a.cache.head_stride + vec % half * 8;
-  auto at = [&](int pos) {
-    return base + table[pos / P] * a.cache.page_stride + pos % P * a.cache.token_stride;
-  };
-  auto weight = [&](int pos) {
-    return a.weights + ((int64_t)table[pos / P] * a.Hkv + g) * P + pos % P;
-  };
+  const PageDiv div = a.pages;
   for (int w0 = p.cut; w0 < p.keep; w0 += U * rows) {
     uint4 v[U];
     float x[U];
@@ -172,8 +169,10 @@ __device__ __forceinline__ void shift_rows(const EvictArgs& a, int item, const P
     for (int u = 0; u < U; ++u) {
       const int pos = w0 + u * rows + tid / vecs;
       if (pos < p.keep) {
-        v[u] = *reinterpret_cast<const uint4*>(at(pos + by));
-        if (vec == 0) x[u] = *weight(pos + by);
+        const int i = div.page(pos + by), o = div.place(pos + by, i), page = table[i];
+        v[u] = *reinterpret_cast<const uint4*>(base + page * a.cache.page_stride +
+                                               o * a.cache.token_stride);
+        if (vec == 0) x[u] = a.weights[((int64_t)page * a.Hkv + g) * P + o];
       }
     }
     __syncthreads();
@@ -181,8 +180,10 @@ __device__ __forceinline__ void shift_rows(const EvictArgs& a, int item, const P
     for (int u = 0; u < U; ++u) {
       const int pos = w0 + u * rows + tid / vecs;
       if (pos < p.keep) {
-        *reinterpret_cast<uint4*>(at(pos)) = v[u];
-        if (vec == 0) *weight(pos) = x[u];
+        const int i = div.page(pos), o = div.place(pos, i), page = table[i];
+        *reinterpret_cast<uint4*>(base + page * a.cache.page_stride + o * a.cache.token_stride) =
+            v[u];
+        if (vec == 0) a.weights[((int64_t)page * a.Hkv + g) * P + o] = x[u];
       }
     }
   }
@@ -322,9 +323,10 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
   const int per = (M + C - 1) / C;
   const int lo = p.f + min(M, rank * per), n = p.f + min(M, (rank + 1) * per) - lo;
   const bool held = per <= kRun;
+  const PageDiv div = a.pages;
   auto score = [&](int pos) {
-    const int page = table[pos / P];
-    return ordered(a.scores[((int64_t)page * a.Hkv + g) * P + pos % P]);
+    const int i = div.page(pos);
+    return ordered(a.scores[((int64_t)table[i] * a.Hkv + g) * P + div.place(pos, i)]);
   };
   auto key_of = [&](int i) { return held ? s.run[i] : score(lo + i); };
   if (held) {
