@@ -779,11 +779,26 @@ def _cache_args(k_cache, v_cache, Hkv, D, dtype, device):
     return shape[0], shape[1], strides[0], strides[1], strides[2]
 
 
+_short_calls = {}
+
+
+def _short_call(name):
+    """The entry point with every integer taken as c_void_p: ctypes hands a Python int
+    on as it is then (27 arguments take 2.3 us; as c_int and c_int64 6.1 us).  Both
+    calling conventions give an int the slot or register of a pointer, of which it is the
+    low half."""
+    res, args = SIGNATURES[name]
+    fn = lib()[name]  # a function object of its own
+    fn.restype, fn.argtypes = res, [t if t in (_f, _d) else _vp for t in args]
+    _short_calls[name] = fn
+    return fn
+
+
 def _launch(name, device, *args):
     """Calls the library on `device`'s current stream.  These calls are short
     enough for their way through Python to count: pointers go as plain numbers,
     and the device is switched only if it has to be."""
-    fn, index = getattr(_lib or lib(), name), device.index
+    fn, index = _short_calls.get(name) or _short_call(name), device.index
     if torch._C._cuda_getDevice() == index:
         rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
