@@ -340,6 +340,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
   // begin alike.
   uint32_t found = 0;
   int left = m, shift = 32;
+  bool plain = true;  // all that begin like `found` stay
   if (m > 0) {
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
@@ -392,9 +393,9 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
       for (int i = tid; i < kBins; i += kThreads) s.count[i] = 0;
       found = found << bits | (uint32_t)s.pick[0];
       left = s.pick[1];
-      const bool enough = s.pick[2];
+      plain = s.pick[2];
       together();  // before the next digit is picked
-      if (enough) break;  // all that begin alike stay
+      if (plain) break;
     }
   }
   // Of those whose leading bits equal `found` the first `left` stay: which of them are in this
@@ -404,20 +405,24 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
   const int chunk = (n + kThreads - 1) / kThreads * 32;
   const int i0 = min(n, warp * chunk), i1 = min(n, i0 + chunk);
   auto lead_of = [&](int i) { return shift < 32 ? key_of(i) >> shift : 0u; };
-  int equal = 0;
-  for (int i = i0; i < i1; i += 32)
-    equal += __popc(__ballot_sync(0xffffffffu, m > 0 && i + lane < i1 && lead_of(i + lane) == found));
-  int mine_equal, quota = left;
-  const int equal0 = warps_before(equal, s.warp[3], mine_equal);
-  if (C > 1) {
-    if (tid == 0) s.meet[0] = mine_equal;
-    cluster.sync();
-    for (int c = 0; c < rank; ++c) quota -= *cluster.map_shared_rank(&s.meet[0], c);
+  int equal0 = 0, quota = INT_MAX;
+  if (!plain) {
+    int equal = 0, mine_equal;
+    for (int i = i0; i < i1; i += 32)
+      equal += __popc(__ballot_sync(0xffffffffu, i + lane < i1 && lead_of(i + lane) == found));
+    equal0 = warps_before(equal, s.warp[3], mine_equal);
+    quota = left;
+    if (C > 1) {
+      if (tid == 0) s.meet[0] = mine_equal;
+      cluster.sync();
+      for (int c = 0; c < rank; ++c) quota -= *cluster.map_shared_rank(&s.meet[0], c);
+    }
   }
   // Whether the warp's 32 positions from i on stay, as bits.
   auto stays = [&](int i, int& seen) {
     const bool on = m > 0 && i + lane < i1;
     const uint32_t k = on ? lead_of(i + lane) : 0;
+    if (plain) return __ballot_sync(0xffffffffu, on && k >= found);
     const unsigned same = __ballot_sync(0xffffffffu, on && k == found);
     const bool stay = on && (k > found || (k == found && seen + __popc(same & below) < quota));
     seen += __popc(same);
@@ -432,6 +437,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
   int holes = 0, late = 0, seen = equal0;
   for (int i = i0; i < i1; i += 32) {
     const unsigned stay = stays(i, seen), early = early_of(i);
+    if (held) s.count[i >> 5] = (int)stay;  // (the counts of digits are no longer needed)
     holes += __popc(early & ~stay);
     late += __popc(stay & ~early);
   }
@@ -460,7 +466,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
   int* from = to + a.list_cap;
   seen = equal0;
   for (int i = i0; i < i1; i += 32) {
-    const unsigned stay = stays(i, seen), early = early_of(i);
+    const unsigned stay = held ? (unsigned)s.count[i >> 5] : stays(i, seen), early = early_of(i);
     const unsigned free_ = early & ~stay, go = stay & ~early;
     if (free_ >> lane & 1) to[hole0 + __popc(free_ & below)] = lo + i + lane;
     if (go >> lane & 1) from[late0 + __popc(go & below)] = lo + i + lane;
