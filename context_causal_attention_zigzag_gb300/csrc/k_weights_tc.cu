@@ -73,9 +73,9 @@ struct Cfg {
   static constexpr int kThreads = 32 * kCtl + kHands;
   static constexpr int kHalves = D / 64;
   static constexpr int kTileBytes = kHalves * kBoxBytes;
-  static constexpr int kDepth = kDeep ? (D == 128 ? 3 : 6) : 2;  // of a key tile's ring
+  static constexpr int kDepth = kDeep ? (D == 128 ? 3 : 6) : (D == 128 ? 1 : 2);  // of a key tile's ring
   static constexpr int kKeys = 2 * kDepth;
-  static constexpr int kRows = kDeep ? 1 : (D == 128 ? 2 : 8);
+  static constexpr int kRows = kDeep ? 1 : (D == 128 ? 4 : 8);
   // Of normalisers: more than the warpgroups that take the steps by turns, so that none waits
   // for a place of which it has not seen the phase before.
   static constexpr int kNorms = kRows < 4 ? 4 : kRows;

@@ -155,7 +155,7 @@ def test_pieces_cover_every_step_once(tmp_path):
 
 PIECES = [(1, 0, 0, True), (1, 0, 0, False), (1, 0, 1, True), (2, 0, 0, False), (4, 0, 2, False), (5, 0, 5, False),
           (3, 0, 1, False), (2, 0, 2, False)]
-RINGS = [dict(), dict(rows=8), dict(depth=3, rows=1, deep=True), dict(depth=6, rows=1, deep=True)]
+RINGS = [dict(depth=1, rows=4), dict(rows=8), dict(depth=3, rows=1, deep=True), dict(depth=6, rows=1, deep=True)]
 
 
 def draws(n, seed):
