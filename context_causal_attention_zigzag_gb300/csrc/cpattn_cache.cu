@@ -35,6 +35,32 @@ bool rows_meet(const void* pa, Bytes sa, Bytes na, Bytes wa, const void* pb, Byt
   return d < wb || d + wa > sa;
 }
 
+// A stretch of memory.
+struct Stretch {
+  const void* p;
+  Bytes n;
+};
+// Whether one that is written meets another, or one that is read.  Kernels read lengths, tables
+// and lists again, and go by what they found the first time: another value there could lead
+// them out of the cache.
+template <int kW, int kR>
+bool any_meet(const Stretch (&written)[kW], const Stretch (&read)[kR]) {
+  auto meet = [](const Stretch& x, const Stretch& y) {
+    return rows_meet(x.p, x.n, x.n > 0, x.n, y.p, y.n, y.n > 0, y.n);
+  };
+  for (int i = 0; i < kW; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (meet(written[i], written[j])) return true;
+    for (int j = 0; j < kR; ++j)
+      if (meet(written[i], read[j])) return true;
+  }
+  return false;
+}
+// From a table's first byte to its last.
+Stretch table_stretch(const int32_t* table, int R, int width, int64_t stride) {
+  return {table, R > 0 && width > 0 ? 4 * ((Bytes)(R - 1) * stride + width) : 0};
+}
+
 // From a cache's first byte to its last.
 Bytes cache_bytes(const CacheShape& c, int Hkv, int D) {
   return 2 * ((Bytes)(c.num_pages - 1) * c.page_stride +
@@ -198,14 +224,20 @@ int cpattn_cache_weights(const void* q, int64_t q_stride, const void* k_cache, i
       !aligned(block_table, 4) || !aligned(ctx_lens, 4) || !aligned(cu_new, 4) ||
       !aligned(tree, 8))
     return CPATTN_ERR_INVALID_ARG;
-  const Bytes ww = 4 * (Bytes)num_pages * Hkv * page_size, wc = cache_bytes(c, Hkv, D);
-  if (rows_meet(weights, ww, 1, ww, k_cache, wc, 1, wc) ||
-      rows_meet(weights, ww, 1, ww, q, 2 * q_stride, N, 2 * (int64_t)H * D) ||
-      rows_meet(weights, ww, 1, ww, lse, 4 * (Bytes)H * N, 1, 4 * (Bytes)H * N))
-    return CPATTN_ERR_INVALID_ARG;
-  if (!workspace || !aligned(workspace, 256) ||
-      workspace_bytes < weights_workspace_bytes())
+  const Stretch written[] = {{weights, 4 * (Bytes)num_pages * Hkv * page_size}};
+  const Stretch read[] = {{k_cache, cache_bytes(c, Hkv, D)},
+                          {q, 2 * ((Bytes)(N - 1) * q_stride + (Bytes)H * D)},
+                          {lse, 4 * (Bytes)H * N},
+                          {ctx_lens, 4 * (Bytes)R},
+                          {cu_new, 4 * ((Bytes)R + 1)},
+                          {tree, tree ? 8 * (Bytes)N : 0},
+                          table_stretch(block_table, R, table_width, table_stride)};
+  if (any_meet(written, read)) return CPATTN_ERR_INVALID_ARG;
+  const size_t need = weights_workspace_bytes();
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < need)
     return CPATTN_ERR_WORKSPACE;
+  const Stretch both[] = {written[0], {workspace, (Bytes)need}};
+  if (any_meet(both, read)) return CPATTN_ERR_INVALID_ARG;
   int* err = device_error_word();
   if (err == nullptr) return CPATTN_ERR_CUDA;
   WeightsArgs w;
@@ -279,17 +311,30 @@ int cpattn_cache_evict(float* weights, const float* scores, void* k_cache, void*
                 !aligned(ctx_lens, 4) || !keep || !aligned(keep, 4) || !new_lens ||
                 !aligned(new_lens, 4) || !kept || !aligned(kept, 4)))
     return CPATTN_ERR_INVALID_ARG;
-  // Other CTAs still read the lengths when the new ones are written.
-  const int64_t rb = 4 * (int64_t)R;
-  if (R > 0 && (rows_meet(new_lens, rb, 1, rb, ctx_lens, rb, 1, rb) ||
-                rows_meet(new_lens, rb, 1, rb, keep, rb, 1, rb)))
-    return CPATTN_ERR_INVALID_ARG;
-  const Bytes ww = 4 * (Bytes)num_pages * Hkv * page_size;
-  if (R > 0 && scores && scores != weights && rows_meet(scores, ww, 1, ww, weights, ww, 1, ww))
-    return CPATTN_ERR_INVALID_ARG;
   const size_t need = cpattn_cache_evict_workspace_bytes(R, Hkv, table_width, page_size, most);
+  const Bytes rows = 4 * (Bytes)R, wc = R > 0 ? cache_bytes(c, Hkv, D) : 0,
+              ww = R > 0 ? 4 * (Bytes)num_pages * Hkv * page_size : 0;
+  // (Keys and values may lie side by side in one tensor.)
+  const Stretch caches[] = {{k_cache, wc}, {v_cache, wc}};
+  const Stretch written[] = {{weights, ww},
+                             {new_lens, rows},
+                             {kept, rows * Hkv * most},
+                             {freed, 4 * (Bytes)num_freed_max},
+                             {num_freed, 4}};
+  const Stretch read[] = {{ctx_lens, rows},
+                          {keep, rows},
+                          {scores != weights ? scores : nullptr, scores != weights && scores ? ww : 0},
+                          table_stretch(block_table, R, table_width, table_stride)};
+  if (any_meet(written, read) || any_meet(written, caches)) return CPATTN_ERR_INVALID_ARG;
+  for (const Stretch& x : caches) {
+    const Stretch one[] = {x};
+    if (any_meet(one, read)) return CPATTN_ERR_INVALID_ARG;
+  }
   if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need))
     return CPATTN_ERR_WORKSPACE;
+  const Stretch scratch[] = {{workspace, (Bytes)need}};
+  if (any_meet(scratch, read) || any_meet(scratch, written) || any_meet(scratch, caches))
+    return CPATTN_ERR_INVALID_ARG;
   int* err = device_error_word();
   if (err == nullptr) return CPATTN_ERR_CUDA;
   EvictArgs a = {PageDiv(page_size)};

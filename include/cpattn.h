@@ -666,9 +666,8 @@ CPATTN_API int cpattn_prompt_attn(const void* q, int64_t q_stride, const void* k
                                   cpattn_stream_t stream);
 
 /*
- * Rotary positions.  The pages' models give attention its positions before the
- * ring; these calls turn q and k (and their gradients) where the ring and the
- * cache hold them.
+ * Rotary positions: q and k (and their gradients) turned on their way into and
+ * out of the ring, and on their way into the cache.
  *
  * Of each head's D values the first `rot` are pairs, pair i being the values
  * (i, i + rot / 2), or (2 i, 2 i + 1) with interleaved = 1; the others pass.
@@ -803,7 +802,8 @@ CPATTN_API int cpattn_cache_weights(const void* q, int64_t q_stride, const void*
  * two requests of the call.
  *   first, recent >= 0; most 1 to 2^26; R and Hkv at most 65535, R * Hkv at
  *   most 2^24, R * Hkv * most below 2^40; the cache as above, dtype CPATTN_BF16
- *   or CPATTN_F16.
+ *   or CPATTN_F16.  What is written, the workspace too, overlaps nothing else
+ *   (the keys and values may lie in one tensor).
  * workspace: device, at least cpattn_cache_evict_workspace_bytes, 256-byte
  * aligned, scratch.
  */

@@ -134,3 +134,23 @@ def test_frequencies():
 def test_frequencies_refuse(args):
     with pytest.raises(cp_attn.CpattnError):
         cp_attn.rotary_frequencies(*args, device="cpu")
+
+
+# What is written (weights 1024 bytes, a cache 32768, lists of tens of bytes) at the end of, within or around
+# something else.
+@pytest.mark.parametrize("changes", [
+    dict(w=at(0x7ffffc)), dict(w=at(0x807ffc)), dict(w=at(0x400600)), dict(w=at(0x1000)), dict(w=at(0xffc)),
+    dict(tree=at(0x500018)), dict(w=at(0x10f000), ws=at(0x100000)), dict(ws=at(0x800000)), dict(ws=at(0x400000))])
+def test_cache_weights_refuses_overlaps(changes):
+    apart = dict(table=at(0x1000), ctx=at(0x1100), cu=at(0x1200), tree=at(0x1300), ws=at(0x100000))
+    assert call("cpattn_cache_weights", WEIGHTS, **dict(apart, **changes)) == E
+
+
+@pytest.mark.parametrize("changes", [
+    dict(new=at(0x4000)), dict(kept=at(0x1f9c)), dict(kept=at(0x5000)), dict(freed=at(0x1004)), dict(freed=at(0x7014)),
+    dict(count=at(0x4010)), dict(count=at(0x701c)), dict(w=at(0x7000)), dict(w=at(0x800000)), dict(sc=at(0x4ffc04)),
+    dict(kept=at(0x807fe0)), dict(new=at(0x900000)), dict(table=at(0x800100)), dict(keep=at(0x907ff8)),
+    dict(ws=at(0x4000)), dict(ws=at(0x1000)), dict(ws=at(0x500300)), dict(ws=at(0x900000)), dict(sc=at(0x900000))])
+def test_cache_evict_refuses_overlaps(changes):
+    apart = dict(table=at(0x7000), ws=at(0x100000))
+    assert call("cpattn_cache_evict", EVICT, **dict(apart, **changes)) == E
