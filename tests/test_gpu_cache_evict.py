@@ -283,3 +283,29 @@ def test_graph_replays_see_new_lengths():
         want = reference(state[2], state[2], state[0], state[1], table, ctx, keep, 2, 10, 150, table.numel())
         for x, y in zip((k, v, w) + tuple(outputs), want):
             assert same(x, y)
+
+
+@pytest.mark.parametrize("R,Hkv,longest", [(20, 8, 3000), (70, 3, 2100)])
+def test_wide_tables_in_one_launch_and_their_freed_pages(R, Hkv, longest):
+    rng = random.Random(R)
+    ctx = [longest] + [rng.randrange(longest) for _ in range(R - 1)]
+    run(ctx, [rng.randrange(c + 20) for c in ctx], 4, 32, Hkv, 64, 16, "fp16", seed=R)
+
+
+def test_two_calls_at_once():
+    calls = []
+    for i in range(2):
+        ctx, keep = [5000 + i, 800, 20000], [2000, 100 + i, 700]
+        k, v, w, table = make(ctx, 4, 64, 32, "bf16", seed=i)
+        want = reference(w, w, k, v, table, ctx, keep, 4, 60, 2000, table.numel())
+        calls.append((torch.cuda.Stream(), (w, k, v, table, ints(ctx), ints(keep), 2000), want))
+    torch.cuda.synchronize()
+    got = []
+    for s, args, _ in calls:
+        with torch.cuda.stream(s):
+            got.append(cpa.cache_evict(*args, first=4, recent=60))
+    torch.cuda.synchronize()
+    assert cpa.device_status() == 0
+    for (_, (w, k, v, *_), want), out in zip(calls, got):
+        for x, y in zip((k, v, w) + out, want):
+            assert same(x, y)

@@ -238,3 +238,36 @@ def test_other_streams_and_graphs():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, cpa.rotary(x, f, at))
+
+
+@pytest.mark.parametrize("B,S_nat,S,H,Hkv,D,rot,cp,own", [(2, 90, 96, 4, 2, 64, 64, 4, False), (1, 61, 64, 2, 1, 128, 96, 2, True)])
+def test_training_through_the_ring(B, S_nat, S, H, Hkv, D, rot, cp, own):
+    """q and k turned into the ring's order, attention and its gradient there, the gradients turned back out,
+    against the formula in 64 bits.  The ring's float32 results are held to 1e-4; inputs off by 2^-21 |x| (above)
+    move scores by 2^-21 |q| |k| / sqrt(D), about 2^-21 sqrt(D) = 6e-6, and results by a few times that."""
+    q, k, v, do = (normal(20 + i, B, S_nat, n, D) for i, n in enumerate((H, Hkv, Hkv, H)))
+    freqs = frequencies(rot)
+    at = torch.arange(S_nat, device=DEV, dtype=torch.int32).repeat(B, 1)
+    if own:  # a second document's positions begin anew
+        at[:, S_nat // 2:] -= S_nat // 2
+    into, back = dict(cp=cp, to_sharded=True, length=S), dict(cp=cp, from_sharded=True, length=S_nat)
+    qs, ks = cpa.rotary(q, freqs, at, **into), cpa.rotary(k, freqs, at, **into)
+    vs, dos = cpa.zigzag_permute_pad(v, cp, S), cpa.zigzag_permute_pad(do, cp, S)
+    o, lse = cpa.ring_fwd(qs, ks, vs, cp)
+    dq, dk, dv = cpa.ring_bwd(qs, ks, vs, o, dos, lse, cp)
+    got = (cpa.zigzag_unpermute(o, cp)[:, :S_nat], cpa.rotary_bwd(dq, freqs, at, **back),
+           cpa.rotary_bwd(dk, freqs, at, **back), cpa.zigzag_unpermute(dv, cp)[:, :S_nat])
+    x = [t.double().requires_grad_() for t in (q, k, v)]
+    angle = (at.double()[..., None] * freqs)[:, :, None]
+
+    def turn(t):
+        a, b, rest = t.split([rot // 2, rot // 2, D - rot], -1)
+        c, s = angle.cos(), angle.sin()
+        return torch.cat([a * c - b * s, a * s + b * c, rest], -1).transpose(1, 2)
+    qt, kt, vt = turn(x[0]), turn(x[1]), x[2].transpose(1, 2)
+    kt, vt = (t.repeat_interleave(H // Hkv, 1) for t in (kt, vt))
+    z = qt @ kt.transpose(2, 3) / math.sqrt(D)
+    z = z.masked_fill(torch.ones(S_nat, S_nat, device=DEV, dtype=torch.bool).triu(1), -math.inf)
+    want = (z.softmax(-1) @ vt).transpose(1, 2)
+    for name, a, b in zip(("o", "dq", "dk", "dv"), got, (want,) + torch.autograd.grad(want, x, do.double())):
+        assert float((a.detach().double() - b.detach()).abs().max()) <= 1.5e-4, name
