@@ -11,9 +11,9 @@
 //     one adds the counts up (through distributed shared memory) and finds the digit in
 //     which the m-th lies.  Counts are integers: no order of additions matters.
 //  3. What is above it stays, and of its equals as many as are left, from the
-//     lowest position on.  Counts of a thread's positions, summed over the CTA and
-//     the cluster, number the places below the cut that become free and the
-//     positions behind it that stay; both go into lists, so that the n-th place is
+//     lowest position on.  A thread has which of its positions stay as bits.  Their counts,
+//     summed over the CTA and the cluster, number the places below the cut that become free
+//     and the positions behind it that stay; both go into lists, so that the n-th place is
 //     filled by the n-th position.
 // evict_fill_kernel copies the pairs of the lists: a lane looks up a pair's pages and moves
 // its weight, then the warp copies the pairs' rows, key and value at once.  Sources lie
@@ -24,10 +24,12 @@
 // became free.
 //
 // Bound by HBM for many positions (scores once, moved rows once in and out), by the
-// chain of its steps for few.
+// chain of its steps for few.  Measured, 8 heads of 128 in bfloat16: 1100 positions cut to 990
+// in 16.4 us; 16 requests of 1000-8192 to the half in 56 us (172 MB, 25 at the copy rate: the
+// longest one's CTA selects for 16, fills for 21, shifts for 14); 131072 to 16384 in 59 us (select
+// 25, fill 21 at 5.5 TB/s of rows in and out, shift 5).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
-#include <limits.h>
 #include <stdint.h>
 
 #include "cpattn.h"
@@ -51,8 +53,8 @@ struct Shared {
   int count[kBins];  // of the digits
   int total[kBins];  // the cluster's, in its first CTA
   int meet[4];       // this CTA's counts, read by the others
-  int warp[6][kWarps];
-  int pick[3];
+  int warp[5][kWarps];
+  int pick[3][3];    // of each pass
 };
 
 // Integers in the order of the scores: NaN lowest, -0 as 0.
@@ -104,11 +106,12 @@ __device__ __forceinline__ int warps_before(int x, int* part, int& tot) {
 // Runs `chunk`, chunk + chunks, .. of `pairs` (at most 32) of the item's lists, by this warp: a
 // lane looks up a pair's pages and moves its weight, the warp copies the rows.
 template <int D>
-__device__ __forceinline__ void fill_places(const EvictArgs& a, int item, int fills, int pairs,
-                                            int chunk, int chunks) {
+__device__ __forceinline__ void fill_places(const EvictArgs& a, int item, const int* to,
+                                            const int* from, int fills, int pairs, int chunk,
+                                            int chunks) {
   constexpr int kLanes = D / 4;       // of a pair of rows, 16 bytes each
   constexpr int kRows = 32 / kLanes;  // of a warp at a time
-  constexpr int U = 8 / kRows;        // turns whose loads are in flight
+  constexpr int U = 4;                // turns of a set
   const int lane = threadIdx.x & 31, r = item / a.Hkv, g = item % a.Hkv, P = a.cache.page_size;
   const PageDiv div = a.pages;
   const int* table = a.table + (int64_t)r * a.table_stride;
@@ -116,8 +119,6 @@ __device__ __forceinline__ void fill_places(const EvictArgs& a, int item, int fi
   // The first half of a pair's lanes copies the key, the second the value.
   uint16_t* base = static_cast<uint16_t*>(l < kLanes / 2 ? a.k_cache : a.v_cache) +
                    g * a.cache.head_stride + l % (kLanes / 2) * 8;
-  const int* to = a.lists + 2 * (int64_t)item * a.list_cap;
-  const int* from = to + a.list_cap;
   for (int h0 = chunk * pairs; h0 < fills; h0 += chunks * pairs) {
     const int n = min(pairs, fills - h0);
     int64_t src = 0, dst = 0;
@@ -131,20 +132,30 @@ __device__ __forceinline__ void fill_places(const EvictArgs& a, int item, int fi
       src = px * a.cache.page_stride + ox * a.cache.token_stride;
       dst = py * a.cache.page_stride + oy * a.cache.token_stride;
     }
-    for (int j0 = 0; j0 < n; j0 += U * kRows) {
-      uint4 v[U];
+    // Two sets by turns: one is stored while the other's loads are in flight.
+    uint4 v[2][U];
+    auto load = [&](uint4 (&v)[U], int j0) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int j = j0 + u * kRows + sub;
         const int64_t at = __shfl_sync(0xffffffffu, src, j & 31);
         if (j < n) v[u] = *reinterpret_cast<const uint4*>(base + at);
       }
+    };
+    auto store = [&](const uint4 (&v)[U], int j0) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int j = j0 + u * kRows + sub;
         const int64_t at = __shfl_sync(0xffffffffu, dst, j & 31);
         if (j < n) *reinterpret_cast<uint4*>(base + at) = v[u];
       }
+    };
+    load(v[0], 0);
+    for (int j0 = 0; j0 < n; j0 += 2 * U * kRows) {
+      load(v[1], j0 + U * kRows);
+      store(v[0], j0);
+      load(v[0], j0 + 2 * U * kRows);
+      store(v[1], j0 + U * kRows);
     }
   }
 }
@@ -330,7 +341,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
   };
   auto key_of = [&](int i) { return held ? s.run[i] : score(lo + i); };
   if (held) {
-#pragma unroll 4
+#pragma unroll 8
     for (int i = tid; i < n; i += kThreads) s.run[i] = score(lo + i);
   }
   for (int i = tid; i < kBins; i += kThreads) s.count[i] = s.total[i] = 0;
@@ -380,7 +391,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
         }
         if (digit >= 0)
           for (int c = 0; c < C; ++c) {
-            int* pick = C > 1 ? cluster.map_shared_rank(s.pick, c) : s.pick;
+            int* pick = C > 1 ? cluster.map_shared_rank(s.pick[pass], c) : s.pick[pass];
             pick[0] = digit;
             pick[1] = rest;
             pick[2] = rest == alike;
@@ -391,64 +402,77 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
       }
       if (C > 1) cluster.sync();
       for (int i = tid; i < kBins; i += kThreads) s.count[i] = 0;
-      found = found << bits | (uint32_t)s.pick[0];
-      left = s.pick[1];
-      plain = s.pick[2];
-      together();  // before the next digit is picked
+      found = found << bits | (uint32_t)s.pick[pass][0];
+      left = s.pick[pass][1];
+      plain = s.pick[pass][2];
+      __syncthreads();
       if (plain) break;
     }
   }
-  // Of those whose leading bits equal `found` the first `left` stay: which of them are in this
-  // run, by the runs before.  A warp takes a row of positions, 32 at a time.
+  // Of those whose leading bits equal `found` the first `left` stay: how many of them are in
+  // this run, by the runs before.
   const int lane = tid & 31, warp = tid >> 5;
-  const unsigned below = (1u << lane) - 1;
-  const int chunk = (n + kThreads - 1) / kThreads * 32;
-  const int i0 = min(n, warp * chunk), i1 = min(n, i0 + chunk);
-  auto lead_of = [&](int i) { return shift < 32 ? key_of(i) >> shift : 0u; };
-  int equal0 = 0, quota = INT_MAX;
-  if (!plain) {
-    int equal = 0, mine_equal;
-    for (int i = i0; i < i1; i += 32)
-      equal += __popc(__ballot_sync(0xffffffffu, i + lane < i1 && lead_of(i + lane) == found));
-    equal0 = warps_before(equal, s.warp[3], mine_equal);
-    quota = left;
-    if (C > 1) {
-      if (tid == 0) s.meet[0] = mine_equal;
-      cluster.sync();
-      for (int c = 0; c < rank; ++c) quota -= *cluster.map_shared_rank(&s.meet[0], c);
+  const bool some = m > 0;
+  auto lead_of = [&](uint32_t key) { return shift < 32 ? key >> shift : 0u; };
+  int quota = left;
+  if (C > 1 && !plain) {
+    int equal = 0, all;
+    for (int i = tid; i < n; i += kThreads) equal += lead_of(key_of(i)) == found;
+    const int upto = warp_sums(equal);
+    warps_before(__shfl_sync(0xffffffffu, upto, 31), s.warp[3], all);
+    if (tid == 0) s.meet[0] = all;
+    cluster.sync();
+    for (int c = 0; c < rank; ++c) quota -= *cluster.map_shared_rank(&s.meet[0], c);
+  }
+  // The run in windows of what shared memory holds (one, unless a run is too long for it).  A
+  // thread takes q positions of a window, q odd for the banks, as bits: which of them become free
+  // below the cut, and which stay behind it; the block's counts of both in one word, before this
+  // thread and in all.
+  uint32_t free_ = 0, go = 0;
+  int first = 0, before = 0, all = 0, seen = 0;
+  auto window = [&](int w0) {
+    const int len = min(kRun, n - w0), q = (len + kThreads - 1) / kThreads | 1;
+    if (!held) {
+      __syncthreads();  // the window before has been read
+#pragma unroll 4
+      for (int i = tid; i < len; i += kThreads) s.run[i] = score(lo + w0 + i);
+      __syncthreads();
     }
-  }
-  // Whether the warp's 32 positions from i on stay, as bits.
-  auto stays = [&](int i, int& seen) {
-    const bool on = m > 0 && i + lane < i1;
-    const uint32_t k = on ? lead_of(i + lane) : 0;
-    if (plain) return __ballot_sync(0xffffffffu, on && k >= found);
-    const unsigned same = __ballot_sync(0xffffffffu, on && k == found);
-    const bool stay = on && (k > found || (k == found && seen + __popc(same & below) < quota));
-    seen += __popc(same);
-    return __ballot_sync(0xffffffffu, stay);
+    const int i0 = min(len, tid * q), mine = min(len, i0 + q) - i0;
+    uint32_t above = 0, same = 0;
+    for (int j = 0; j < mine; ++j) {
+      const uint32_t k = lead_of(s.run[i0 + j]);
+      above |= (uint32_t)(k > found) << j;
+      same |= (uint32_t)(k == found) << j;
+    }
+    if (!plain) {  // the lowest of the block's equals, as far as the quota goes
+      int tot;
+      const int upto = warp_sums(__popc(same));
+      const int base = warps_before(__shfl_sync(0xffffffffu, upto, 31), s.warp[3], tot);
+      int over = min(__popc(same), max(0, seen + base + upto - quota));
+      for (; over > 0; --over) same &= ~(0x80000000u >> __clz(same));
+      seen += tot;
+    }
+    const uint32_t stay = some ? above | same : 0, live = (1u << mine) - 1;
+    first = lo + w0 + i0;
+    const int e = min(mine, max(0, p.cut - first));
+    const uint32_t early = (1u << e) - 1;
+    free_ = early & ~stay;
+    go = stay & live & ~early;
+    const int x = __popc(free_) | __popc(go) << 16, upto = warp_sums(x);
+    before = upto - x + warps_before(__shfl_sync(0xffffffffu, upto, 31), s.warp[4], all);
   };
-  // Positions from i on that lie below the cut, as bits.
-  auto early_of = [&](int i) {
-    const int e = min(p.cut, lo + i1) - (lo + i);
-    return e >= 32 ? 0xffffffffu : (e <= 0 ? 0u : (1u << e) - 1);
-  };
-  // Places that become free below the cut, and positions that stay behind it.
-  int holes = 0, late = 0, seen = equal0;
-  for (int i = i0; i < i1; i += 32) {
-    const unsigned stay = stays(i, seen), early = early_of(i);
-    if (held) s.count[i >> 5] = (int)stay;  // (the counts of digits are no longer needed)
-    holes += __popc(early & ~stay);
-    late += __popc(stay & ~early);
+  int holes = 0, late = 0;
+  for (int w0 = 0; w0 == 0 || w0 < n; w0 += kRun) {
+    window(w0);
+    holes += all & 0xffff;
+    late += all >> 16;
   }
-  int all_holes, all_late;
-  int hole0 = warps_before(holes, s.warp[4], all_holes);
-  int late0 = warps_before(late, s.warp[5], all_late);
-  int fills = all_holes;
+  int hole0 = 0, late0 = 0, fills = holes;
   if (C > 1) {
     if (tid == 0) {
-      s.meet[1] = all_holes;
-      s.meet[2] = all_late;
+      s.meet[1] = holes;
+      s.meet[2] = late;
     }
     cluster.sync();
     fills = 0;
@@ -462,25 +486,36 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
     }
   }
   if (rank == 0 && tid == 0) a.fills[item] = fills;
-  int* to = a.lists + 2 * (int64_t)item * a.list_cap;
-  int* from = to + a.list_cap;
-  seen = equal0;
-  for (int i = i0; i < i1; i += 32) {
-    const unsigned stay = held ? (unsigned)s.count[i >> 5] : stays(i, seen), early = early_of(i);
-    const unsigned free_ = early & ~stay, go = stay & ~early;
-    if (free_ >> lane & 1) to[hole0 + __popc(free_ & below)] = lo + i + lane;
-    if (go >> lane & 1) from[late0 + __popc(go & below)] = lo + i + lane;
-    hole0 += __popc(free_);
-    late0 += __popc(go);
+  // A window's lists take the scores' place; where other kernels read them they go out from
+  // there (straight from the bits a CTA of 14000 free places took 7 us).
+  int* const free_list = reinterpret_cast<int*>(s.run);
+  int* const go_list = free_list + (kAll ? kRun / 2 : 0);  // (neither is longer than half of a run)
+  seen = 0;
+  for (int w0 = 0; w0 == 0 || w0 < n; w0 += kRun) {
+    if (!held) window(w0);
+    const int frees = all & 0xffff, goes = all >> 16;
+    int h = before & 0xffff, l = (before >> 16) + (kAll ? 0 : frees);
+    for (; free_ != 0; free_ &= free_ - 1) free_list[h++] = first + __ffs(free_) - 1;
+    for (; go != 0; go &= go - 1) go_list[l++] = first + __ffs(go) - 1;
+    if constexpr (!kAll) {
+      int* to = a.lists + 2 * (int64_t)item * a.list_cap;
+      int* from = to + a.list_cap + late0;
+      to += hole0;
+      __syncthreads();
+      for (int i = tid; i < frees; i += kThreads) to[i] = free_list[i];
+      for (int i = tid; i < goes; i += kThreads) from[i] = go_list[frees + i];
+      hole0 += frees;
+      late0 += goes;
+    }
   }
   if (C > 1) cluster.sync();  // no CTA leaves while another reads its shared memory
   if constexpr (kAll) {
     __syncthreads();
     const int pairs = min(32, max(4, (fills + kWarps - 1) / kWarps));
     if (a.D == 128)
-      fill_places<128>(a, item, fills, pairs, warp, kWarps);
+      fill_places<128>(a, item, free_list, go_list, fills, pairs, warp, kWarps);
     else
-      fill_places<64>(a, item, fills, pairs, warp, kWarps);
+      fill_places<64>(a, item, free_list, go_list, fills, pairs, warp, kWarps);
     __syncthreads();  // the fills have read what the shift writes over
     shift_rows<kThreads>(a, item, p, 0, a.D / 4);
   }
@@ -490,14 +525,18 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
 // Blocks (part, item): a warp takes 32 pairs of the item's lists at a time.
 // ---------------------------------------------------------------------------
 constexpr int kFillWarps = 4;
+// Pairs a warp looks up at a time; all their rows are in flight at once (131072 positions: with
+// 32, four rows by turns behind another, 20 of 60 us; 8 the same, 4 requests of 4000 22 -> 19 us).
+constexpr int kFillPairs = 8;
 
 template <int D>
-__global__ void __launch_bounds__(kFillWarps * 32) evict_fill_kernel(const EvictArgs a) {
+__global__ void __launch_bounds__(kFillWarps * 32, 8) evict_fill_kernel(const EvictArgs a) {
   tc::launch_dependents();
   tc::wait_prior_grid();
   const int item = a.item0 + blockIdx.y;
-  fill_places<D>(a, item, a.fills[item], 32, blockIdx.x * kFillWarps + (threadIdx.x >> 5),
-                     gridDim.x * kFillWarps);
+  const int* to = a.lists + 2 * (int64_t)item * a.list_cap;
+  fill_places<D>(a, item, to, to + a.list_cap, a.fills[item], kFillPairs,
+                 blockIdx.x * kFillWarps + (threadIdx.x >> 5), gridDim.x * kFillWarps);
 }
 
 // ---------------------------------------------------------------------------
@@ -550,10 +589,12 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t stream) {
   const int freed_blocks = a.num_freed_max / (8 * kShiftThreads) < sms
                                ? a.num_freed_max / (8 * kShiftThreads) + 1
                                : sms;
-  // A CTA a head does all where that is little or the heads fill the SMs.  Measured (us, one
-  // launch / three; 8 heads a request, keys and values of 128):
-  //    1 request, 1000 of 2000 kept:  19 / 19       1 request, 2000 of 4000: 28 / 22
-  //   16 requests, 1000 of 2000:      21 / 31      16 requests, 4000 of 8000: 66 / 84
+  // A CTA a head does all where the heads fill the SMs, or where that is so little that the host
+  // (5 us more for three launches than for one) decides.  Measured (us on the device, one launch /
+  // three; 8 heads a request, keys and values of 128, half kept of):
+  //    1 request of 1000: 14 / 12    1 of 2000: 17 / 14     1 of 4000: 28 / 16
+  //    8 requests of 1000: 15 / 16   8 of 4000: 27 / 25     8 of 8000: 49 / 47
+  //   12 requests of 1000: 15 / 19  12 of 4000: 32 / 38    12 of 8000: 57 / 63
   if (items > 0 && longest <= kRun && (longest <= kAllLongest || 2 * items >= sms)) {
     static DeviceOnce all_allowed;
     e = all_allowed.shared_memory(reinterpret_cast<const void*>(evict_select_kernel<true>), dev,
@@ -570,8 +611,14 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t stream) {
   }
   const int slices = a.D * 4 / 64;
   if (items > 0) {
-    // A CTA whose shared memory holds the scores that a request can have, or a cluster.
+    // A CTA whose shared memory holds the scores that a request can have, or a cluster; a wider
+    // one where it finds room at once.  Measured (us, clusters of 1, 2, 4 and 8; 8 heads a request):
+    //   1 request of  8000: 20, 22, 20, 20     4 requests of  8000: 25, 27, 26, 47
+    //   1 request of 16000: 28, 26, 21, 22     4 requests of 16000: 51, 49, 47, 70
+    //   1 request of 32000: 65, 35, 30, 29     2 requests of 32000: 92, 55, 49, 62
     int C = 1;
+    if (longest > kRun / 2 && 4 * items <= sms) C = 4;
+    if (longest > kRun * 2 && 16 * items <= sms) C = 8;
     while (C < kMaxCluster && C * (int64_t)kRun < longest) C *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(items * C));
@@ -588,7 +635,7 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t stream) {
     e = cudaLaunchKernelEx(&cfg, evict_select_kernel<false>, a);
     if (e != cudaSuccess) return e;
     // Warps for all the pairs that there can be, as far as the SMs can hold them.
-    const int64_t pairs = (a.list_cap + kFillWarps * 32 - 1) / (kFillWarps * 32);
+    const int64_t pairs = (a.list_cap + kFillWarps * kFillPairs - 1) / (kFillWarps * kFillPairs);
     int64_t parts = (int64_t)sms * 16 / items + 1;
     if (parts > pairs) parts = pairs > 0 ? pairs : 1;
     // (65535 blocks in y at most.)
