@@ -525,8 +525,8 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
 // Blocks (part, item): a warp takes 32 pairs of the item's lists at a time.
 // ---------------------------------------------------------------------------
 constexpr int kFillWarps = 4;
-// Pairs a warp looks up at a time; all their rows are in flight at once (131072 positions: with
-// 32, four rows by turns behind another, 20 of 60 us; 8 the same, 4 requests of 4000 22 -> 19 us).
+// Pairs a warp looks up at a time, all their rows in flight at once (4 requests of 4000, half
+// kept: 19 us, with 32 pairs 22; 131072 positions take the same either way).
 constexpr int kFillPairs = 8;
 
 template <int D>

@@ -309,3 +309,11 @@ def test_two_calls_at_once():
     for (_, (w, k, v, *_), want), out in zip(calls, got):
         for x, y in zip((k, v, w) + out, want):
             assert same(x, y)
+
+
+@pytest.mark.parametrize("ctx,keep,first,recent,Hkv", [
+    ([9000], [4000], 4, 64, 8), ([40000, 33000], [20000, 5], 0, 1000, 1), ([140001], [70000], 4, 100, 1),
+    ([140001], [139000], 0, 0, 1)])
+@pytest.mark.parametrize("kind", ["ties", "equal", "wild"])
+def test_equals_among_ctas_and_windows(ctx, keep, first, recent, Hkv, kind):
+    run(ctx, keep, first, recent, Hkv, 64, 64, "bf16", kind)
