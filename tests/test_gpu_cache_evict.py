@@ -317,3 +317,43 @@ def test_two_calls_at_once():
 @pytest.mark.parametrize("kind", ["ties", "equal", "wild"])
 def test_equals_among_ctas_and_windows(ctx, keep, first, recent, Hkv, kind):
     run(ctx, keep, first, recent, Hkv, 64, 64, "bf16", kind)
+
+
+def test_offsets_beyond_32_bits():
+    """A cache of 5 GB whose requests lie at its end gives what a small one does, bit by bit."""
+    H, Hkv, D, P, pages = 16, 8, 128, 64, 40000
+    assert pages * P * Hkv * D > 1 << 31
+    ctx, new = [500, 333], [3, 20]
+    need = [-(-(c + n) // P) for c, n in zip(ctx, new)]
+    table = torch.full((2, max(need)), -1, dtype=torch.int32, device=DEV)
+    for r, n in enumerate(need):
+        table[r, :n] = torch.arange(n, device=DEV) + sum(need[:r])
+    g = torch.Generator().manual_seed(5)
+    small = torch.randn(2, sum(need), P, Hkv, D, generator=g).to(torch.bfloat16).to(DEV)
+    weights = torch.rand(sum(need), Hkv, P, generator=g).to(DEV)
+    q, k, v = (torch.randn(sum(new), n, D, generator=g).to(torch.bfloat16).to(DEV) for n in (H, Hkv, Hkv))
+    freqs, at = torch.rand(D // 2, generator=g, dtype=torch.float64).to(DEV), torch.arange(sum(new), device=DEV).int()
+    slot = [int(table[r, p // P]) * P + p % P for r in range(2) for p in range(ctx[r], ctx[r] + new[r])]
+    results = []
+    for first in (0, pages - sum(need)):
+        if first:
+            cache = [torch.empty(pages, P, Hkv, D, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+            for x, y in zip(cache, small):
+                x[first:] = y
+            w = torch.empty(pages, Hkv, P, device=DEV)
+            w[first:] = weights
+        else:
+            cache, w = [x.clone() for x in small], weights.clone()
+        t = torch.where(table >= 0, table + first, table)
+        slots = torch.tensor(slot, device=DEV) + first * P
+        cu, total = ints([0, new[0], sum(new)]), ints([c + n for c, n in zip(ctx, new)])
+        out, kc, vc = cpa.rotary_cache_write(q, k, v, freqs, at, cache[0], cache[1], slots)
+        o, lse = cpa.tree_attention(out, kc, vc, t, ints(ctx), cu)
+        cpa.cache_weights(out, kc, t, ints(ctx), cu, lse, w)
+        moved = cpa.cache_evict(w, kc, vc, t, total, ints([200, 100]), 200, first=4, recent=30)
+        assert cpa.device_status() == 0
+        freed = torch.where(moved[2] >= 0, moved[2] - first, moved[2])
+        results.append((out, o, kc[first:].clone(), vc[first:].clone(), w[first:].clone(), moved[0], moved[1], freed, moved[3]))
+        del cache, kc, vc, w
+    for x, y in zip(*results):
+        assert same(x, y)

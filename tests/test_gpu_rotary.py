@@ -271,3 +271,15 @@ def test_training_through_the_ring(B, S_nat, S, H, Hkv, D, rot, cp, own):
     want = (z.softmax(-1) @ vt).transpose(1, 2)
     for name, a, b in zip(("o", "dq", "dk", "dv"), got, (want,) + torch.autograd.grad(want, x, do.double())):
         assert float((a.detach().double() - b.detach()).abs().max()) <= 1.5e-4, name
+
+
+def test_offsets_beyond_32_bits():
+    S, H, D, cp = 600000, 32, 128, 4
+    x, f = torch.empty(1, S, H, D, dtype=torch.bfloat16, device=DEV), frequencies(D)
+    x[0, -100:] = normal(30, 100, H, D, dtype=torch.bfloat16)
+    want = cpa.rotary(x[0, -100:].clone(), f, offset=S - 100)
+    out = cpa.rotary(x, f, cp=cp, to_sharded=True)
+    # The last chunk of the zigzag order is the second of rank 0.
+    c = S // (2 * cp)
+    assert torch.equal(out[0, 2 * c - 100:2 * c], want)
+    assert torch.equal(cpa.rotary(x, f)[0, -100:], want)
