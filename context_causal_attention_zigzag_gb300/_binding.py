@@ -1156,7 +1156,7 @@ def cache_evict(weights, k_cache, v_cache, block_table, ctx_lens, keep, most, fi
     _launch("cpattn_cache_evict", dev, weights.data_ptr(),
             None if scores is None else scores.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             *cache, block_table.data_ptr(), width, stride, ctx_lens.data_ptr(), keep.data_ptr(),
-            first, recent, most, new_lens.data_ptr(), kept.data_ptr(), freed.data_ptr(),
+            min(first, 2**31 - 1), min(recent, 2**31 - 1), most, new_lens.data_ptr(), kept.data_ptr(), freed.data_ptr(),
             freed.numel(), count.data_ptr(), R, Hkv, D, code, ws.data_ptr(), ws.numel())
     return outputs
 

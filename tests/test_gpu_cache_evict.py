@@ -357,3 +357,8 @@ def test_offsets_beyond_32_bits():
         del cache, kc, vc, w
     for x, y in zip(*results):
         assert same(x, y)
+
+
+def test_first_or_recent_beyond_any_length():
+    for first, recent in ((1 << 40, 3), (0, 1 << 32)):
+        run([300, 90], [100, 80], first, recent, 2, 64, 16, "bf16")
