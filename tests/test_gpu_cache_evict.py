@@ -362,3 +362,10 @@ def test_offsets_beyond_32_bits():
 def test_first_or_recent_beyond_any_length():
     for first, recent in ((1 << 40, 3), (0, 1 << 32)):
         run([300, 90], [100, 80], first, recent, 2, 64, 16, "bf16")
+
+
+@pytest.mark.parametrize("R,width", [(2500, 3), (3000, 3)])  # the freed pages listed by the one launch, by one of their own
+def test_thousands_of_requests(R, width):
+    rng = random.Random(R)
+    ctx = [rng.randrange(16 * (width - 1) + 1) for _ in range(R)]
+    run(ctx, [rng.randrange(c + 5) for c in ctx], 1, 3, 1, 64, 16, "bf16", seed=R)

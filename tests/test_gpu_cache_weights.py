@@ -234,3 +234,14 @@ def test_broken_lengths_and_tables_are_reported():
         cpa.cache_weights(q, k, table, c, cu, lse, weights, tree=tree)
         assert cpa.device_status() == -1, what
     assert cpa.device_status() == 0
+
+
+@pytest.mark.parametrize("R,most_ctx,most_new", [(1500, 60, 3), (1300, 5, 90)])
+def test_thousands_of_requests(R, most_ctx, most_new):
+    g = torch.Generator().manual_seed(R)
+    ctx, new = (torch.randint(0, n + 1, (R,), generator=g).tolist() for n in (most_ctx, most_new))
+    q, k, table, c, cu, lse, weights, _ = make(ctx, new, 4, 1, 64, 16, False, "bf16", seed=R)
+    want, tol = reference(q, k, table, ctx, new, lse, weights, None, None, 1.0)
+    got = cpa.cache_weights(q, k, table, c, cu, lse, weights)
+    assert cpa.device_status() == 0
+    check(got, want, tol)
