@@ -369,3 +369,56 @@ def test_thousands_of_requests(R, width):
     rng = random.Random(R)
     ctx = [rng.randrange(16 * (width - 1) + 1) for _ in range(R)]
     run(ctx, [rng.randrange(c + 5) for c in ctx], 1, 3, 1, 64, 16, "bf16", seed=R)
+
+
+def test_a_step_from_a_graph():
+    """Turn and write, attend, weigh and evict, captured once and replayed with other lengths: the eager call's bits."""
+    H, Hkv, D, P, most, N = 8, 2, 64, 16, 120, 40
+    k0, v0, w0, table = make([300, 300, 300], Hkv, D, P, "bf16", seed=9, extra=0)
+    w0.abs_()
+    g = torch.Generator().manual_seed(9)
+    q, k, v = (torch.randn(N, n, D, generator=g).to(torch.bfloat16).to(DEV) for n in (H, Hkv, Hkv))
+    freqs = torch.rand(D // 2, generator=g, dtype=torch.float64).to(DEV)
+    ctx, cu, total, at = ints([0] * 3), ints([0] * 4), ints([0] * 3), torch.zeros(N, dtype=torch.int32, device=DEV)
+    slots, keep = torch.full((N,), -1, dtype=torch.int64, device=DEV), ints([most, 30, 0])
+    kc, vc, w = k0.clone(), v0.clone(), w0.clone()
+    turned, out, lse = torch.empty_like(q), torch.empty_like(q), torch.empty(H, N, device=DEV)
+    moved = cpa.cache_evict_outputs(kc, table, ctx, most)
+    spaces = (cpa.tree_attention_workspace(q, kc, cu), cpa.cache_weights_workspace(q, kc, cu),
+              cpa.cache_evict_workspace(kc, table, most))
+
+    def step():
+        cpa.rotary_cache_write(q, k, v, freqs, at, kc, vc, slots, out=turned)
+        cpa.tree_attention(turned, kc, vc, table, ctx, cu, out=out, lse=lse, workspace=spaces[0])
+        cpa.cache_weights(turned, kc, table, ctx, cu, lse, w, decay=0.5, workspace=spaces[1])
+        cpa.cache_evict(w, kc, vc, table, total, keep, most, first=2, recent=20, outputs=moved, workspace=spaces[2])
+
+    def set_lens(lens, new):
+        for x, y in zip((kc, vc, w), (k0, v0, w0)):
+            x.copy_(y)
+        ctx.copy_(ints(lens))
+        cu.copy_(ints([sum(new[:i]) for i in range(4)]))
+        total.copy_(ints([a + b for a, b in zip(lens, new)]))
+        places = [(r, p) for r in range(3) for p in range(lens[r], lens[r] + new[r])]
+        at.zero_()
+        slots.fill_(-1)
+        at[:len(places)] = ints([p for _, p in places])
+        slots[:len(places)] = torch.tensor([int(table[r, p // P]) * P + p % P for r, p in places], device=DEV)
+
+    set_lens([10, 10, 10], [1, 1, 1])
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for lens, new in (([250, 0, 299], [30, 9, 1]), ([100, 17, 200], [1, 1, 1]), ([0, 280, 0], [40, 0, 0])):
+        results = []
+        for run_step in (step, graph.replay):
+            set_lens(lens, new)
+            run_step()
+            torch.cuda.synchronize()
+            assert cpa.device_status() == 0
+            n = sum(new)
+            results.append([x.clone() for x in (turned, out[:n], lse[:, :n], kc, vc, w) + tuple(moved)])
+        for x, y in zip(*results):
+            assert same(x.contiguous(), y.contiguous())
+        assert results[0][6].tolist() == [min(a + b, c) for a, b, c in zip(lens, new, (most, 30, 0))]
