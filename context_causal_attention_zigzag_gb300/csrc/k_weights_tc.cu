@@ -110,7 +110,7 @@ struct Cfg {
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kOffNotes = (kOffMisc + 16 + 15) / 16 * 16;
   static constexpr int kSmemBytes = kOffNotes + kNotes * (int)sizeof(Note);
-  static_assert(kSmemBytes <= 232448, "shared memory");
+  static_assert(kSmemBytes <= 232448 && kNorms <= 8, "shared memory");
 };
 
 // TMEM: two places of products for each key tile.
@@ -179,6 +179,8 @@ __global__ void __launch_bounds__(Cfg<D, kDeep>::kThreads, 1)
   auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+  // Of each place for normalisers: whether a row there gives nothing (its lse is -inf).
+  volatile uint8_t* some_void = smem + C::kOffMisc + 8;
   // [20] of the warps; then where this CTA begins: in_req, r and the request.
   long long* sums = reinterpret_cast<long long*>(smem + C::kOffL);
 
@@ -424,9 +426,9 @@ __global__ void __launch_bounds__(Cfg<D, kDeep>::kThreads, 1)
   } else if (warp == 3) {
     // ---------------------------------------------------- notes and normalisers
     // The pieces' notes, each before the normalisers of the piece before it (the
-    // warpgroups look one piece ahead); -lse log2(e) of each row, -inf for those that
-    // give nothing, four rows a lane, a step's values fetched while the step before is
-    // handed over.
+    // warpgroups look one piece ahead); -lse log2(e) of each row (infinity: it gives nothing,
+    // whatever its products are), four rows a lane, a step's values fetched while the step
+    // before is handed over.
     int tok[4], head[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -507,11 +509,9 @@ __global__ void __launch_bounds__(Cfg<D, kDeep>::kThreads, 1)
         continue;
       }
       for (; ok && at.s < at.s1; ) {
-        float4 l;
-        l.x = v[0] == -INFINITY ? -INFINITY : -kLog2e * v[0];
-        l.y = v[1] == -INFINITY ? -INFINITY : -kLog2e * v[1];
-        l.z = v[2] == -INFINITY ? -INFINITY : -kLog2e * v[2];
-        l.w = v[3] == -INFINITY ? -INFINITY : -kLog2e * v[3];
+        const float4 l = {-kLog2e * v[0], -kLog2e * v[1], -kLog2e * v[2], -kLog2e * v[3]};
+        const bool none = __any_sync(0xffffffffu, l.x == INFINITY || l.y == INFINITY ||
+                                                      l.z == INFINITY || l.w == INFINITY);
         ++at.s;
         if (at.s < at.s1)
           fetch(at);
@@ -522,6 +522,7 @@ __global__ void __launch_bounds__(Cfg<D, kDeep>::kThreads, 1)
         if (!ok) break;
         ++rows;
         reinterpret_cast<float4*>(smem + C::kOffL + sl * kT * 4)[lane] = l;
+        if (lane == 0) some_void[sl] = none;
         mbar_arrive(bar(C::kBarLFull + sl));
       }
       some = more;
@@ -555,8 +556,8 @@ __global__ void __launch_bounds__(Cfg<D, kDeep>::kThreads, 1)
     Two t0, t1;
     // Adds up 32 columns from c on of a key's row of products with the tile of rows at tok0, of
     // which all (whole) or those that see the key count.
-    auto columns = [&](const uint32_t* r, const float* nl, int c, bool whole, int ahead_by, int tok0,
-                       int ntok, int n, int q0) {
+    auto columns = [&](const uint32_t* r, const float* nl, int c, bool whole, bool voids, int ahead_by,
+                       int tok0, int ntok, int n, int q0) {
       float y[32];
 #pragma unroll
       for (int j = 0; j < 32; j += 4) {
@@ -582,6 +583,11 @@ __global__ void __launch_bounds__(Cfg<D, kDeep>::kThreads, 1)
           }
           seen &= named;
         }
+        if (voids) {  // (some row of the tile: seldom)
+#pragma unroll 1
+          for (int j = 0; j < 32; ++j)
+            if (nl[c + j] == INFINITY) seen &= ~(1u << j);
+        }
 #pragma unroll
         for (int j = 0; j < 32; ++j) y[j] = seen >> j & 1 ? y[j] : 0.f;
       }
@@ -595,7 +601,8 @@ __global__ void __launch_bounds__(Cfg<D, kDeep>::kThreads, 1)
     // is `first` new tokens on) sees are passed over, those that all see need no selection: of a
     // key tile's steps along the diagonal only one in four selects in a warp (16 prompts of
     // 100-2000 tokens 113.3 -> 112.1 us, 64 single tokens 94.9 -> 93.8; one of 16384 872 -> 875).
-    auto row_sum = [&](uint32_t at, int free_bar, const float* nl, int first, int tok0, int n, int q0) {
+    auto row_sum = [&](uint32_t at, int free_bar, const float* nl, bool voids, int first, int tok0, int n,
+                       int q0) {
       t0 = t1 = two(0.f, 0.f);
       const int ntok = min(tpt, n - tok0), live = ntok * G;
       const int any = chain ? max(0, min(first - tok0, tpt)) * G : 0;
@@ -614,7 +621,7 @@ __global__ void __launch_bounds__(Cfg<D, kDeep>::kThreads, 1)
           tc_fence_before();
           mbar_arrive(bar(free_bar));
         }
-        columns(r, nl, c, c >= all && c + 32 <= live, first + lane, tok0, ntok, n, q0);
+        columns(r, nl, c, c >= all && c + 32 <= live && !voids, voids, first + lane, tok0, ntok, n, q0);
       }
       const float2 x0 = apart(t0), x1 = apart(t1);
       return (x0.x + x0.y) + (x1.x + x1.y);
@@ -654,6 +661,7 @@ __global__ void __launch_bounds__(Cfg<D, kDeep>::kThreads, 1)
           const uint32_t slot = (rows - 1) % C::kNorms;
           ok = wwait(bar(C::kBarLFull + slot), ((rows - 1) / C::kNorms) & 1);
           if (!ok) break;
+          const bool voids = some_void[slot];
           if (s >= (group == 0 ? from0 : from1)) {
             const int at = 2 * group + (used & 1), tok0 = (q0t + s) * tpt;
             ok = wwait(bar(C::kBarS + 3 * at), used >> 1 & 1);
@@ -662,7 +670,7 @@ __global__ void __launch_bounds__(Cfg<D, kDeep>::kThreads, 1)
             tc_fence_after();
             plus(total0, lost0,
                  row_sum(tl + col_s(at), C::kBarSFree + at,
-                         reinterpret_cast<const float*>(smem + C::kOffL + slot * kT * 4),
+                         reinterpret_cast<const float*>(smem + C::kOffL + slot * kT * 4), voids,
                          first + group * kT, tok0, n, q0));
           }
           if (last || s + 1 < s1) mbar_arrive(bar(C::kBarLEmpty + slot));
@@ -675,6 +683,7 @@ __global__ void __launch_bounds__(Cfg<D, kDeep>::kThreads, 1)
           const int tok0 = (q0t + s) * tpt;
           const float* nl = reinterpret_cast<const float*>(smem + C::kOffL + slot * kT * 4);
           ok = wwait(bar(C::kBarLFull + slot), (step / C::kNorms) & 1);
+          const bool voids = some_void[slot];
 #pragma unroll 1
           for (int i = 0; ok && i < (s >= from1 ? 2 : 1); ++i) {
             const int at = 2 * i + ((i == 0 ? step : made1 + (uint32_t)(s - from1)) & 1);
@@ -682,7 +691,8 @@ __global__ void __launch_bounds__(Cfg<D, kDeep>::kThreads, 1)
             if (!ok) break;
             phases ^= 1u << at;
             tc_fence_after();
-            const float x = row_sum(tl + col_s(at), C::kBarSFree + at, nl, first + i * kT, tok0, n, q0);
+            const float x =
+                row_sum(tl + col_s(at), C::kBarSFree + at, nl, voids, first + i * kT, tok0, n, q0);
             plus(i == 0 ? total0 : total1, i == 0 ? lost0 : lost1, x);
           }
           if (!ok) break;

@@ -146,6 +146,24 @@ def test_rows_with_broken_normalisers(form):
 
 
 @pytest.mark.parametrize("form", list(FORMS))
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_rows_that_give_nothing_may_hold_anything(form, value):
+    """Padding within a request, say: q as it was left, lse -inf."""
+    ctx, new = FORMS[form][:2]
+    q, k, table, c, cu, lse, weights = make(*FORMS[form])
+    want_q = q.clone()
+    for h in range(q.shape[1]):
+        for i in (h % sum(new), (sum(new) - 1 - h) % sum(new), sum(new) // 2):
+            lse[h, i] = -math.inf
+            q[i, h, h % 7] = value
+            want_q[i, h] = 0
+    want, tol = reference(want_q, k, table, ctx, new, lse, weights)
+    got = cpa.cache_weights(q, k, table, c, cu, lse, weights)
+    assert cpa.device_status() == 0
+    check(got, want, tol)
+
+
+@pytest.mark.parametrize("form", list(FORMS))
 def test_graphs_streams_and_changing_lengths(form):
     ctx, new = FORMS[form][:2]
     q, k, table, c, cu, lse, weights = make(*FORMS[form])
