@@ -815,8 +815,7 @@ cudaError_t run(const WeightsArgs& w, int dev, int sms, cudaStream_t stream) {
 
 template <bool kBf16, int D>
 cudaError_t run_deep(const WeightsArgs& w, int dev, int sms, cudaStream_t stream) {
-  // Few rows a request on the average: keys are what streams.
-  const bool deep = (int64_t)w.t.N * (w.t.H / w.t.Hkv) <= (int64_t)w.t.R * kT;
+  const bool deep = keys_stream(w.t.R, w.t.N, w.t.H / w.t.Hkv);
   return deep ? run<kBf16, D, true>(w, dev, sms, stream) : run<kBf16, D, false>(w, dev, sms, stream);
 }
 

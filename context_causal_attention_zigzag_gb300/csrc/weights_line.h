@@ -18,6 +18,26 @@ constexpr int kItemCost = 1;
 // Least part of the line for a CTA.
 constexpr int kMinPart = 2;
 
+// Which form of the kernel takes a call of N new tokens of R requests, G query heads a kv head:
+// keys that stream past a request's rows (a deep ring of key tiles, one place for rows), or rows
+// that stream past two key tiles.  The lengths themselves are on the device, so the mean decides.
+// Measured (us, keys stream / rows stream; H = 32, Hkv = 8, D = 128, pages of 64):
+//   32 requests of 16 tokens over 4000   68 / 84     64 single tokens over 1000-8192     127 / 170
+//   32 of 30 (a tile of rows at most)    74 / 88     63 of them and a prompt of 100      152 / 170
+//   32 of 33 (two tiles)                108 / 107    63 and a prompt of 500              246 / 174
+//   32 of 100                           180 / 164    63 and a prompt of 2000             266 / 195
+// So requests of more than one tile of rows are better off where rows stream; a prompt beside
+// enough single tokens is not told apart from drafts of the same mean.
+// Where keys stream a step of a request of several tiles waits for its rows: 1.7 us, and the
+// loading of the key tile behind it waits for the item.  Up to kMostKeyRows rows that is 0.3 s
+// at 1.5 GHz, where the bounded waits allow 2; the rows of the most that a call takes (2^27)
+// stream past an item's keys in 1.4 s.
+constexpr int64_t kMostKeyRows = (int64_t)1 << 24;
+inline bool keys_stream(int R, int N, int G) {
+  const int64_t rows = (int64_t)N * G;
+  return rows <= (int64_t)R * kTcTile && rows <= kMostKeyRows;
+}
+
 __host__ __device__ inline int tiles_of(const Req& x, int tpt) { return (x.n + tpt - 1) / tpt; }
 __host__ __device__ inline int items_of(const Req& x) { return (x.total + kPair - 1) / kPair; }
 // First tile of tokens that sees position p or one behind it.

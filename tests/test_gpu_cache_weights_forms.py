@@ -274,3 +274,19 @@ def test_tiles_are_added_with_compensation():
     want = 8 * ((-lse[0, 0].double()).exp() + (n - 1) * (-lse[0, 1].double()).exp())
     off = (weights[page, :, i].double() / want - 1).abs()
     assert float(off.max()) < 1.2e-5
+
+
+def test_more_rows_than_stream_past():
+    """Single tokens of so many requests that the form for a few rows each is not taken."""
+    R, H, D, P = 140000, 128, 64, 16
+    q = torch.zeros(R, H, D, device=DEV, dtype=torch.bfloat16)
+    k = torch.ones(R, P, 1, D, device=DEV, dtype=torch.bfloat16)
+    table = torch.arange(R, device=DEV, dtype=torch.int32).flip(0).contiguous()[:, None]
+    ctx = torch.arange(R, device=DEV, dtype=torch.int32) % 12
+    weights = torch.full((R, 1, P), 3.0, device=DEV)
+    cpa.cache_weights(q, k, table, ctx, torch.arange(R + 1, device=DEV, dtype=torch.int32),
+                      torch.zeros(H, R, device=DEV), weights, decay=0.5)
+    assert cpa.device_status() == 0
+    pos, x = torch.arange(P, device=DEV), ctx.flip(0)[:, None]
+    want = torch.where(pos < x, 1.5 + H, torch.where(pos == x, float(H), 3.0))
+    assert torch.equal(weights[:, 0], want)
