@@ -756,8 +756,8 @@ CPATTN_API int cpattn_rotary_cache_write(
  * kv head.  A row whose lse is -inf gives nothing.  Requests without new tokens
  * are left as they are, and so is everything else in weights; two runs give
  * the same bits.
- *   q [N, H, D], tokens q_stride apart; lse [H, N]; decay finite; N * H / Hkv at
- *   most 2^27.  The rest, and
+ *   q [N, H, D], tokens q_stride apart; lse [H, N]; decay finite; N at most 2^20
+ *   times the whole tokens of 128 rows (128 / (H / Hkv), rounded down).  The rest, and
  *   what broken lengths and tables do, as cpattn_tree_attn.
  * No page belongs to two requests of the call, or the old weights that it holds
  * may count for either.
