@@ -6,6 +6,8 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <algorithm>
+
 #include "answer_checks.h"
 #include "cpattn.h"
 #include "cpattn_internal.h"
@@ -65,6 +67,41 @@ Stretch table_stretch(const int32_t* table, int R, int width, int64_t stride) {
 Bytes cache_bytes(const CacheShape& c, int Hkv, int D) {
   return 2 * ((Bytes)(c.num_pages - 1) * c.page_stride +
               (Bytes)(c.page_size - 1) * c.token_stride + (Bytes)(Hkv - 1) * c.head_stride + D);
+}
+
+// Whether rows of `width` bytes, `stride` apart, and a stretch share memory.
+bool row_meets(const void* p, Bytes stride, Bytes rows, Bytes width, const Stretch& x) {
+  return rows_meet(p, stride, rows, width, x.p, stride, x.n > 0, x.n);
+}
+
+// Whether the keys and values of a cache share memory: both have its strides, and may lie by
+// turns in one tensor.  With the axes from the widest stride down, an axis cannot make up for
+// more than a step of those before it, so that of each only the steps around what is left matter.
+bool caches_meet(const void* k, const void* v, const CacheShape& c, int Hkv, int D) {
+  struct Axis {
+    Bytes stride, n;
+  } axes[3] = {{2 * (Bytes)c.page_stride, c.num_pages},
+               {2 * (Bytes)c.token_stride, c.page_size},
+               {2 * (Bytes)c.head_stride, Hkv}};
+  std::sort(axes, axes + 3, [](const Axis& x, const Axis& y) { return x.stride > y.stride; });
+  Bytes left[8] = {(Bytes)reinterpret_cast<intptr_t>(v) - reinterpret_cast<intptr_t>(k)};
+  int ways = 1;
+  for (const Axis& x : axes) {
+    if (x.n == 1) continue;  // its stride says nothing
+    int next = 0;
+    Bytes then[8];
+    for (int i = 0; i < ways; ++i) {
+      Bytes m = left[i] / x.stride;
+      if (m * x.stride > left[i]) --m;
+      for (int j = 0; j < 2; ++j, ++m)
+        if (m < x.n && -m < x.n) then[next++] = left[i] - m * x.stride;
+    }
+    ways = next;
+    for (int i = 0; i < ways; ++i) left[i] = then[i];
+  }
+  for (int i = 0; i < ways; ++i)
+    if (left[i] < 2 * D && -left[i] < 2 * D) return true;
+  return false;
 }
 
 bool turn_ok(int D, int rot, int interleaved, const double* freqs, float magnitude) {
@@ -137,6 +174,13 @@ int cpattn_rotary(const void* x, int64_t x_stride, void* out, int64_t out_stride
   if (!same && rows_meet(x, x_stride * elt, (int64_t)B * a.S_in, width * elt, out,
                          out_stride * elt, (int64_t)B * a.S_out, width * elt))
     return CPATTN_ERR_INVALID_ARG;
+  // (Several blocks read these while others write.)
+  const Stretch read[] = {
+      {positions, positions && S_nat > 0 ? 4 * ((Bytes)(B - 1) * positions_stride + S_nat) : 0},
+      {freqs, 4 * (Bytes)rot}};
+  for (const Stretch& r : read)
+    if (row_meets(out, out_stride * elt, (Bytes)B * a.S_out, width * elt, r))
+      return CPATTN_ERR_INVALID_ARG;
   a.x = x;
   a.out = out;
   a.x_stride = x_stride;
@@ -189,6 +233,17 @@ int cpattn_rotary_cache_write(const void* q, int64_t q_stride, const void* k, in
       rows_meet(k_cache, wc, 1, wc, out, 2 * out_stride, N, wq) ||
       rows_meet(v_cache, wc, 1, wc, out, 2 * out_stride, N, wq))
     return CPATTN_ERR_INVALID_ARG;
+  if (caches_meet(k_cache, v_cache, c, Hkv, D)) return CPATTN_ERR_INVALID_ARG;
+  const Stretch lists[] = {{positions, 4 * (Bytes)N}, {slots, 8 * (Bytes)N}, {freqs, 4 * (Bytes)rot}};
+  for (const Stretch& x : lists)
+    if (row_meets(out, 2 * out_stride, N, wq, x)) return CPATTN_ERR_INVALID_ARG;
+  const Stretch caches[] = {{k_cache, wc}, {v_cache, wc}};
+  for (const Stretch& x : caches) {
+    const Stretch one[] = {x};
+    if (any_meet(one, lists) || row_meets(q, 2 * q_stride, N, wq, x) ||
+        row_meets(k, 2 * k_stride, N, wk, x) || row_meets(v, 2 * v_stride, N, wk, x))
+      return CPATTN_ERR_INVALID_ARG;
+  }
   int* err = device_error_word();
   if (err == nullptr) return CPATTN_ERR_CUDA;
   RotaryWriteArgs a = {q,     k,         v,         out,  q_stride, k_stride, v_stride, out_stride,

@@ -713,8 +713,8 @@ CPATTN_API int cpattn_rotary_frequencies(double* freqs, double* magnitude, int r
  *   Tokens lie x_stride / out_stride elements apart, sequences Sx / So tokens.
  * dtype CPATTN_F32, CPATTN_BF16 or CPATTN_F16; D a multiple of 8 up to 256, rot even, 2 to
  * D; x and out 16-byte aligned, strides multiples of 16 bytes.  out may be x
- * itself (same stride and order), else they must not overlap.  S at most 2^30,
- * B at most 65535.  The gradient of a call is the same call with transposed = 1
+ * itself (same stride and order), else they must not overlap; nor does it overlap
+ * positions or freqs.  S at most 2^30, B at most 65535.  The gradient of a call is the same call with transposed = 1
  * and the orders exchanged.
  */
 CPATTN_API int cpattn_rotary(const void* x, int64_t x_stride, void* out, int64_t out_stride, int B,
@@ -732,7 +732,8 @@ CPATTN_API int cpattn_rotary(const void* x, int64_t x_stride, void* out, int64_t
  *   q [N, H, D], out [N, H, D] (out may be q itself), k, v [N, Hkv, D], tokens
  *   q_stride, out_stride, k_stride, v_stride apart; positions int32 [N].
  * Types, D and the cache as in the answering calls; rot, freqs, interleaved and
- * magnitude as above.
+ * magnitude as above.  What is written (out, the caches) overlaps nothing else, but out
+ * may be q; the keys and values share no element (they may lie in one tensor).
  */
 CPATTN_API int cpattn_rotary_cache_write(
     const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,

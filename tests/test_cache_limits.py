@@ -35,3 +35,28 @@ def test_rows_whose_tiles_outlast_the_waits(G):
     assert call("cpattn_cache_weights", args, N=most + 1) == E
     # (The workspace is looked at last: without one nothing is launched.)
     assert call("cpattn_cache_weights", args, N=most) == _binding.ERR_WORKSPACE
+
+
+ROTARY = dict(x=at(GB), xs=256, out=at(2 * GB), os=384, B=2, S_nat=8, S=8, H=2, D=128, rot=128, inter=0,
+              freqs=at(3 * GB), m=1.0, tr=0, pos=at(4 * GB), ps=8, off=0, cp=2, layout=1, frm=0, to=1, dtype=1, stream=null)
+WRITE = dict(q=at(GB), qs=256, k=at(2 * GB), ks=128, v=at(3 * GB), vs=128, out=at(4 * GB), os=384, pos=at(5 * GB),
+             slots=at(6 * GB), N=4, rot=64, inter=0, freqs=at(7 * GB), m=1.0, kc=at(8 * GB), vc=at(9 * GB), **CACHE, H=4,
+             Hkv=2, D=64, dtype=1, stream=null)
+CACHE_BYTES = 8 * 16 * 2 * 64 * 2
+
+
+# out's rows are 512 bytes, 768 apart: 16 of them in the first, 4 in the second call.
+@pytest.mark.parametrize("changes", [
+    dict(pos=at(2 * GB)), dict(pos=at(2 * GB - 60)), dict(pos=at(2 * GB + 15 * 768 + 508)), dict(pos=at(2 * GB + 516), ps=100),
+    dict(freqs=at(2 * GB + 768)), dict(freqs=at(2 * GB - 504)), dict(freqs=at(2 * GB + 700))])
+def test_rotary_refuses_overlaps(changes):
+    assert call("cpattn_rotary", ROTARY, **changes) == E
+
+
+@pytest.mark.parametrize("changes", [
+    dict(pos=at(4 * GB + 768)), dict(slots=at(4 * GB - 24)), dict(slots=at(4 * GB + 508 - 508 % 8)), dict(freqs=at(4 * GB)),
+    dict(pos=at(8 * GB)), dict(pos=at(9 * GB + CACHE_BYTES - 4)), dict(slots=at(8 * GB - 8)), dict(freqs=at(9 * GB + 64)),
+    dict(q=at(8 * GB)), dict(q=at(8 * GB - 16)), dict(k=at(9 * GB + CACHE_BYTES - 16)), dict(v=at(8 * GB + 4096)),
+    dict(k=at(8 * GB)), dict(vc=at(8 * GB)), dict(vc=at(8 * GB + CACHE_BYTES // 8)), dict(vc=at(8 * GB - 128))])
+def test_rotary_cache_write_refuses_overlaps(changes):
+    assert call("cpattn_rotary_cache_write", WRITE, **changes) == E
