@@ -370,7 +370,8 @@ int cpattn_cache_evict(float* weights, const float* scores, void* k_cache, void*
   const size_t need = cpattn_cache_evict_workspace_bytes(R, Hkv, table_width, page_size, most);
   const Bytes rows = 4 * (Bytes)R, wc = R > 0 ? cache_bytes(c, Hkv, D) : 0,
               ww = R > 0 ? 4 * (Bytes)num_pages * Hkv * page_size : 0;
-  // (Keys and values may lie side by side in one tensor.)
+  // Keys and values may lie side by side in one tensor, but share nothing: the shift moves both.
+  if (R > 0 && caches_meet(k_cache, v_cache, c, Hkv, D)) return CPATTN_ERR_INVALID_ARG;
   const Stretch caches[] = {{k_cache, wc}, {v_cache, wc}};
   const Stretch written[] = {{weights, ww},
                              {new_lens, rows},

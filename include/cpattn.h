@@ -804,7 +804,7 @@ CPATTN_API int cpattn_cache_weights(const void* q, int64_t q_stride, const void*
  *   first, recent >= 0; most 1 to 2^26; R and Hkv at most 65535, R * Hkv at
  *   most 2^24, R * Hkv * most below 2^40; the cache as above, dtype CPATTN_BF16
  *   or CPATTN_F16.  What is written, the workspace too, overlaps nothing else
- *   (the keys and values may lie in one tensor).
+ *   (the keys and values may lie in one tensor, but share no element).
  * workspace: device, at least cpattn_cache_evict_workspace_bytes, 256-byte
  * aligned, scratch.
  */

@@ -60,3 +60,27 @@ def test_rotary_refuses_overlaps(changes):
     dict(k=at(8 * GB)), dict(vc=at(8 * GB)), dict(vc=at(8 * GB + CACHE_BYTES // 8)), dict(vc=at(8 * GB - 128))])
 def test_rotary_cache_write_refuses_overlaps(changes):
     assert call("cpattn_rotary_cache_write", WRITE, **changes) == E
+
+
+EVICT = dict(w=at(GB), sc=null, kc=at(8 * GB), vc=at(9 * GB), **CACHE, table=at(2 * GB), width=4, stride=4, ctx=at(3 * GB),
+             keep=at(3 * GB + 64), first=0, recent=0, most=10, new=at(4 * GB), kept=at(5 * GB), freed=at(6 * GB), room=8,
+             count=at(7 * GB), R=2, Hkv=2, D=64, dtype=1, ws=null, wb=0, stream=null)
+TOKEN, PAGE = 2 * 64, 16 * 2 * 64  # values
+
+
+@pytest.mark.parametrize("strides,apart", [
+    (dict(), 0), (dict(), 8), (dict(), PAGE - 8), (dict(), -PAGE), (dict(), 8 * PAGE - 8), (dict(), 56),
+    (dict(ps=2 * PAGE), PAGE - 64), (dict(ps=2 * PAGE), 3 * PAGE + 8), (dict(ps=PAGE, hs=16 * 64, ts=64), 64),
+    (dict(ps=2 * PAGE, ts=2 * TOKEN), TOKEN - 32), (dict(pages=1, ps=64), 3 * TOKEN), (dict(pages=1, ps=64, hs=16 * 64, ts=64), 64)])
+def test_keys_and_values_that_share_elements(strides, apart):
+    assert call("cpattn_cache_evict", EVICT, **strides, vc=at(8 * GB + 2 * apart)) == E
+
+
+@pytest.mark.parametrize("strides,apart", [
+    (dict(), 8 * PAGE), (dict(), -8 * PAGE), (dict(ps=2 * PAGE), PAGE), (dict(ps=2 * PAGE), -PAGE), (dict(ps=2 * PAGE), 5 * PAGE),
+    (dict(ps=2 * PAGE, hs=16 * 64, ts=64), PAGE), (dict(ps=2 * PAGE, ts=2 * TOKEN), TOKEN),
+    (dict(ps=2 * PAGE, ts=2 * TOKEN, hs=2 * 64), 64), (dict(ps=2 * PAGE, hs=2 * 16 * 64, ts=64), 16 * 64),
+    (dict(hs=8 * PAGE, ps=16 * 64, ts=64), 8 * 16 * 64), (dict(pages=1, ps=64), 16 * TOKEN),
+    (dict(ps=6 * PAGE), 5 * PAGE)])
+def test_keys_and_values_side_by_side(strides, apart):
+    assert call("cpattn_cache_evict", EVICT, **strides, vc=at(8 * GB + 2 * apart)) == _binding.ERR_WORKSPACE
