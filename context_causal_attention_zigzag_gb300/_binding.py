@@ -6,6 +6,7 @@ memory plumbing) and passes raw pointers plus the current CUDA stream.  If
 the library has not been built, every call raises: there is no fallback.
 """
 import ctypes
+import operator
 import os
 
 import torch
@@ -779,6 +780,14 @@ def _cache_args(k_cache, v_cache, Hkv, D, dtype, device):
     return shape[0], shape[1], strides[0], strides[1], strides[2]
 
 
+def _whole(x, name, bits=32):
+    """A caller's integer, of any kind, that fits the library's."""
+    x = operator.index(x)
+    if not -1 << bits - 1 <= x < 1 << bits - 1:
+        raise ValueError(f"{name} must fit {bits} bits")
+    return x
+
+
 _short_calls = {}
 
 
@@ -786,7 +795,8 @@ def _short_call(name):
     """The entry point with every integer taken as c_void_p: ctypes hands a Python int
     on as it is then (27 arguments take 2.3 us; as c_int and c_int64 6.1 us).  Both
     calling conventions give an int the slot or register of a pointer, of which it is the
-    low half."""
+    low half.  (c_void_p takes None and strings, too, and no other kind of integer: what a
+    caller gives goes through _whole.)"""
     res, args = SIGNATURES[name]
     fn = lib()[name]  # a function object of its own
     fn.restype, fn.argtypes = res, [t if t in (_f, _d) else _vp for t in args]
@@ -988,7 +998,8 @@ def _rotary(transposed, x, freqs, positions, interleaved, magnitude, offset, cp,
         raise TypeError(f"unsupported dtype {x.dtype}: float32, bfloat16 or float16")
     B, S_in, H, D, xs = _token_rows(x, "x")
     rot = _turned_values(freqs, dev)
-    S_out = S_in if length is None else int(length)
+    S_out = S_in if length is None else _whole(int(length), "length")
+    cp, layout, offset = _whole(cp, "cp"), _whole(layout, "layout"), _whole(offset, "offset", 64)
     if from_sharded == to_sharded and not from_sharded and S_out != S_in:
         raise ValueError("a sequence changes its length only on its way into or out of the ring")
     if from_sharded and to_sharded and S_out != S_in:
@@ -1137,7 +1148,8 @@ def cache_evict(weights, k_cache, v_cache, block_table, ctx_lens, keep, most, fi
         raise ValueError("k_cache and v_cache must be [pages, page_size, Hkv, D] of one shape")
     Hkv, D = k_cache.shape[2:]
     cache = _cache_args(k_cache, v_cache, Hkv, D, k_cache.dtype, dev)
-    R, most = ctx_lens.numel(), int(most)
+    R, most = ctx_lens.numel(), _whole(int(most), "most")
+    first, recent = (max(-1, min(operator.index(n), 2**31 - 1)) for n in (first, recent))
     _on(dev, "ctx_lens", ctx_lens, torch.int32)
     _on(dev, "keep", keep, torch.int32, R)
     width, stride = _table_args(block_table, R, dev)
@@ -1156,7 +1168,7 @@ def cache_evict(weights, k_cache, v_cache, block_table, ctx_lens, keep, most, fi
     _launch("cpattn_cache_evict", dev, weights.data_ptr(),
             None if scores is None else scores.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             *cache, block_table.data_ptr(), width, stride, ctx_lens.data_ptr(), keep.data_ptr(),
-            min(first, 2**31 - 1), min(recent, 2**31 - 1), most, new_lens.data_ptr(), kept.data_ptr(), freed.data_ptr(),
+            first, recent, most, new_lens.data_ptr(), kept.data_ptr(), freed.data_ptr(),
             freed.numel(), count.data_ptr(), R, Hkv, D, code, ws.data_ptr(), ws.numel())
     return outputs
 
