@@ -1000,9 +1000,7 @@ def _rotary(transposed, x, freqs, positions, interleaved, magnitude, offset, cp,
     rot = _turned_values(freqs, dev)
     S_out = S_in if length is None else _whole(int(length), "length")
     cp, layout, offset = _whole(cp, "cp"), _whole(layout, "layout"), _whole(offset, "offset", 64)
-    if from_sharded == to_sharded and not from_sharded and S_out != S_in:
-        raise ValueError("a sequence changes its length only on its way into or out of the ring")
-    if from_sharded and to_sharded and S_out != S_in:
+    if bool(from_sharded) == bool(to_sharded) and S_out != S_in:
         raise ValueError("a sequence changes its length only on its way into or out of the ring")
     # The natural side holds the real tokens.
     S_nat, S = (S_out, S_in) if from_sharded else (S_in, S_out)
@@ -1017,7 +1015,7 @@ def _rotary(transposed, x, freqs, positions, interleaved, magnitude, offset, cp,
     if positions is not None:
         if positions.shape == (B, S_nat) and B > 1:
             ps = S_nat
-        elif positions.numel() != S_nat or positions.dim() not in (1, 2):
+        elif positions.shape not in ((S_nat,), (1, S_nat)):
             raise ValueError(f"positions must be [{S_nat}] or [{B}, {S_nat}] (natural order)")
         _on(dev, "positions", positions, torch.int32)
         at = positions.data_ptr()

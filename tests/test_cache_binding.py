@@ -77,3 +77,16 @@ def test_integers_that_do_not_fit_are_refused(launched):
     evict(first=1 << 40, recent=1 << 31)
     evict(first=-(1 << 32), recent=-(1 << 40))
     assert [named(c)[n] for c in launched for n in ("first", "recent")] == [2**31 - 1] * 2 + [-1] * 2
+
+
+@pytest.mark.parametrize("shape,stride", [((8,), 0), ((1, 8), 0), ((2, 8), 8)])
+def test_positions_of_one_row_or_of_each_sequence(launched, shape, stride):
+    turn(positions=torch.zeros(shape, dtype=torch.int32))
+    assert named(launched[0])["positions_stride"] == stride
+
+
+@pytest.mark.parametrize("shape", [(8, 1), (4, 2), (2, 4), (16,), (1, 16), (8, 2), (1, 1, 8), (2, 1, 8), (), (3, 8), (7,)])
+def test_positions_of_another_shape_are_refused(launched, shape):
+    with pytest.raises(ValueError):
+        turn(positions=torch.zeros(shape, dtype=torch.int32))
+    assert not launched
