@@ -7,9 +7,9 @@
 //
 // The angle p f of a far position has lost its fraction in float32 (p = 10^6: off
 // by 0.03).  Here a frequency is held as the fraction of a turn a position, in
-// units of 2^-64 of a turn; its product with the position, modulo 2^64, is the
-// angle without the whole turns, exact but for the frequency's own rounding
-// (2^-53), at the price of three 32-bit products.  It is split at the nearest
+// units of 2^-64 of a turn, to the nearest; its product with the position, modulo
+// 2^64, is the angle without the whole turns, off by half a unit a position (2^-22
+// at 2^40), at the price of three 32-bit products.  It is split at the nearest
 // quarter turn, so that sine and cosine are taken of at most an eighth of one.
 // For float32 they come from sincospif; for 16-bit outputs from __sinf and
 // __cosf, whose 2^-21 is far below half a step of the output (2^-12).
@@ -109,10 +109,17 @@ struct Values {
   }
 };
 
-// Fraction of a turn a position, in units of 2^-64.
+// Fraction of a turn a position, in units of 2^-64, to the nearest: 1 / 2 pi and its product
+// with f as sums of two (a product rounded to 53 bits is off by up to 2^-53 of the angle: 2^-22
+// at position 2^31, 2^-13 at 2^40).
 __device__ __forceinline__ unsigned long long turns(double f) {
-  const double t = f * 0.15915494309189535;  // 1 / 2 pi
-  return __double2ull_rn((t - floor(t)) * 18446744073709551616.0);
+  const double inv = 0.15915494309189535, inv_rest = -9.839338337591243e-18;
+  const double t = __dmul_rn(f, inv), rest = __fma_rn(f, inv, -t) + f * inv_rest;
+  double part = t - rint(t);  // exact
+  if (part >= 0.5) part -= 1.0;
+  const double units = part * 18446744073709551616.0, whole = rint(units);
+  return (unsigned long long)(__double2ll_rn(whole) +
+                              __double2ll_rn((units - whole) + rest * 18446744073709551616.0));
 }
 
 // Sine and cosine of `phase` units of 2^-64 turns.

@@ -675,8 +675,8 @@ CPATTN_API int cpattn_prompt_attn(const void* q, int64_t q_stride, const void* k
  * becomes
  *   (m (a cos pf - b sin pf), m (a sin pf + b cos pf)),  m = magnitude,
  * and with transposed = 1 (the gradient of that) the same with -sin.  Angles
- * are reduced in 64-bit fixed point, so that far positions lose nothing;
- * products and sums are float32, rounded once.
+ * are reduced in 64-bit fixed point, off by |p| 2^-62 at most, so that positions
+ * lose nothing up to some 2^40; products and sums are float32, rounded once.
  *
  * cpattn_rotary_frequencies (host only) fills freqs [rot / 2] and *magnitude:
  *   CPATTN_ROTARY_PLAIN   f_i = base^(-2 i / rot)
