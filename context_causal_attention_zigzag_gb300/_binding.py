@@ -780,12 +780,9 @@ def _cache_args(k_cache, v_cache, Hkv, D, dtype, device):
     return shape[0], shape[1], strides[0], strides[1], strides[2]
 
 
-def _whole(x, name, bits=32):
-    """A caller's integer, of any kind, that fits the library's."""
-    x = operator.index(x)
-    if not -1 << bits - 1 <= x < 1 << bits - 1:
-        raise ValueError(f"{name} must fit {bits} bits")
-    return x
+_index = operator.index  # a caller's integer, of any kind
+_INT = 2**31 - 1
+_INT64 = 2**63 - 1
 
 
 _short_calls = {}
@@ -795,8 +792,8 @@ def _short_call(name):
     """The entry point with every integer taken as c_void_p: ctypes hands a Python int
     on as it is then (27 arguments take 2.3 us; as c_int and c_int64 6.1 us).  Both
     calling conventions give an int the slot or register of a pointer, of which it is the
-    low half.  (c_void_p takes None and strings, too, and no other kind of integer: what a
-    caller gives goes through _whole.)"""
+    low half.  (c_void_p takes None and strings, too, no other kind of integer, and more than
+    fits: what a caller gives goes through _index and a comparison.)"""
     res, args = SIGNATURES[name]
     fn = lib()[name]  # a function object of its own
     fn.restype, fn.argtypes = res, [t if t in (_f, _d) else _vp for t in args]
@@ -998,8 +995,11 @@ def _rotary(transposed, x, freqs, positions, interleaved, magnitude, offset, cp,
         raise TypeError(f"unsupported dtype {x.dtype}: float32, bfloat16 or float16")
     B, S_in, H, D, xs = _token_rows(x, "x")
     rot = _turned_values(freqs, dev)
-    S_out = S_in if length is None else _whole(int(length), "length")
-    cp, layout, offset = _whole(cp, "cp"), _whole(layout, "layout"), _whole(offset, "offset", 64)
+    S_out = S_in if length is None else int(length)
+    cp, layout, offset = _index(cp), _index(layout), _index(offset)
+    if not (-_INT <= cp <= _INT and -_INT <= layout <= _INT and -_INT64 <= offset <= _INT64
+            and S_in <= _INT and S_out <= _INT and B <= _INT and H <= _INT):
+        raise ValueError("x's dimensions, length, cp and layout must fit 32 bits, offset 64")
     if bool(from_sharded) == bool(to_sharded) and S_out != S_in:
         raise ValueError("a sequence changes its length only on its way into or out of the ring")
     # The natural side holds the real tokens.
@@ -1013,9 +1013,10 @@ def _rotary(transposed, x, freqs, positions, interleaved, magnitude, offset, cp,
     os_ = _token_rows(out, "out")[4]
     at, ps = None, 0
     if positions is not None:
-        if positions.shape == (B, S_nat) and B > 1:
-            ps = S_nat
-        elif positions.shape not in ((S_nat,), (1, S_nat)):
+        shape = positions.shape
+        if shape == (B, S_nat):
+            ps = S_nat if B > 1 else 0
+        elif shape != (S_nat,) and shape != (1, S_nat):
             raise ValueError(f"positions must be [{S_nat}] or [{B}, {S_nat}] (natural order)")
         _on(dev, "positions", positions, torch.int32)
         at = positions.data_ptr()
@@ -1146,8 +1147,11 @@ def cache_evict(weights, k_cache, v_cache, block_table, ctx_lens, keep, most, fi
         raise ValueError("k_cache and v_cache must be [pages, page_size, Hkv, D] of one shape")
     Hkv, D = k_cache.shape[2:]
     cache = _cache_args(k_cache, v_cache, Hkv, D, k_cache.dtype, dev)
-    R, most = ctx_lens.numel(), _whole(int(most), "most")
-    first, recent = (max(-1, min(operator.index(n), 2**31 - 1)) for n in (first, recent))
+    R, most, first, recent = ctx_lens.numel(), int(most), _index(first), _index(recent)
+    if most > _INT:
+        raise ValueError("most must fit 32 bits")
+    first = _INT if first > _INT else -1 if first < 0 else first
+    recent = _INT if recent > _INT else -1 if recent < 0 else recent
     _on(dev, "ctx_lens", ctx_lens, torch.int32)
     _on(dev, "keep", keep, torch.int32, R)
     width, stride = _table_args(block_table, R, dev)
