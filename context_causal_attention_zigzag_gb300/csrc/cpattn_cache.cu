@@ -79,19 +79,19 @@ bool row_meets(const void* p, Bytes stride, Bytes rows, Bytes width, const Stret
 // more than a step of those before it, so that of each only the steps around what is left matter.
 bool caches_meet(const void* k, const void* v, const CacheShape& c, int Hkv, int D) {
   struct Axis {
-    Bytes stride, n;
-  } axes[3] = {{2 * (Bytes)c.page_stride, c.num_pages},
-               {2 * (Bytes)c.token_stride, c.page_size},
-               {2 * (Bytes)c.head_stride, Hkv}};
+    int64_t stride, n;
+  } axes[3] = {{2 * c.page_stride, c.num_pages}, {2 * c.token_stride, c.page_size}, {2 * c.head_stride, Hkv}};
   std::sort(axes, axes + 3, [](const Axis& x, const Axis& y) { return x.stride > y.stride; });
-  Bytes left[8] = {(Bytes)reinterpret_cast<intptr_t>(v) - reinterpret_cast<intptr_t>(k)};
+  int64_t left[8] = {reinterpret_cast<intptr_t>(v) - reinterpret_cast<intptr_t>(k)};
+  const Bytes all = cache_bytes(c, Hkv, D);
+  if (left[0] >= all || -left[0] >= all) return false;
   int ways = 1;
   for (const Axis& x : axes) {
     if (x.n == 1) continue;  // its stride says nothing
     int next = 0;
-    Bytes then[8];
+    int64_t then[8];
     for (int i = 0; i < ways; ++i) {
-      Bytes m = left[i] / x.stride;
+      int64_t m = left[i] / x.stride;
       if (m * x.stride > left[i]) --m;
       for (int j = 0; j < 2; ++j, ++m)
         if (m < x.n && -m < x.n) then[next++] = left[i] - m * x.stride;
