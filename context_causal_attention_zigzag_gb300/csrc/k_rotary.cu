@@ -12,7 +12,8 @@
 // at 2^40), at the price of three 32-bit products.  It is split at the nearest
 // quarter turn, so that sine and cosine are taken of at most an eighth of one.
 // For float32 they come from sincospif; for 16-bit outputs from __sinf and
-// __cosf, whose 2^-21 is far below half a step of the output (2^-12).
+// __cosf, whose 2^-21 (absolute) moves a value by 2^-21 (|a| + |b|) at most: far below
+// half a step (2^-12) of a value as large as its pair, not of one that nearly cancels.
 //
 // Both calls are bound by HBM: each value is read and written once, in 16-byte
 // vectors where rot allows it.  A thread holds the same vectors of each head (both

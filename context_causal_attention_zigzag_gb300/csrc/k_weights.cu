@@ -6,8 +6,9 @@
 //
 // On CUDA cores, for calls of few rows and keys (the rest: k_weights_tc.cu): a thread holds a
 // key's row and walks the rows of q, which lie in shared memory as float32 a few at a time;
-// the block's keys share them.  Bound by that chain: 6 us for one token of 32 + 8 heads over
-// 1000 positions, where the tensor cores' kernel needs 8 for its start.
+// the block's keys share them.  Bound by that chain: 6 us on the device (of many calls in a
+// graph) for one token of 32 + 8 heads over 1000 positions, where the tensor cores' kernel needs
+// 8 for its start.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -28,10 +28,10 @@
 // 8 or 12 warps are the warpgroups, a key a thread.  TMEM: two places of 128 columns for
 // each key tile's products.
 //
-// Measured (H = 32, Hkv = 8, D = 128): 64 single tokens over 100-8192 positions 93 us (5.1
+// Measured (H = 32, Hkv = 8, D = 128): 64 single tokens over 100-8192 positions 94 us (5.1
 // TB/s, HBM at 75 %: an item takes a CTA about as long to walk, issue and add up as to load);
 // 16 prompts of 100-2000, D = 64, float16 112 us (the warpgroups' way through the rows:
-// exponentials 42 % of the time, issue slots 51 %); one of 16384 855-907 us (1.2-1.3 PFLOP/s; 1965 cycles a
+// exponentials 42 % of the time, issue slots 51 %); one of 16384 855-915 us (1.2-1.3 PFLOP/s; 1965 cycles a
 // step of two products of 128 x 128 x 128, which as instructions of their own take 1712).
 // Two key tiles an item, so that a tile of rows is loaded for 256 keys.  Not faster: four
 // warpgroups (924-978 us), products' rows read 64 columns at a time or a read ahead (spills).

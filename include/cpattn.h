@@ -796,7 +796,8 @@ CPATTN_API int cpattn_cache_weights(const void* q, int64_t q_stride, const void*
  *   most for the others.
  *   freed [num_freed_max] int32: the pages that requests no longer need, in request
  *   order, then -1; num_freed [1] int32: how many.  The tables stay as they are
- *   (entries behind a request's last page are not read).
+ *   (entries behind a request's last page are not read; how the work is laid out
+ *   follows from their width, so one no wider than the requests need is faster).
  * Broken lengths, tables, a negative keep, one above `most`, or too little room
  * in freed raise the device error word; such a request is left as it is
  * (new_lens = c), and pages that freed has no room for are not listed.  No page belongs to
