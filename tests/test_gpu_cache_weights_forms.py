@@ -290,3 +290,22 @@ def test_more_rows_than_stream_past():
     pos, x = torch.arange(P, device=DEV), ctx.flip(0)[:, None]
     want = torch.where(pos < x, 1.5 + H, torch.where(pos == x, float(H), 3.0))
     assert torch.equal(weights[:, 0], want)
+
+
+def test_most_rows_of_one_request_where_keys_stream():
+    """2^17 requests, all tokens one's: tiles of one token, 2^17 steps of 1.7 us to an item at most (0.2 s of the
+    2 after which waits give up).  Each row gives 1, and sums up to 2^24 are exact."""
+    R, H, D, P = 1 << 17, 128, 64, 1024
+    N, at = R, 70001
+    q = torch.zeros(N, H, D, device=DEV, dtype=torch.bfloat16)
+    k = torch.ones(N // P, P, 1, D, device=DEV, dtype=torch.bfloat16)
+    table = torch.full((R, N // P), -1, device=DEV, dtype=torch.int32)
+    table[at] = torch.arange(N // P, device=DEV, dtype=torch.int32).flip(0)
+    cu = torch.zeros(R + 1, device=DEV, dtype=torch.int32)
+    cu[at + 1:] = N
+    weights = torch.full((N // P, 1, P), 3.0, device=DEV)
+    cpa.cache_weights(q, k, table, torch.zeros(R, device=DEV, dtype=torch.int32), cu, torch.zeros(H, N, device=DEV),
+                      weights)
+    assert cpa.device_status() == 0
+    want = (N - torch.arange(N, device=DEV)).float() * H
+    assert torch.equal(weights.flip(0).reshape(-1), want)
